@@ -31,6 +31,9 @@ SGEMM_ERR_WORKSPACE = -102
 SGEMM_ERR_NO_SLOT = -103
 SGEMM_ERR_CAPTURING = -104
 
+SGEMM_TYPE_F32 = 0
+SGEMM_TYPE_BF16 = 1
+
 SCONV_VARIANT_AUTO = 0
 SCONV_VARIANT_STEM = 1
 SCONV_VARIANT_GENERAL = 2
@@ -42,7 +45,10 @@ EXPORTS = ("sgemm_f32", "sgemm_f32_variant", "sgemm_plan", "sgemm_tune", "sgemm_
            "sgemm_num_mfma_tiles", "sgemm_status_string",
            # include/sconv.h
            "sconv2d_f32", "sconv2d_f32_variant", "sgemm_im2col_f32", "sconv2d_plan",
-           "sconv2d_num_stem_kernels")
+           "sconv2d_num_stem_kernels",
+           # include/slm.h
+           "sgemm_grouped", "sgemm_grouped_wgrad", "sgemm_xent", "sgemm_xent_backward",
+           "sgemm_xent_workspace", "sgemm_q4_matvec", "sgemm_q4_quantize")
 
 if not os.path.exists(LIBRARY):
     raise ImportError("libsgemm.so is not built; run __graft_entry__.build() "
@@ -91,11 +97,32 @@ _lib.sconv2d_plan.restype = ctypes.c_int
 _lib.sconv2d_plan.argtypes = [ctypes.c_int] * 13 + [ctypes.c_char_p, ctypes.c_int]
 _lib.sconv2d_num_stem_kernels.restype = ctypes.c_int
 _lib.sconv2d_num_stem_kernels.argtypes = []
+_i, _i64, _f, _p = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
+for _name, _args in {
+        "sgemm_grouped": [_i] * 6 + [_f, _p, _i, _p, _i, _i64, _f, _p, _i, _p, _p],
+        "sgemm_grouped_wgrad": [_i] * 5 + [_f, _p, _i, _p, _i, _f, _p, _i, _i64, _p, _p],
+        "sgemm_xent": [_i] * 4 + [_p, _i, _p, _i, _p, _p, _p, _p, _i64, _p],
+        "sgemm_xent_backward": [_i] * 4 + [_p, _i, _p, _i] + [_p] * 4 + [_i, _p, _i, _p, _i64, _p],
+        "sgemm_q4_matvec": [_i] * 6 + [_p, _i, _p, _p, _p, _p, _i, _p, _p],
+        "sgemm_q4_quantize": [_i] * 4 + [_p, _i, _p, _p, _p, _p],
+}.items():
+    getattr(_lib, _name).restype = ctypes.c_int
+    getattr(_lib, _name).argtypes = _args
+_lib.sgemm_xent_workspace.restype = ctypes.c_int64
+_lib.sgemm_xent_workspace.argtypes = [ctypes.c_int] * 5
 
 
 class SgemmError(RuntimeError):
-    def __init__(self, status: int):
-        super().__init__("sgemm failed with status %d: %s" % (status, sgemm_status_string(status)))
+    """A non-zero status; ``call`` names the entry point whose header says what
+    -p means where it is not sgemm_f32's list."""
+
+    def __init__(self, status: int, call: str = ""):
+        if call and -100 < status < 0:
+            text = "%s failed with status %d: invalid parameter %d" % (call, status, -status)
+        else:
+            text = "%s failed with status %d: %s" % (call or "sgemm", status,
+                                                      sgemm_status_string(status))
+        super().__init__(text)
         self.status = status
 
 
@@ -281,3 +308,317 @@ def im2col(X, kernel, stride=1, pad=0, B=None, stream=None):
     if rc != 0:
         raise SgemmError(rc)
     return B
+
+
+# ---------------------------------------------- language-model products
+
+def sgemm_grouped(type, trans, groups, rows, N, K, alpha, X, ldx, W, ldw, stride_w, beta, Y, ldy,
+                  offsets, stream=0) -> int:
+    """C ABI ``sgemm_grouped``; pointers and stream are integers.  Returns the status."""
+    return _lib.sgemm_grouped(type, trans, groups, rows, N, K, alpha, X, ldx, W, ldw, stride_w,
+                              beta, Y, ldy, offsets, stream)
+
+
+def sgemm_grouped_wgrad(type, groups, rows, M, N, alpha, X, ldx, G, ldg, beta, D, ldd, stride_d,
+                        offsets, stream=0) -> int:
+    """C ABI ``sgemm_grouped_wgrad``.  Returns the status."""
+    return _lib.sgemm_grouped_wgrad(type, groups, rows, M, N, alpha, X, ldx, G, ldg, beta, D, ldd,
+                                    stride_d, offsets, stream)
+
+
+def sgemm_xent(type, rows, vocab, K, X, ldx, W, ldw, targets, loss, lse, ws, ws_bytes,
+               stream=0) -> int:
+    """C ABI ``sgemm_xent``.  Returns the status."""
+    return _lib.sgemm_xent(type, rows, vocab, K, X, ldx, W, ldw, targets, loss, lse, ws, ws_bytes,
+                           stream)
+
+
+def sgemm_xent_backward(type, rows, vocab, K, X, ldx, W, ldw, targets, lse, dloss, dX, lddx, dW,
+                        lddw, ws, ws_bytes, stream=0) -> int:
+    """C ABI ``sgemm_xent_backward``.  Returns the status."""
+    return _lib.sgemm_xent_backward(type, rows, vocab, K, X, ldx, W, ldw, targets, lse, dloss, dX,
+                                    lddx, dW, lddw, ws, ws_bytes, stream)
+
+
+def sgemm_xent_workspace(type, rows, vocab, K, backward) -> int:
+    """C ABI ``sgemm_xent_workspace``: bytes, or a negative status."""
+    return _lib.sgemm_xent_workspace(type, rows, vocab, K, backward)
+
+
+def sgemm_q4_matvec(type, groups, rows, N, K, block, X, ldx, Q, S, Z, Y, ldy, offsets,
+                    stream=0) -> int:
+    """C ABI ``sgemm_q4_matvec``.  Returns the status."""
+    return _lib.sgemm_q4_matvec(type, groups, rows, N, K, block, X, ldx, Q, S, Z, Y, ldy, offsets,
+                                stream)
+
+
+def sgemm_q4_quantize(type, N, K, block, W, ldw, Q, S, Z, stream=0) -> int:
+    """C ABI ``sgemm_q4_quantize``.  Returns the status."""
+    return _lib.sgemm_q4_quantize(type, N, K, block, W, ldw, Q, S, Z, stream)
+
+
+_TYPES = {torch.float32: SGEMM_TYPE_F32, torch.bfloat16: SGEMM_TYPE_BF16}
+
+
+def _operand(t, name, dtype, device, dim=2, rows=None, cols=None):
+    """Checks a tensor of rows with unit column stride; returns its leading dimension."""
+    if t.dtype != dtype or t.dim() != dim:
+        raise TypeError("%s must be a %d-D %s tensor, not %d-D %s"
+                        % (name, dim, dtype, t.dim(), t.dtype))
+    if t.device != device or device.type != "cuda":
+        raise ValueError("%s is on %s: every operand must be on one GPU" % (name, t.device))
+    r, c = t.shape[-2], t.shape[-1]
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError("%s is %s: %s x %s is wanted" % (name, tuple(t.shape), rows, cols))
+    if t.numel() == 0:
+        return max(1, c)
+    if c > 1 and t.stride(-1) != 1:
+        raise ValueError("%s must have unit column stride" % name)
+    if r > 1:
+        if t.stride(-2) < c:
+            raise ValueError("%s has overlapping rows" % name)
+        return t.stride(-2)
+    return max(1, c)
+
+
+def _groups_of(t):
+    """Elements from one group's matrix to the next."""
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _vector(t, name, dtype, device, n):
+    if t.dtype != dtype or tuple(t.shape) != (n,) or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be a packed %s vector of %d on %s" % (name, dtype, n, device))
+    return t.data_ptr()
+
+
+def _type_of(t, name):
+    if t.dtype not in _TYPES:
+        raise TypeError("%s must be float32 or bfloat16, not %s" % (name, t.dtype))
+    return _TYPES[t.dtype]
+
+
+def _run(call, device, stream, body):
+    """body(stream handle) with ``device`` current and, where a stream is given,
+    with it current too, so that what body allocates belongs to that stream."""
+    with torch.cuda.device(device):
+        if stream is None:
+            rc = body(torch.cuda.current_stream().cuda_stream)
+        else:
+            with torch.cuda.stream(stream):
+                rc = body(stream.cuda_stream)
+    if rc != 0:
+        raise SgemmError(rc, call)
+
+
+def grouped_gemm(X, W, offsets, Y=None, trans: bool = False, alpha: float = 1.0,
+                 beta: float = 0.0, stream=None):
+    """Y[r] <- alpha * X[r] @ W[e] + beta * Y[r] for the rows r of each group e,
+    offsets[e] <= r < offsets[e + 1] (``sgemm_grouped``).
+
+    X: (rows, K); W: (groups, K, N), or (groups, N, K) with ``trans``; offsets:
+    groups + 1 int32 on the device, increasing; Y: (rows, N), allocated as
+    zeros when None.  float32 or bfloat16, rows may be padded.  Rows outside
+    every group keep what Y holds.  The gradient of X is
+    ``grouped_gemm(dY, W, offsets, trans=not trans)``.  Returns Y.
+    """
+    t = _type_of(X, "X")
+    dev = X.device
+    ldx = _operand(X, "X", X.dtype, dev)
+    rows, K = X.shape
+    if W.dim() != 3:
+        raise TypeError("W must be 3-D")
+    groups, N = W.shape[0], W.shape[1 if trans else 2]
+    ldw = _operand(W, "W", X.dtype, dev, 3, *((N, K) if trans else (K, N)))
+    off = _vector(offsets, "offsets", torch.int32, dev, groups + 1)
+    ldy = _operand(Y, "Y", X.dtype, dev, 2, rows, N) if Y is not None else max(1, N)
+
+    def body(s):
+        nonlocal Y
+        if Y is None:
+            Y = torch.zeros((rows, N), dtype=X.dtype, device=dev)
+        return _lib.sgemm_grouped(t, int(trans), groups, rows, N, K, alpha, X.data_ptr(), ldx,
+                                  W.data_ptr(), ldw, _groups_of(W), beta, Y.data_ptr(), ldy, off, s)
+    _run("sgemm_grouped", dev, stream, body)
+    return Y
+
+
+def grouped_wgrad(X, G, offsets, D=None, alpha: float = 1.0, beta: float = 0.0, stream=None):
+    """D[e] <- alpha * X_e^T @ G_e + beta * D[e] over each group's rows
+    (``sgemm_grouped_wgrad``): the gradient of grouped weights.
+
+    X: (rows, M); G: (rows, N); offsets as in ``grouped_gemm``; D: (groups, M,
+    N), allocated as zeros when None.  For weights stored (K, N): X is the
+    product's input and G its output's gradient; for weights stored (N, K),
+    exchange the two.  Returns D.
+    """
+    t = _type_of(X, "X")
+    dev = X.device
+    ldx = _operand(X, "X", X.dtype, dev)
+    rows, M = X.shape
+    ldg = _operand(G, "G", X.dtype, dev, 2, rows)
+    N = G.shape[1]
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be a vector of groups + 1 row numbers")
+    groups = offsets.shape[0] - 1
+    off = _vector(offsets, "offsets", torch.int32, dev, groups + 1)
+    if D is not None and D.shape[0] != groups:
+        raise ValueError("D has %d groups, offsets %d" % (D.shape[0], groups))
+    ldd = _operand(D, "D", X.dtype, dev, 3, M, N) if D is not None else max(1, N)
+
+    def body(s):
+        nonlocal D
+        if D is None:
+            D = torch.empty((groups, M, N), dtype=X.dtype, device=dev)
+            if beta != 0.0:
+                D.zero_()
+        return _lib.sgemm_grouped_wgrad(t, groups, rows, M, N, alpha, X.data_ptr(), ldx,
+                                        G.data_ptr(), ldg, beta, D.data_ptr(), ldd, _groups_of(D),
+                                        off, s)
+    _run("sgemm_grouped_wgrad", dev, stream, body)
+    return D
+
+
+def _xent_operands(X, W, targets):
+    t = _type_of(X, "X")
+    dev = X.device
+    ldx = _operand(X, "X", X.dtype, dev)
+    rows, K = X.shape
+    ldw = _operand(W, "W", X.dtype, dev, 2, None, K)
+    vocab = W.shape[0]
+    if vocab == 0 and rows > 0:
+        raise ValueError("W holds no vocabulary")
+    return t, dev, ldx, ldw, rows, K, vocab, _vector(targets, "targets", torch.int64, dev, rows)
+
+
+def linear_cross_entropy(X, W, targets, stream=None):
+    """(loss, lse) of each row of X: the softmax cross entropy of the logits
+    X @ W.T at ``targets``, and the logits' log-sum-exp (``sgemm_xent``).  The
+    logits are not kept.
+
+    X: (rows, K); W: (vocab, K), float32 or bfloat16; targets: int64, one per
+    row; a target outside [0, vocab) marks a row that does not count (loss 0).
+    loss and lse are float32.
+    """
+    t, dev, ldx, ldw, rows, K, vocab, tg = _xent_operands(X, W, targets)
+    loss = lse = None
+
+    def body(s):
+        nonlocal loss, lse
+        loss, lse = torch.empty((2, rows), dtype=torch.float32, device=dev)
+        n = _lib.sgemm_xent_workspace(t, rows, vocab, K, 0)
+        ws = torch.empty((n,), dtype=torch.uint8, device=dev)
+        return _lib.sgemm_xent(t, rows, vocab, K, X.data_ptr(), ldx, W.data_ptr(), ldw, tg,
+                               loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), n, s)
+    _run("sgemm_xent", dev, stream, body)
+    return loss, lse
+
+
+def linear_cross_entropy_backward(dloss, X, W, targets, lse, dX=None, dW=None, need_dX: bool = True,
+                                  need_dW: bool = True, stream=None):
+    """(dX, dW): gradients of sum(dloss * loss) of ``linear_cross_entropy`` by X
+    and W (``sgemm_xent_backward``).  dloss: float32, one per row; lse as the
+    forward pass gave it; dX and dW are allocated when None; one that is not
+    needed is not computed and comes back as None.
+    """
+    t, dev, ldx, ldw, rows, K, vocab, tg = _xent_operands(X, W, targets)
+    pl = _vector(lse, "lse", torch.float32, dev, rows)
+    pd = _vector(dloss, "dloss", torch.float32, dev, rows)
+    lddx = _operand(dX, "dX", X.dtype, dev, 2, rows, K) if dX is not None else max(1, K)
+    lddw = _operand(dW, "dW", X.dtype, dev, 2, vocab, K) if dW is not None else max(1, K)
+    dX, dW = dX if need_dX else None, dW if need_dW else None
+
+    def body(s):
+        nonlocal dX, dW
+        if need_dX and dX is None:
+            dX = torch.empty((rows, K), dtype=X.dtype, device=dev)
+        if need_dW and dW is None:
+            dW = torch.empty((vocab, K), dtype=X.dtype, device=dev)
+        n = _lib.sgemm_xent_workspace(t, rows, vocab, K, 1)
+        ws = torch.empty((n,), dtype=torch.uint8, device=dev)
+        return _lib.sgemm_xent_backward(t, rows, vocab, K, X.data_ptr(), ldx, W.data_ptr(), ldw, tg,
+                                        pl, pd, dX.data_ptr() if need_dX else 0, lddx,
+                                        dW.data_ptr() if need_dW else 0, lddw, ws.data_ptr(), n, s)
+    _run("sgemm_xent_backward", dev, stream, body)
+    return dX, dW
+
+
+Q4_BLOCKS = (32, 64, 128)
+
+
+def _packed(t, name, dtype, device, shape):
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s must be a packed %s tensor of %s on %s" % (name, dtype, shape, device))
+    return t.data_ptr()
+
+
+def q4_quantize(W, block: int = 128, zeros: bool = True, stream=None):
+    """(Q, scales, zeros): W in 4 bits with a scale, and with ``zeros`` a zero, for
+    each ``block`` (32, 64 or 128) of weights along K (``sgemm_q4_quantize``).
+
+    W: (N, K) or (groups, N, K), packed groups, float32 or bfloat16, K even.  Q: uint8 of (..., N,
+    K/2), two weights a byte, the even one in the low half; scales: W's type,
+    (..., N, ceil(K/block)); zeros: uint8 likewise, or None.
+    """
+    t = _type_of(W, "W")
+    dev, lead, (N, K) = W.device, tuple(W.shape[:-2]), W.shape[-2:]
+    ldw = _operand(W, "W", W.dtype, dev, W.dim())
+    if W.dim() not in (2, 3):
+        raise TypeError("W must be 2-D or 3-D")
+    if block not in Q4_BLOCKS:
+        raise ValueError("block must be one of %s" % (Q4_BLOCKS,))
+    if K % 2:
+        raise ValueError("K must be even")
+    if W.dim() == 3 and W.shape[0] > 1 and W.numel() and W.stride(0) != N * ldw:
+        raise ValueError("W's groups must follow one another")
+    blocks = -(-K // block)
+    rows = N * (lead[0] if lead else 1)
+    Q = S = Z = None
+
+    def body(s):
+        nonlocal Q, S, Z
+        Q = torch.empty(lead + (N, K // 2), dtype=torch.uint8, device=dev)
+        S = torch.empty(lead + (N, blocks), dtype=W.dtype, device=dev)
+        Z = torch.empty(lead + (N, blocks), dtype=torch.uint8, device=dev) if zeros else None
+        return _lib.sgemm_q4_quantize(t, rows, K, block, W.data_ptr(), ldw, Q.data_ptr(),
+                                      S.data_ptr(), Z.data_ptr() if zeros else 0, s)
+    _run("sgemm_q4_quantize", dev, stream, body)
+    return Q, S, Z
+
+
+def q4_matvec(X, Q, scales, zeros=None, block: int = 128, Y=None, offsets=None, stream=None):
+    """Y[r] <- X[r] @ w.T with weights held in 4 bits, w[n, k] = (q[n, k] - zero) *
+    scale of the row's block (``sgemm_q4_matvec``), for a few rows.
+
+    X: (rows, K), float32 or bfloat16; Q, scales, zeros as ``q4_quantize`` gives
+    them (zeros None: 8); Y: (rows, N), allocated when None.  With ``offsets``
+    (groups + 1 int32), Q, scales and zeros hold one set of weights per group, and
+    row r uses its group's; rows outside every group keep what Y holds.
+    """
+    t = _type_of(X, "X")
+    dev = X.device
+    ldx = _operand(X, "X", X.dtype, dev)
+    rows, K = X.shape
+    if block not in Q4_BLOCKS:
+        raise ValueError("block must be one of %s" % (Q4_BLOCKS,))
+    if K % 2:
+        raise ValueError("K must be even")
+    if Q.dim() != (2 if offsets is None else 3):
+        raise ValueError("Q must be (N, K/2), or (groups, N, K/2) with offsets")
+    lead, N = tuple(Q.shape[:-2]), Q.shape[-2]
+    groups, blocks = lead[0] if lead else 1, -(-K // block)
+    pq = _packed(Q, "Q", torch.uint8, dev, lead + (N, K // 2))
+    ps = _packed(scales, "scales", X.dtype, dev, lead + (N, blocks))
+    pz = _packed(zeros, "zeros", torch.uint8, dev, lead + (N, blocks)) if zeros is not None else 0
+    off = _vector(offsets, "offsets", torch.int32, dev, groups + 1) if offsets is not None else 0
+    ldy = _operand(Y, "Y", X.dtype, dev, 2, rows, N) if Y is not None else max(1, N)
+
+    def body(s):
+        nonlocal Y
+        if Y is None:
+            new = torch.empty if offsets is None else torch.zeros
+            Y = new((rows, N), dtype=X.dtype, device=dev)
+        return _lib.sgemm_q4_matvec(t, groups, rows, N, K, block, X.data_ptr(), ldx, pq, ps, pz,
+                                    Y.data_ptr(), ldy, off, s)
+    _run("sgemm_q4_matvec", dev, stream, body)
+    return Y

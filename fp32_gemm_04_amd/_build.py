@@ -28,6 +28,10 @@ SOURCES = {
     "sgemm.hip": [],
     "mfma_dl.hip": ["-Xarch_device", "-mllvm=--misched=gcn-max-ilp"],
     "conv.hip": [],
+    "lm.hip": [],
+    "lm_bf16.hip": [],
+    "lm_f32.hip": [],
+    "q4.hip": [],
 }
 
 

@@ -1,0 +1,464 @@
+// libsgemm language-model products: argument checks, the choice of tile,
+// workspace layout and launches, behind the C ABI declared in include/slm.h.
+// Nothing here allocates, frees, copies or synchronises: work is queued on the
+// caller's stream.
+#include <hip/hip_runtime.h>
+
+#include <atomic>
+#include <climits>
+#include <cstdint>
+
+#include "../../include/slm.h"
+#include "lm_kernels.hpp"
+
+namespace sgemm {
+namespace lm {
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+int elem_size(int type) { return type == SGEMM_TYPE_BF16 ? 2 : 4; }
+bool aligned(const void *p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Compute units of the current device (cached; 0 on failure, with the error in *rc).
+int compute_units(int *rc)
+{
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e == hipSuccess && dev >= 0 && dev < 64) {
+        int n = cache[dev].load(std::memory_order_relaxed);
+        if (n > 0) return n;
+        e = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev);
+        if (e == hipSuccess && n > 0) {
+            cache[dev].store(n, std::memory_order_relaxed);
+            return n;
+        }
+    }
+    *rc = e == hipSuccess ? (int)hipErrorInvalidDevice : (int)e;
+    return 0;
+}
+
+// An operand the direct loads take: 16-byte rows, and tile offsets below 2^31.
+bool fast_operand(const void *p, int64_t ld, int64_t cols, int64_t group_stride, int size)
+{
+    return aligned(p, 16) && ld * size % 16 == 0 && cols * size % 16 == 0 &&
+           group_stride * size % 16 == 0 && ld * size < ((int64_t)1 << 22);
+}
+
+TileKernel kernel_for(int type, int form, int tile, bool fast)
+{
+    return type == SGEMM_TYPE_BF16 ? bf16_kernel(form, tile, fast) : f32_kernel(form, tile, fast);
+}
+
+int launch(const TileKernel &k, TileArgs &a, int64_t blocks, int slices, hipStream_t stream)
+{
+    if (blocks > INT_MAX) return (int)hipErrorInvalidConfiguration;
+    k.fn<<<dim3((unsigned)blocks, 1, (unsigned)slices), dim3(k.threads), 0, stream>>>(a);
+    return (int)hipGetLastError();
+}
+
+// Tile for one product of M x N outputs: the largest whose tiles still give
+// every compute unit one.
+int plain_tile(int type, int64_t M, int64_t N, int cus)
+{
+    if (M <= 16) return S16;
+    if (type == SGEMM_TYPE_BF16 && ceil_div(M, 256) * ceil_div(N, 256) >= cus) return T256;
+    if (ceil_div(M, 128) * ceil_div(N, 128) >= cus) return T128;
+    return M64;
+}
+
+}  // namespace
+}  // namespace lm
+}  // namespace sgemm
+
+using namespace sgemm::lm;
+
+extern "C" int sgemm_grouped(int type, int trans, int groups, int rows, int N, int K, float alpha,
+                             const void *X, int ldx, const void *W, int ldw, int64_t stride_w,
+                             float beta, void *Y, int ldy, const int *offsets, hipStream_t stream)
+{
+    if (type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16) return -1;
+    if (trans != 0 && trans != 1) return -2;
+    if (groups < 0) return -3;
+    if (rows < 0) return -4;
+    if (N < 0) return -5;
+    if (K < 0) return -6;
+    const int size = elem_size(type);
+    const bool work = groups > 0 && rows > 0 && N > 0;
+    const bool reads = work && K > 0 && alpha != 0.f;
+    if ((reads && !X) || !aligned(X, size)) return -8;
+    if (ldx < (K > 1 ? K : 1)) return -9;
+    if ((reads && !W) || !aligned(W, size)) return -10;
+    const int wcols = trans ? K : N;
+    if (ldw < (wcols > 1 ? wcols : 1)) return -11;
+    if (stride_w < 0) return -12;
+    if ((work && !Y) || !aligned(Y, size)) return -14;
+    if (ldy < (N > 1 ? N : 1)) return -15;
+    if ((work && !offsets) || !aligned(offsets, 4)) return -16;
+    if (!work) return 0;
+    const int used = groups < rows ? groups : rows;  // groups with rows, at most
+    if ((rows + (int64_t)used * 15) / 16 * ceil_div(N, 64) > INT_MAX) return -5;
+
+    const int64_t mean = ceil_div(rows, used);
+    int rc = 0;
+    const int cus = compute_units(&rc);
+    if (cus == 0) return rc;
+    int tile = mean <= 16 ? S16 : mean <= 64 ? M64 : T128;
+    if (type == SGEMM_TYPE_BF16 && mean > 192 &&
+        (ceil_div(rows, 256) + used / 2) * ceil_div(N, 256) >= cus)
+        tile = T256;
+    const int kk = reads ? K : 0;
+    const bool fast = kk == 0 || (fast_operand(X, ldx, K, 0, size) &&
+                                  fast_operand(W, ldw, wcols, stride_w, size));
+    if (!fast && tile == T256) tile = T128;
+    const TileKernel k = kernel_for(type, trans ? F_ROWS_T : F_ROWS_N, tile, fast);
+    // Every group's last tile may be part full.
+    const int64_t most = (rows + (int64_t)used * (k.bm - 1)) / k.bm;
+    const int64_t blocks = most * ceil_div(N, k.bn);
+    TileArgs a = {};
+    a.A = X, a.B = W, a.C = Y;
+    a.lda = ldx, a.ldb = ldw, a.ldc = ldy;
+    a.group_stride = stride_w;
+    a.M = rows, a.N = N, a.K = kk;
+    a.a_cols = K, a.b_cols = wcols, a.b_rows = kk;
+    a.groups = groups, a.offsets = offsets, a.most_tiles = (int)most;
+    a.alpha = alpha, a.beta = beta;
+    a.vec_c = aligned(Y, 4 * size) && ldy % 4 == 0;
+    return launch(k, a, blocks, 1, stream);
+}
+
+extern "C" int sgemm_grouped_wgrad(int type, int groups, int rows, int M, int N, float alpha,
+                                   const void *X, int ldx, const void *G, int ldg, float beta,
+                                   void *D, int ldd, int64_t stride_d, const int *offsets,
+                                   hipStream_t stream)
+{
+    if (type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16) return -1;
+    if (groups < 0) return -2;
+    if (rows < 0) return -3;
+    if (M < 0) return -4;
+    if (N < 0) return -5;
+    const int size = elem_size(type);
+    const bool work = groups > 0 && M > 0 && N > 0;
+    const bool reads = work && rows > 0 && alpha != 0.f;
+    if ((reads && !X) || !aligned(X, size)) return -7;
+    if (ldx < (M > 1 ? M : 1)) return -8;
+    if ((reads && !G) || !aligned(G, size)) return -9;
+    if (ldg < (N > 1 ? N : 1)) return -10;
+    if ((work && !D) || !aligned(D, size)) return -12;
+    if (ldd < (N > 1 ? N : 1)) return -13;
+    if (stride_d < 0) return -14;
+    if ((work && !offsets) || !aligned(offsets, 4)) return -15;
+    if (!work) return 0;
+    // In parts, so that the product of three extents cannot overflow.
+    const int64_t tiles64 = ceil_div(M, 64) * ceil_div(N, 64);
+    if (tiles64 > INT_MAX / groups) return -5;
+
+    int rc = 0;
+    const int cus = compute_units(&rc);
+    if (cus == 0) return rc;
+    const int kk = reads ? rows : 0;  // 0: every group is empty
+    const bool fast = kk == 0 || (fast_operand(X, ldx, M, 0, size) &&
+                                  fast_operand(G, ldg, N, 0, size));
+    int tile = M64;
+    if (type == SGEMM_TYPE_BF16 && fast && ceil_div(M, 256) * ceil_div(N, 256) * groups >= cus)
+        tile = T256;
+    else if (ceil_div(M, 128) * ceil_div(N, 128) * groups >= cus)
+        tile = T128;
+    const TileKernel k = kernel_for(type, F_SUM, tile, fast);
+    const int64_t blocks = ceil_div(M, k.bm) * ceil_div(N, k.bn) * groups;
+    TileArgs a = {};
+    a.A = X, a.B = G, a.C = D;
+    a.lda = ldx, a.ldb = ldg, a.ldc = ldd;
+    a.group_stride = stride_d;
+    a.M = M, a.N = N, a.K = kk;
+    a.a_cols = M, a.b_cols = N;
+    a.groups = groups, a.offsets = offsets;
+    a.alpha = alpha, a.beta = beta;
+    a.vec_c = aligned(D, 4 * size) && ldd % 4 == 0 && stride_d % 4 == 0;
+    return launch(k, a, blocks, 1, stream);
+}
+
+// ---------------------------------------------------------------- cross entropy
+
+namespace sgemm {
+namespace lm {
+namespace {
+
+// Joins the tiles' row statistics, one wave per row: with top the largest
+// maximum, lse = top + log(sum of the tiles' sums, each scaled to top).
+__global__ void __launch_bounds__(256) xent_join_kernel(int rows, int tiles, int vocab,
+                                                        const f32x2 *parts,
+                                                        const float *target_value,
+                                                        const int64_t *targets, float *loss,
+                                                        float *lse)
+{
+    const int lane = threadIdx.x & 63;
+    const int row = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row >= rows) return;
+    const f32x2 *p = parts + (int64_t)row * tiles;
+    float top = -INFINITY, sum = 0.f;
+    for (int t = lane; t < tiles; t += 64) {
+        const f32x2 v = p[t];
+        const float m = fmaxf(top, v[0]);
+        // A side without a finite maximum has an empty sum, or one that is not finite
+        // whatever it is scaled by.
+        const float a = top == m || !isfinite(top) ? 1.f : expf(top - m);
+        const float b = v[0] == m || !isfinite(v[0]) ? 1.f : expf(v[0] - m);
+        sum = sum * a + v[1] * b;
+        top = m;
+    }
+#pragma unroll
+    for (int d = 32; d; d /= 2) {
+        const float t = __shfl_xor(top, d), s = __shfl_xor(sum, d);
+        const float m = fmaxf(top, t);
+        const float a = top == m || !isfinite(top) ? 1.f : expf(top - m);
+        const float b = t == m || !isfinite(t) ? 1.f : expf(t - m);
+        sum = sum * a + s * b;
+        top = m;
+    }
+    if (lane == 0) {
+        const float v = (isfinite(top) ? top : 0.f) + logf(sum);
+        lse[row] = v;
+        const int64_t target = targets[row];
+        loss[row] = target >= 0 && target < vocab ? v - target_value[row] : 0.f;
+    }
+}
+
+// dX <- the slices' fp32 sums added in order, rounded once.
+template <typename T>
+__global__ void __launch_bounds__(256) xent_sum_kernel(int rows, int K, int slices,
+                                                       int64_t slice_stride, const float *parts,
+                                                       T *dX, int64_t lddx)
+{
+    const int64_t n = (int64_t)rows * K;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n;
+         i += (int64_t)gridDim.x * 256) {
+        float v = parts[i];
+        for (int s = 1; s < slices; ++s) v += parts[s * slice_stride + i];
+        dX[i / K * lddx + i % K] = (T)v;
+    }
+}
+
+// How the backward pass is cut: `piece` columns of the vocabulary at a time, and
+// the sum over a piece that gives dX in `slices` (few rows and hidden values
+// leave compute units idle otherwise).
+struct XentPlan {
+    int64_t piece, pieces, ld;  // ld: leading dimension of the piece's derivatives
+    int slices;
+    bool sums;                  // dX goes through fp32 sums in the workspace
+    int64_t d_bytes, bytes;
+};
+
+XentPlan xent_plan(int type, int rows, int vocab, int K, int cus)
+{
+    XentPlan p;
+    const int size = elem_size(type);
+    // A piece's derivatives take up to 256 MiB (the last-level cache's size), but a
+    // piece is never narrower than 2048 columns.
+    int64_t most = ((int64_t)256 << 20) / ((int64_t)rows * size) / 256 * 256;
+    if (most < 2048) most = 2048;
+    p.pieces = ceil_div(vocab, most);
+    p.piece = round_up(ceil_div(vocab, p.pieces), 256);
+    p.pieces = ceil_div(vocab, p.piece);
+    p.ld = p.piece;
+    p.d_bytes = round_up((int64_t)rows * p.ld * size, 256);
+    const int64_t tiles = ceil_div(rows, 128) * ceil_div(K, 128);
+    int64_t s = tiles >= cus ? 1 : cus / tiles;
+    if (s > p.piece / 1024) s = p.piece / 1024;
+    p.slices = s < 1 ? 1 : s > 64 ? 64 : (int)s;
+    p.sums = p.slices > 1 || (p.pieces > 1 && type != SGEMM_TYPE_F32);
+    p.bytes = p.d_bytes + (p.sums ? (int64_t)p.slices * rows * K * 4 : 0);
+    return p;
+}
+
+// Row statistics of the narrowest tile's columns, so that the workspace fits
+// whichever tile runs, and each row's value at its target.
+int64_t stats_bytes(int rows, int vocab)
+{
+    return round_up((int64_t)rows * 4, 256) + (int64_t)rows * ceil_div(vocab, 64) * 8;
+}
+
+int check_xent(int type, int rows, int vocab, int K, const void *X, int ldx, const void *W, int ldw,
+               const int64_t *targets)
+{
+    if (type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16) return -1;
+    if (rows < 0) return -2;
+    if (vocab < 0 || (vocab == 0 && rows > 0)) return -3;
+    if (K < 0) return -4;
+    const int size = elem_size(type);
+    const bool reads = rows > 0 && K > 0;
+    if ((reads && !X) || !aligned(X, size)) return -5;
+    if (ldx < (K > 1 ? K : 1)) return -6;
+    if ((reads && !W) || !aligned(W, size)) return -7;
+    if (ldw < (K > 1 ? K : 1)) return -8;
+    if ((rows > 0 && !targets) || !aligned(targets, 8)) return -9;
+    if (ceil_div(rows, 16) * ceil_div(vocab, 64) > INT_MAX) return -3;
+    return 0;
+}
+
+}  // namespace
+}  // namespace lm
+}  // namespace sgemm
+
+extern "C" int64_t sgemm_xent_workspace(int type, int rows, int vocab, int K, int backward)
+{
+    if (type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16) return -1;
+    if (rows < 0) return -2;
+    if (vocab < 0) return -3;
+    if (K < 0) return -4;
+    if (backward != 0 && backward != 1) return -5;
+    if (rows == 0 || vocab == 0) return 0;
+    if (!backward) return stats_bytes(rows, vocab);
+    int rc = 0;
+    int cus = compute_units(&rc);
+    if (cus == 0) cus = 256;  // no device: the plan of a whole MI355X
+    return xent_plan(type, rows, vocab, K, cus).bytes;
+}
+
+extern "C" int sgemm_xent(int type, int rows, int vocab, int K, const void *X, int ldx,
+                          const void *W, int ldw, const int64_t *targets, float *loss, float *lse,
+                          void *ws, int64_t ws_bytes, hipStream_t stream)
+{
+    if (int rc = check_xent(type, rows, vocab, K, X, ldx, W, ldw, targets)) return rc;
+    if ((rows > 0 && !loss) || !aligned(loss, 4)) return -10;
+    if ((rows > 0 && !lse) || !aligned(lse, 4)) return -11;
+    if ((rows > 0 && !ws) || !aligned(ws, 16)) return -12;
+    if (rows == 0) return 0;
+    if (ws_bytes < stats_bytes(rows, vocab)) return -13;
+
+    int rc = 0;
+    const int cus = compute_units(&rc);
+    if (cus == 0) return rc;
+    const int size = elem_size(type);
+    const bool fast = K == 0 || (fast_operand(X, ldx, K, 0, size) &&
+                                 fast_operand(W, ldw, K, 0, size));
+    int tile = plain_tile(type, rows, vocab, cus);
+    if (!fast && tile == T256) tile = T128;
+    const TileKernel k = kernel_for(type, F_STATS, tile, fast);
+    float *value = static_cast<float *>(ws);
+    float *parts = value + round_up((int64_t)rows * 4, 256) / 4;
+    const int tiles = (int)ceil_div(vocab, k.bn);
+    TileArgs a = {};
+    a.A = X, a.B = W;
+    a.lda = ldx, a.ldb = ldw;
+    a.M = rows, a.N = vocab, a.K = K;
+    a.a_cols = a.b_cols = K;
+    a.targets = targets, a.parts = parts, a.target_value = value;
+    rc = launch(k, a, ceil_div(rows, k.bm) * tiles, 1, stream);
+    if (rc) return rc;
+    xent_join_kernel<<<dim3((unsigned)ceil_div(rows, 4)), dim3(256), 0, stream>>>(
+        rows, tiles, vocab, reinterpret_cast<const sgemm::f32x2 *>(parts), value, targets, loss, lse);
+    return (int)hipGetLastError();
+}
+
+extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const void *X, int ldx,
+                                   const void *W, int ldw, const int64_t *targets, const float *lse,
+                                   const float *dloss, void *dX, int lddx, void *dW, int lddw,
+                                   void *ws, int64_t ws_bytes, hipStream_t stream)
+{
+    if (int rc = check_xent(type, rows, vocab, K, X, ldx, W, ldw, targets)) return rc;
+    const int size = elem_size(type);
+    if ((rows > 0 && !lse) || !aligned(lse, 4)) return -10;
+    if ((rows > 0 && !dloss) || !aligned(dloss, 4)) return -11;
+    if (!aligned(dX, size)) return -12;
+    if (lddx < (K > 1 ? K : 1)) return -13;
+    if (!aligned(dW, size)) return -14;
+    if (lddw < (K > 1 ? K : 1)) return -15;
+    if ((rows > 0 && !ws) || !aligned(ws, 16)) return -16;
+    if (K == 0 || vocab == 0 || (!dX && !dW) || (rows == 0 && !dW)) return 0;
+    int rc = 0;
+    const int cus = compute_units(&rc);
+    if (cus == 0) return rc;
+    TileArgs a = {};
+    if (rows == 0) {  // no row: dW is zero
+        a.C = dW, a.ldc = lddw;
+        a.M = vocab, a.N = K;
+        a.vec_c = aligned(dW, 4 * size) && lddw % 4 == 0;
+        const TileKernel k = kernel_for(type, F_DW, M64, true);
+        return launch(k, a, ceil_div(vocab, k.bm) * ceil_div(K, k.bn), 1, stream);
+    }
+    const XentPlan p = xent_plan(type, rows, vocab, K, cus);
+    if (ws_bytes < p.bytes) return -17;
+    float *sums = reinterpret_cast<float *>(static_cast<char *>(ws) + p.d_bytes);
+    const bool fast_x = fast_operand(X, ldx, K, 0, size), fast_w = fast_operand(W, ldw, K, 0, size);
+    // The piece's derivatives are read with their own leading dimension.
+    const bool fast_d = p.ld * size < ((int64_t)1 << 22);
+
+    for (int64_t c = 0; c < p.pieces; ++c) {
+        const int64_t col0 = c * p.piece;
+        const int n = (int)(vocab - col0 < p.piece ? vocab - col0 : p.piece);
+        const int n8 = (int)round_up(n, 8);  // columns the derivatives are written for
+        const char *Wc = static_cast<const char *>(W) + col0 * ldw * size;
+        {
+            const bool fast = fast_x && fast_w;
+            int tile = plain_tile(type, rows, n, cus);
+            if (!fast && tile == T256) tile = T128;
+            const TileKernel k = kernel_for(type, F_GRAD, tile, fast);
+            a = TileArgs{};
+            a.A = X, a.B = Wc, a.C = ws;
+            a.lda = ldx, a.ldb = ldw, a.ldc = p.ld;
+            a.M = rows, a.N = n, a.K = K;
+            a.a_cols = a.b_cols = K;
+            a.targets = targets, a.lse = lse, a.dloss = dloss;
+            a.col0 = (int)col0, a.vocab = vocab;
+            rc = launch(k, a, ceil_div(rows, k.bm) * ceil_div(n, k.bn), 1, stream);
+            if (rc) return rc;
+        }
+        if (dW) {
+            const bool fast = fast_d && fast_x;
+            int tile = plain_tile(type, n, K, cus);
+            if (tile == S16 || (!fast && tile == T256)) tile = tile == S16 ? M64 : T128;
+            const TileKernel k = kernel_for(type, F_DW, tile, fast);
+            a = TileArgs{};
+            a.A = ws, a.B = X, a.C = static_cast<char *>(dW) + col0 * lddw * size;
+            a.lda = p.ld, a.ldb = ldx, a.ldc = lddw;
+            a.M = n, a.N = K, a.K = rows;
+            a.a_cols = n8, a.b_cols = K, a.b_rows = rows;
+            a.alpha = 1.f;
+            a.vec_c = aligned(dW, 4 * size) && lddw % 4 == 0;
+            rc = launch(k, a, ceil_div(n, k.bm) * ceil_div(K, k.bn), 1, stream);
+            if (rc) return rc;
+        }
+        if (dX) {
+            const bool fast = fast_d && fast_w;
+            int tile = plain_tile(type, rows, K, cus);
+            if (tile == M64 && p.slices > 1 && rows > 64) tile = T128;
+            if (!fast && tile == T256) tile = T128;
+            a = TileArgs{};
+            a.A = ws, a.B = Wc;
+            a.lda = p.ld, a.ldb = ldw;
+            a.M = rows, a.N = K, a.K = n;
+            a.a_cols = n8, a.b_cols = K, a.b_rows = n;
+            const bool direct = !p.sums && p.pieces == 1;
+            const TileKernel k = kernel_for(type, direct ? F_DX : F_PART, tile, fast);
+            if (direct) {
+                a.C = dX, a.ldc = lddx, a.alpha = 1.f;
+                a.vec_c = aligned(dX, 4 * size) && lddx % 4 == 0;
+            } else {
+                a.C = p.sums ? static_cast<void *>(sums) : dX;
+                a.ldc = p.sums ? K : lddx;
+                a.vec_c = aligned(a.C, 16) && a.ldc % 4 == 0;
+                a.accumulate = c > 0;
+                a.split_k = (int)round_up(ceil_div(n, p.slices), 64);
+                a.slice_stride = (int64_t)rows * K;
+            }
+            rc = launch(k, a, ceil_div(rows, k.bm) * ceil_div(K, k.bn), direct ? 1 : p.slices,
+                        stream);
+            if (rc) return rc;
+        }
+    }
+    if (dX && p.sums) {
+        const int64_t blocks = ceil_div((int64_t)rows * K, 1024);
+        const dim3 grid((unsigned)(blocks < 16 * cus ? blocks : 16 * cus));
+        const int64_t stride = (int64_t)rows * K;
+        if (type == SGEMM_TYPE_BF16)
+            xent_sum_kernel<bf16><<<grid, dim3(256), 0, stream>>>(rows, K, p.slices, stride, sums,
+                                                                  static_cast<bf16 *>(dX), lddx);
+        else
+            xent_sum_kernel<float><<<grid, dim3(256), 0, stream>>>(rows, K, p.slices, stride, sums,
+                                                                   static_cast<float *>(dX), lddx);
+        return (int)hipGetLastError();
+    }
+    return 0;
+}

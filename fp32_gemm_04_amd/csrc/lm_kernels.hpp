@@ -1,0 +1,52 @@
+// The tile kernels that are built, by type, form and tile; shared by the
+// host code (lm.hip) and the translation units that instantiate them.
+#pragma once
+
+#include "lm_tile.hpp"
+
+namespace sgemm {
+namespace lm {
+
+enum Tile { S16, M64, T128, T256, NUM_TILES };
+// The operand layouts and epilogues of the products.
+enum Form {
+    F_ROWS_T,   // grouped rows, weights N x K
+    F_ROWS_N,   // grouped rows, weights K x N
+    F_SUM,      // grouped contraction
+    F_STATS,    // logits to row statistics
+    F_GRAD,     // logits to their derivatives
+    F_PART,     // d W, fp32 sums
+    F_DX,       // d W, rounded to the type
+    F_DW,       // d^T X
+    NUM_FORMS
+};
+
+struct TileKernel {
+    TileFn fn;
+    int bm, bn, threads;
+};
+
+// null fn: that tile is not built for the form and type.
+TileKernel bf16_kernel(int form, int tile, bool fast);
+TileKernel f32_kernel(int form, int tile, bool fast);
+
+template <typename T, int BM, int BN, int WM, int WN, int NBUF, bool FAST>
+TileKernel tile_entry(int form)
+{
+    TileFn fn = nullptr;
+    switch (form) {
+    case F_ROWS_T: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, KC, KC, ROWS, STORE, FAST>; break;
+    case F_ROWS_N: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, KC, MC, ROWS, STORE, FAST>; break;
+    case F_SUM: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, MC, MC, SUM, STORE, FAST>; break;
+    case F_STATS: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, KC, KC, PLAIN, STATS, FAST>; break;
+    case F_GRAD: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, KC, KC, PLAIN, GRAD, FAST>; break;
+    case F_PART: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, KC, MC, PLAIN, PART, FAST>; break;
+    case F_DX: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, KC, MC, PLAIN, STORE, FAST>; break;
+    case F_DW: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, MC, MC, PLAIN, STORE, FAST>; break;
+    default: break;
+    }
+    return TileKernel{fn, BM, BN, WM * WN * 64};
+}
+
+}  // namespace lm
+}  // namespace sgemm

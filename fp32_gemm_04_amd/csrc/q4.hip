@@ -1,0 +1,138 @@
+// libsgemm products with weights held in 4 bits: argument checks, the choice of
+// kernel and launches, behind the C ABI declared in include/slm.h.  Nothing
+// here allocates, frees, copies or synchronises.
+#include <hip/hip_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "../../include/slm.h"
+#include "q4.hpp"
+
+namespace sgemm {
+namespace q4 {
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool aligned(const void *p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+struct Form {
+    int rt, nt;
+};
+
+template <typename T, int BLOCK, bool ALIGNED>
+Q4Fn kernel_of(Form f)
+{
+    if (f.rt == 1) return f.nt == 1 ? q4_kernel<T, BLOCK, 1, 1, ALIGNED>
+                                    : q4_kernel<T, BLOCK, 1, 2, ALIGNED>;
+    if (f.rt == 2) return q4_kernel<T, BLOCK, 2, 2, ALIGNED>;
+    return q4_kernel<T, BLOCK, 4, 2, ALIGNED>;
+}
+
+template <typename T>
+Q4Fn kernel_for(int block, bool al, Form f)
+{
+    if (block == 32) return al ? kernel_of<T, 32, true>(f) : kernel_of<T, 32, false>(f);
+    if (block == 64) return al ? kernel_of<T, 64, true>(f) : kernel_of<T, 64, false>(f);
+    return al ? kernel_of<T, 128, true>(f) : kernel_of<T, 128, false>(f);
+}
+
+template <typename T>
+void quantize(dim3 grid, int N, int K, int block, int nblk, const void *W, int64_t ldw, uint8_t *Q,
+              void *S, uint8_t *Z, hipStream_t stream)
+{
+    auto fn = block == 32 ? (Z ? q4_quantize_kernel<T, 32, true> : q4_quantize_kernel<T, 32, false>)
+            : block == 64 ? (Z ? q4_quantize_kernel<T, 64, true> : q4_quantize_kernel<T, 64, false>)
+                          : (Z ? q4_quantize_kernel<T, 128, true>
+                               : q4_quantize_kernel<T, 128, false>);
+    fn<<<grid, dim3(256), 0, stream>>>(N, K, nblk, static_cast<const T *>(W), ldw, Q,
+                                       static_cast<T *>(S), Z);
+}
+
+}  // namespace
+}  // namespace q4
+}  // namespace sgemm
+
+using namespace sgemm::q4;
+
+extern "C" int sgemm_q4_matvec(int type, int groups, int rows, int N, int K, int block,
+                               const void *X, int ldx, const uint8_t *Q, const void *S,
+                               const uint8_t *Z, void *Y, int ldy, const int *offsets,
+                               hipStream_t stream)
+{
+    if (type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16) return -1;
+    if (groups < 0 || (!offsets && groups != 1) || groups > 65535) return -2;
+    if (rows < 0) return -3;
+    if (N < 0) return -4;
+    if (K < 0 || K % 2 != 0) return -5;
+    if (block != 32 && block != 64 && block != 128) return -6;
+    const int size = type == SGEMM_TYPE_BF16 ? 2 : 4;
+    const bool work = groups > 0 && rows > 0 && N > 0, reads = work && K > 0;
+    if ((reads && !X) || !aligned(X, size)) return -7;
+    if (ldx < (K > 1 ? K : 1)) return -8;
+    if (reads && !Q) return -9;
+    if ((reads && !S) || !aligned(S, size)) return -10;
+    if ((work && !Y) || !aligned(Y, size)) return -12;
+    if (ldy < (N > 1 ? N : 1)) return -13;
+    if (!aligned(offsets, 4)) return -14;
+    if (!work) return 0;
+
+    const int parts = type == SGEMM_TYPE_F32 ? 3 : 1;
+    const int used = groups < rows ? groups : rows;
+    const int64_t places = ceil_div(rows, used) * parts;  // of a group, on average
+    const Form f = places > 32 ? Form{4, 2} : places > 16 ? Form{2, 2} : Form{1, N >= 8192 ? 2 : 1};
+    Q4Args a = {};
+    a.X = X, a.Q = Q, a.S = S, a.Z = Z, a.Y = Y, a.offsets = offsets;
+    a.ldx = ldx, a.ldy = ldy;
+    a.q_stride = (int64_t)N * (K / 2);
+    a.s_stride = (int64_t)N * ceil_div(K, block);
+    a.rows = rows, a.N = N, a.K = K;
+    a.wn = f.rt == 1 ? 1 : 2;
+    // Rows per pass: what the tiles hold, but no more places than a group is likely to
+    // need, so that more of K is staged at once.
+    const int64_t likely = offsets ? 2 * ceil_div(rows, used) : rows;
+    const int hold = f.rt * 16 / parts;
+    a.pass = likely < hold ? (int)likely : hold;
+    const int wide = a.pass * parts;
+    int64_t slab = (kSlab / wide - 16) / 2 / 128 * 128;
+    const int64_t step = 128 * kWaves / a.wn;  // one chunk for every wave
+    if (slab > step) slab = slab / step * step;
+    const int64_t all = ceil_div(K, 128) * 128;
+    a.slab = (int)(slab < all ? slab : all > 0 ? all : 128);
+    a.vec_x = aligned(X, 16) && (int64_t)ldx * size % 16 == 0;
+    const bool al = K % 32 == 0 && aligned(Q, 16);
+    const Q4Fn fn = type == SGEMM_TYPE_BF16 ? kernel_for<bf16>(block, al, f)
+                                            : kernel_for<float>(block, al, f);
+    const int cols = a.wn * f.nt * 16;
+    const int staged = wide * (a.slab * 2 + 16);
+    const int sums = kWaves / a.wn * f.rt * 16 * cols * 4;
+    const int64_t blocks = ceil_div(N, cols);
+    fn<<<dim3((unsigned)blocks, (unsigned)groups), dim3(kWaves * 64),
+         staged > sums ? staged : sums, stream>>>(a);
+    return (int)hipGetLastError();
+}
+
+extern "C" int sgemm_q4_quantize(int type, int N, int K, int block, const void *W, int ldw,
+                                 uint8_t *Q, void *S, uint8_t *Z, hipStream_t stream)
+{
+    if (type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16) return -1;
+    if (N < 0) return -2;
+    if (K < 0 || K % 2 != 0) return -3;
+    if (block != 32 && block != 64 && block != 128) return -4;
+    const int size = type == SGEMM_TYPE_BF16 ? 2 : 4;
+    const bool work = N > 0 && K > 0;
+    if ((work && !W) || !aligned(W, size)) return -5;
+    if (ldw < (K > 1 ? K : 1)) return -6;
+    if (work && !Q) return -7;
+    if ((work && !S) || !aligned(S, size)) return -8;
+    if (!work) return 0;
+    const int nblk = (int)ceil_div(K, block);
+    const int64_t blocks = ceil_div((int64_t)N * nblk, 16);
+    if (blocks > INT_MAX) return -2;
+    const dim3 grid((unsigned)blocks);
+    if (type == SGEMM_TYPE_BF16)
+        quantize<bf16>(grid, N, K, block, nblk, W, ldw, Q, S, Z, stream);
+    else
+        quantize<float>(grid, N, K, block, nblk, W, ldw, Q, S, Z, stream);
+    return (int)hipGetLastError();
+}

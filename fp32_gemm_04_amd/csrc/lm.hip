@@ -185,8 +185,8 @@ namespace sgemm {
 namespace lm {
 namespace {
 
-// Joins the tiles' row statistics, one wave per row: with top the largest
-// maximum, lse = top + log(sum of the tiles' sums, each scaled to top).
+// Joins the tiles' row statistics, one wave per row: lse = ln 2 (top + log2 sum), top the
+// largest of the tiles' and sum theirs, each scaled to top.
 __global__ void __launch_bounds__(256) xent_join_kernel(int rows, int tiles, int vocab,
                                                         const f32x2 *parts,
                                                         const float *target_value,
@@ -200,25 +200,13 @@ __global__ void __launch_bounds__(256) xent_join_kernel(int rows, int tiles, int
     float top = -INFINITY, sum = 0.f;
     for (int t = lane; t < tiles; t += 64) {
         const f32x2 v = p[t];
-        const float m = fmaxf(top, v[0]);
-        // A side without a finite maximum has an empty sum, or one that is not finite
-        // whatever it is scaled by.
-        const float a = top == m || !isfinite(top) ? 1.f : expf(top - m);
-        const float b = v[0] == m || !isfinite(v[0]) ? 1.f : expf(v[0] - m);
-        sum = sum * a + v[1] * b;
-        top = m;
+        join_sums(top, sum, v[0], v[1]);
     }
 #pragma unroll
-    for (int d = 32; d; d /= 2) {
-        const float t = __shfl_xor(top, d), s = __shfl_xor(sum, d);
-        const float m = fmaxf(top, t);
-        const float a = top == m || !isfinite(top) ? 1.f : expf(top - m);
-        const float b = t == m || !isfinite(t) ? 1.f : expf(t - m);
-        sum = sum * a + s * b;
-        top = m;
-    }
+    for (int d = 32; d; d /= 2) join_sums(top, sum, __shfl_xor(top, d), __shfl_xor(sum, d));
     if (lane == 0) {
-        const float v = (isfinite(top) ? top : 0.f) + logf(sum);
+        constexpr float ln2 = 0.693147180559945309417f;
+        const float v = ((isfinite(top) ? top : 0.f) + log2f(sum)) * ln2;
         lse[row] = v;
         const int64_t target = targets[row];
         loss[row] = target >= 0 && target < vocab ? v - target_value[row] : 0.f;
@@ -261,7 +249,7 @@ XentPlan xent_plan(int type, int rows, int vocab, int K, int cus)
     p.pieces = ceil_div(vocab, most);
     p.piece = round_up(ceil_div(vocab, p.pieces), 256);
     p.pieces = ceil_div(vocab, p.piece);
-    p.ld = p.piece;
+    p.ld = p.piece + 64;
     p.d_bytes = round_up((int64_t)rows * p.ld * size, 256);
     const int64_t tiles = ceil_div(rows, 128) * ceil_div(K, 128);
     int64_t s = tiles >= cus ? 1 : cus / tiles;

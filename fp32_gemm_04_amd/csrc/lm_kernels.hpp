@@ -30,19 +30,19 @@ struct TileKernel {
 TileKernel bf16_kernel(int form, int tile, bool fast);
 TileKernel f32_kernel(int form, int tile, bool fast);
 
-template <typename T, int BM, int BN, int WM, int WN, int NBUF, bool FAST>
+template <typename T, int BM, int BN, int WM, int WN, int NBUF, int BL, int WPE, bool FAST>
 TileKernel tile_entry(int form)
 {
     TileFn fn = nullptr;
     switch (form) {
-    case F_ROWS_T: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, KC, KC, ROWS, STORE, FAST>; break;
-    case F_ROWS_N: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, KC, MC, ROWS, STORE, FAST>; break;
-    case F_SUM: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, MC, MC, SUM, STORE, FAST>; break;
-    case F_STATS: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, KC, KC, PLAIN, STATS, FAST>; break;
-    case F_GRAD: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, KC, KC, PLAIN, GRAD, FAST>; break;
-    case F_PART: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, KC, MC, PLAIN, PART, FAST>; break;
-    case F_DX: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, KC, MC, PLAIN, STORE, FAST>; break;
-    case F_DW: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, MC, MC, PLAIN, STORE, FAST>; break;
+    case F_ROWS_T: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, BL, WPE, KC, KC, ROWS, STORE, FAST>; break;
+    case F_ROWS_N: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, BL, WPE, KC, MC, ROWS, STORE, FAST>; break;
+    case F_SUM: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, BL, WPE, MC, MC, SUM, STORE, FAST>; break;
+    case F_STATS: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, BL, WPE, KC, KC, PLAIN, STATS, FAST>; break;
+    case F_GRAD: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, BL, WPE, KC, KC, PLAIN, GRAD, FAST>; break;
+    case F_PART: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, BL, WPE, KC, MC, PLAIN, PART, FAST>; break;
+    case F_DX: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, BL, WPE, KC, MC, PLAIN, STORE, FAST>; break;
+    case F_DW: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, BL, WPE, MC, MC, PLAIN, STORE, FAST>; break;
     default: break;
     }
     return TileKernel{fn, BM, BN, WM * WN * 64};

@@ -21,20 +21,26 @@
 //
 // LDS layouts, in 16-byte chunks; the permutation is applied to which chunk a
 // lane fetches, since the DMA writes lanes in order:
-//   KC: row r holds its 8 chunks at places p = c ^ (r & 7), so the 16 lanes of
-//       an operand read (one chunk of each of 16 rows) meet every bank evenly.
+// LDS has 64 banks of four bytes; a read is conflict-free when the lanes of each
+// 256 bytes of it meet all banks:
+//   KC: row r holds its 8 chunks at places p = c ^ (r / 2 & 7): the 16 lanes that
+//       read one chunk of 16 rows (two rows per 256 bytes) meet 16 places.
 //   MC: slab row k holds chunk c at p = c ^ swizzle(k).  bf16 operands are
 //       read with ds_read_b64_tr_b16, which hands a lane four consecutive k
-//       of one column: 16 lanes read 32 bytes of 4 rows, and swizzle(k) =
-//       2 (k & 3) puts those rows in different banks.  fp32 operands need one
-//       k per lane and step: four lane groups read 64 bytes of rows 4 apart,
-//       and swizzle(k) = k & 12 separates them.
+//       of one column: 16 lanes read 32 bytes of each of 4 rows.  With BL = 16 the two
+//       halves of 32 lanes are 8 rows apart, so 8 rows must differ in their 32-byte
+//       place; with BL = 32 they are neighbours, so 4 rows in their 64-byte place.
+//       fp32 operands need one k per lane and step: the lane groups read 64 (BL = 32:
+//       128) bytes of rows 4 apart.
 //
-// Both operands of a matrix instruction use the same assignment of k to lanes:
-// with l = lane, g = l / 16, bf16 16x16x32 takes k = 8 g .. 8 g + 7, and four
-// fp32 16x16x4 steps s = 0..3 take k = 4 g + s.  B is the instruction's first
-// operand, so a lane holds four consecutive columns of one row of C:
-//   row l % 16, columns 4 g .. 4 g + 3 of each 16 x 16 block.
+// Both operands of a matrix instruction use the same assignment of k to lanes.
+// With blocks of BL = 16 and g = lane / 16, bf16 16x16x32 takes k = 8 g .. 8 g + 7, and
+// four fp32 16x16x4 steps s = 0..3 take k = 4 g + s; with BL = 32 and g = lane / 32, two
+// bf16 32x32x16 (eight fp32 32x32x2) cover the same half slab.  The larger block
+// halves the instructions a wave issues, which the largest tile needs: its
+// accumulators leave one wave per SIMD.  B is the instruction's first operand, so
+// a lane holds groups of four consecutive columns of one row of C:
+//   row lane % BL, columns 4 g .. 4 g + 3 (BL = 32: and 8, 16, 24 further on).
 #pragma once
 
 #include <type_traits>
@@ -100,10 +106,10 @@ template <> struct Elem<float> {
 
 // Lane l's 16 bytes at base + voff go to LDS [lds + 16 l, + 16); zeros where
 // voff lies outside the descriptor.  s_nop: an LDS DMA needs a wait state after
-// the write of M0, and the descriptor may have been written by the vector unit.
+// the write of M0.
 __device__ __forceinline__ void load_slab16(u32x4 rsrc, uint32_t voff, uint32_t lds)
 {
-    asm volatile("s_nop 4\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\t"
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\t"
                  "buffer_load_dwordx4 %0, %1, 0 offen lds"
                  :
                  : "v"(voff), "s"(rsrc), "s"(lds)
@@ -114,6 +120,20 @@ template <int N>
 __device__ __forceinline__ void wait_slab_barrier()
 {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// (top, sum) stands for sum * 2^top: (top, sum) += (t, s).  A side whose top is not
+// finite has an empty sum (top -inf), or one that is infinite or NaN whatever it is
+// scaled by, and is taken as it is.
+__device__ __forceinline__ void join_sums(float &top, float &sum, float t, float s)
+{
+    const float m = fmaxf(top, t);
+    const float a = top == m || !isfinite(top) ? 1.f : __builtin_amdgcn_exp2f(top - m);
+    const float b = t == m || !isfinite(t) ? 1.f : __builtin_amdgcn_exp2f(t - m);
+    sum = sum * a + s * b;
+    top = m;
 }
 
 constexpr uint32_t kOutside = 0x80000000u;  // beyond every descriptor's range
@@ -132,7 +152,7 @@ __device__ __forceinline__ u32x4 descriptor(const char *p, int64_t left)
 }
 
 // One operand's slabs: where this wave's units (64 chunks each) come from.
-template <typename T, int B, Layout L>
+template <typename T, int B, Layout L, int BL>
 struct Slab {
     static constexpr int BK = Elem<T>::BK, EPC = Elem<T>::EPC;
     static constexpr int UNITS = B / 8;            // 64-chunk units per slab
@@ -141,47 +161,56 @@ struct Slab {
 
     __device__ static __forceinline__ int swizzle(int k)
     {
+        // Rows shorter than 256 bytes already alternate between places.
+        constexpr int ROWS = RC >= 16 ? 1 : 16 / RC;  // rows per 256 bytes
+        const int j = k / ROWS;
+        int p;
         if constexpr (std::is_same<T, float>::value)
-            return (k & 12) & (RC - 1);
+            p = BL == 16 ? 4 * ((k >> 2) & 3) : 8 * ((k >> 2) & 1);
+        else if constexpr (BL == 32)
+            p = 4 * (j & 3);
         else
-            return (2 * (k & 3)) & (RC - 1);
+            p = ROWS == 1 ? 2 * ((k & 3) + ((k >> 1) & 4)) : 2 * ((j & 1) + ((k >> 2) & 2));
+        return p & (RC - 1);
     }
     // Row (KC: of the tile; MC: of the slab) and chunk that slot s fetches.
     __device__ static __forceinline__ void slot(int s, int &row, int &chunk)
     {
         if constexpr (L == KC) {
             row = s >> 3;
-            chunk = (s & 7) ^ (row & 7);
+            chunk = (s & 7) ^ ((row >> 1) & 7);
         } else {
             row = s / RC;
             chunk = (s % RC) ^ swizzle(row);
         }
     }
-    // The operand fragment of 16-row block blk and step (half slab) h.
-    __device__ static __forceinline__ typename Elem<T>::Frag frag(const char *buf, int blk, int h,
+    // The operand fragment of BL-row block blk, step k of 128 / (8 BL) in the slab.
+    __device__ static __forceinline__ typename Elem<T>::Frag frag(const char *buf, int blk, int k,
                                                                   int lane)
     {
-        const int l = lane & 15, g = lane >> 4;
+        constexpr int G = 64 / BL;                    // lane groups: chunks a step takes
+        const int l = lane & (BL - 1), g = lane / BL;
         if constexpr (L == KC) {
-            const char *p = buf + blk * 2048 + l * 128 + (((4 * h + g) ^ (l & 7)) << 4);
+            const char *p = buf + blk * (BL * 128) + l * 128 + (((G * k + g) ^ ((l >> 1) & 7)) << 4);
             return *reinterpret_cast<const typename Elem<T>::Frag *>(p);
         } else if constexpr (std::is_same<T, float>::value) {
             f32x4 v;
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const int k = 16 * h + 4 * g + s;
-                const int c = (4 * blk + (l >> 2)) ^ swizzle(k);
-                v[s] = *reinterpret_cast<const float *>(buf + k * (B * 4) + c * 16 + (l & 3) * 4);
+                const int row = 4 * (G * k + g) + s;
+                const int c = (blk * (BL / 4) + (l >> 2)) ^ swizzle(row);
+                v[s] = *reinterpret_cast<const float *>(buf + row * (B * 4) + c * 16 + (l & 3) * 4);
             }
             return v;
         } else {
             bf16x8 v;
+            const int i = lane & 15;                  // the transposing read works on 16 lanes
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const int k = 32 * h + 8 * g + 4 * s + (l >> 2);
-                const int c = (2 * blk + ((l >> 1) & 1)) ^ swizzle(k);
-                const uint32_t at = (uint32_t)(uintptr_t)(const lds_char *)buf + k * (B * 2) +
-                                    c * 16 + (l & 1) * 8;
+                const int row = 8 * (G * k + g) + 4 * s + (i >> 2);
+                const int c = (blk * (BL / 8) + (l >> 4) * 2 + ((i >> 1) & 1)) ^ swizzle(row);
+                const uint32_t at = (uint32_t)(uintptr_t)(const lds_char *)buf + row * (B * 2) +
+                                    c * 16 + (i & 1) * 8;
                 const s16x4 q = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                     (lds_s16x4 *)(uintptr_t)at);
 #pragma unroll
@@ -192,16 +221,27 @@ struct Slab {
     }
 };
 
-template <typename T>
-__device__ __forceinline__ f32x4 mfma_step(const typename Elem<T>::Frag &b,
-                                           const typename Elem<T>::Frag &a, f32x4 c)
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+template <int BL> struct AccOf { typedef f32x4 Type; };
+template <> struct AccOf<32> { typedef f32x16 Type; };
+
+template <typename T, int BL>
+__device__ __forceinline__ typename AccOf<BL>::Type mfma_step(const typename Elem<T>::Frag &b,
+                                                              const typename Elem<T>::Frag &a,
+                                                              typename AccOf<BL>::Type c)
 {
     if constexpr (std::is_same<T, float>::value) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_16x16x4f32(b[s], a[s], c, 0, 0, 0);
+        for (int s = 0; s < 4; ++s)
+            if constexpr (BL == 16)
+                c = __builtin_amdgcn_mfma_f32_16x16x4f32(b[s], a[s], c, 0, 0, 0);
+            else
+                c = __builtin_amdgcn_mfma_f32_32x32x2f32(b[s], a[s], c, 0, 0, 0);
         return c;
-    } else {
+    } else if constexpr (BL == 16) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
+    } else {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, a, c, 0, 0, 0);
     }
 }
 
@@ -235,20 +275,22 @@ __device__ __forceinline__ int64_t scan_tiles(const int *offsets, int groups, in
     return sum;  // inclusive
 }
 
-template <typename T, int BM, int BN, int WM, int WN, int NBUF, Layout LA, Layout LB, Ragged RG,
-          Epilogue EP, bool FAST>
-__global__ void __launch_bounds__(WM *WN * 64) tile_kernel(TileArgs g)
+template <typename T, int BM, int BN, int WM, int WN, int NBUF, int BL, int WPE, Layout LA,
+          Layout LB, Ragged RG, Epilogue EP, bool FAST>
+__global__ void __launch_bounds__(WM *WN * 64) __attribute__((amdgpu_waves_per_eu(WPE)))
+tile_kernel(TileArgs g)
 {
-    using SA = Slab<T, BM, LA>;
-    using SB = Slab<T, BN, LB>;
+    using SA = Slab<T, BM, LA, BL>;
+    using SB = Slab<T, BN, LB, BL>;
     using Frag = typename Elem<T>::Frag;
     constexpr int BK = Elem<T>::BK, EPC = Elem<T>::EPC, SZ = sizeof(T);
     constexpr int NW = WM * WN;
-    constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
+    constexpr int FM = BM / WM / BL, FN = BN / WN / BL;  // blocks of a wave
+    constexpr int KS = BL / 16;                           // steps per half slab
     constexpr int U = SA::UNITS + SB::UNITS;
     constexpr int LPW = (U + NW - 1) / NW;  // units a wave loads per slab (some twice, the same data)
     constexpr int STAGE = SA::BYTES + SB::BYTES;
-    static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0, "wave tiles are 16-aligned");
+    static_assert(BM % (BL * WM) == 0 && BN % (BL * WN) == 0, "wave tiles are whole blocks");
     static_assert(LPW * (NBUF - 1) <= 63, "loads in flight must fit the vmcnt field");
     static_assert(FAST || NBUF == 2, "the register path alternates two buffers");
     static_assert(EP != STATS || WN * BM * 8 <= NBUF * STAGE, "row statistics fit the ring");
@@ -256,7 +298,7 @@ __global__ void __launch_bounds__(WM *WN * 64) tile_kernel(TileArgs g)
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int l15 = lane & 15, lg = lane >> 4;
+    const int lrow = lane & (BL - 1), lg = lane / BL;
 
     // ---- which tile, of which group
     int tm, tn, group = 0, begin = 0, end = 0, m0;
@@ -346,30 +388,39 @@ __global__ void __launch_bounds__(WM *WN * 64) tile_kernel(TileArgs g)
     const int64_t step_b = LB == KC ? 128 : (int64_t)BK * g.ldb * SZ;
     const int slabs = (K + BK - 1) / BK;
 
-    f32x4 acc[FM][FN];
+    typename AccOf<BL>::Type acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int q = 0; q < BL * BL / 64; ++q) acc[i][j][q] = 0.f;
 
     const int wr = wave / WN, wc = wave % WN;
-    auto compute = [&](const char *buf) {
+    // Operand read r of half slab h: step by step, the wave's B blocks, then its A blocks.
+    constexpr int R1 = FM + FN, R = R1 * KS, M = FM * FN * KS;
+    auto read_op = [&](int r, const char *buf, int h, Frag(&a)[KS][FM], Frag(&b)[KS][FN]) {
+        const int k = r / R1, i = r % R1;
+        if (i < FN)
+            b[k][i] = SB::frag(buf + SA::BYTES, wc * FN + i, h * KS + k, lane);
+        else
+            a[k][i - FN] = SA::frag(buf, wr * FM + i - FN, h * KS + k, lane);
+    };
+    // The products of one half slab; hook(n) runs before the n-th of the M blocks.
+    auto products = [&](const Frag(&a)[KS][FM], const Frag(&b)[KS][FN], auto hook) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            Frag a[FM], b[FN];
-#pragma unroll
-            for (int j = 0; j < FN; ++j) b[j] = SB::frag(buf + SA::BYTES, wc * FN + j, h, lane);
-#pragma unroll
-            for (int i = 0; i < FM; ++i) a[i] = SA::frag(buf, wr * FM + i, h, lane);
+        for (int k = 0; k < KS; ++k)
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
-                for (int j = 0; j < FN; ++j) acc[i][j] = mfma_step<T>(b[j], a[i], acc[i][j]);
-        }
+                for (int j = 0; j < FN; ++j) {
+                    hook((k * FM + i) * FN + j);
+                    acc[i][j] = mfma_step<T, BL>(b[k][j], a[k][i], acc[i][j]);
+                }
     };
 
     // Unit i of this wave fills chunks 64 u .. 64 u + 63 of the slab, A's first.
-    int urow[LPW], uchunk[LPW], uat[LPW];
+    int uat[LPW];
     bool ua[LPW];
 #pragma unroll
     for (int i = 0; i < LPW; ++i) {
@@ -377,49 +428,104 @@ __global__ void __launch_bounds__(WM *WN * 64) tile_kernel(TileArgs g)
         if ((i + 1) * NW > U && u >= U) u -= U;  // another wave's unit: the same bytes again
         ua[i] = (i + 1) * NW <= SA::UNITS || ((i * NW < SA::UNITS || (i + 1) * NW > U) && u < SA::UNITS);
         uat[i] = u * 1024;
-        if (ua[i])
-            SA::slot(u * 64 + lane, urow[i], uchunk[i]);
-        else
-            SB::slot((u - SA::UNITS) * 64 + lane, urow[i], uchunk[i]);
     }
+    // Row and chunk that this lane fetches in unit i.
+    auto slot = [&](int i, int &row, int &chunk) {
+        if (ua[i])
+            SA::slot(uat[i] / 16 + lane, row, chunk);
+        else
+            SB::slot(uat[i] / 16 - SA::UNITS * 64 + lane, row, chunk);
+    };
 
     if constexpr (FAST) {
         uint32_t voff[LPW];
 #pragma unroll
-        for (int i = 0; i < LPW; ++i)
-            voff[i] = (uint32_t)urow[i] * (uint32_t)((ua[i] ? g.lda : g.ldb) * SZ) +
-                      (uint32_t)uchunk[i] * 16u;
+        for (int i = 0; i < LPW; ++i) {
+            int row, chunk;
+            slot(i, row, chunk);
+            voff[i] = (uint32_t)row * (uint32_t)((ua[i] ? g.lda : g.ldb) * SZ) + (uint32_t)chunk * 16u;
+        }
         const uint32_t base = (uint32_t)(uintptr_t)(lds_char *)lds;
         int kleft = K;  // of the next slab to issue
-        auto issue = [&](int buf) {
-            const u32x4 ra = descriptor(pa, LA == MC ? left_a : kleft > 0 ? left_a : 0);
-            const u32x4 rb = descriptor(pb, LB == MC ? left_b : kleft > 0 ? left_b : 0);
-            const uint32_t at = base + (uint32_t)buf * STAGE;
+        u32x4 ra, rb;
+        auto next_slab = [&]() {  // descriptors of the slab whose loads come next
+            ra = descriptor(pa, LA == MC ? left_a : kleft > 0 ? left_a : 0);
+            rb = descriptor(pb, LB == MC ? left_b : kleft > 0 ? left_b : 0);
+            if ((LA == KC || LB == KC) && kleft < BK) {
+                // The last slab is part full (those after it fetch nothing): lanes whose
+                // chunk lies past K leave the range of the descriptor for good.
+                asm volatile("; part-full slab");  // a branch, not a select in every slab
 #pragma unroll
-            for (int i = 0; i < LPW; ++i) {
-                uint32_t v = voff[i];
-                if ((ua[i] ? LA : LB) == KC && kleft < BK && uchunk[i] * EPC >= kleft) v = kOutside;
-                if (ua[i])
-                    load_slab16(ra, v, at + uat[i]);
-                else
-                    load_slab16(rb, v, at + uat[i]);
+                for (int i = 0; i < LPW; ++i) {
+                    int row, chunk;
+                    slot(i, row, chunk);
+                    if ((ua[i] ? LA : LB) == KC && chunk * EPC >= kleft) voff[i] = kOutside;
+                }
             }
+            // Wait states between a vector unit's write of a descriptor and its use.
+            asm volatile("s_nop 4" : "+s"(ra), "+s"(rb));
+        };
+        auto load = [&](int i, uint32_t at) {
+            if (ua[i])
+                load_slab16(ra, voff[i], at + uat[i]);
+            else
+                load_slab16(rb, voff[i], at + uat[i]);
+        };
+        auto advance = [&]() {
             pa += step_a;
             pb += step_b;
             left_a -= step_a;
             left_b -= step_b;
             kleft -= BK;
         };
+        // Half a slab ahead: while the products of one half run, the operands of the
+        // next are read.  In the middle of slab t every wave has read all of it, so
+        // one barrier there both frees its buffer for slab t + NBUF and, after the
+        // wait for this wave's loads, publishes slab t + 1.
 #pragma unroll
-        for (int i = 0; i < NBUF - 1; ++i) issue(i);
+        for (int b = 0; b < NBUF; ++b) {
+            next_slab();
+#pragma unroll
+            for (int i = 0; i < LPW; ++i) load(i, base + (uint32_t)b * STAGE);
+            advance();
+        }
+        wait_slab_barrier<LPW *(NBUF - 1)>();
+        Frag a0[KS][FM], b0[KS][FN], a1[KS][FM], b1[KS][FN];
+#pragma unroll
+        for (int r = 0; r < R; ++r) read_op(r, lds, 0, a0, b0);
         int buf = 0;
         for (int t = 0; t < slabs; ++t) {
-            // Slab t has landed; every wave is done with slab t - 1, whose buffer
-            // slab t + NBUF - 1 now fills.
+            const char *here = lds + buf * STAGE;
+            products(a0, b0, [&](int n) {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    if (n == r * M / (2 * R)) {
+                        read_op(r, here, 1, a1, b1);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+            });
+            __builtin_amdgcn_sched_barrier(0);
             wait_slab_barrier<LPW *(NBUF - 2)>();
-            issue(buf == 0 ? NBUF - 1 : buf - 1);
-            compute(lds + buf * STAGE);
+            const uint32_t at = base + (uint32_t)buf * STAGE;
             buf = buf + 1 == NBUF ? 0 : buf + 1;
+            const char *there = lds + buf * STAGE;
+            next_slab();
+            products(a1, b1, [&](int n) {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    if (n == r * M / (2 * R)) {
+                        read_op(r, there, 0, a0, b0);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+#pragma unroll
+                for (int i = 0; i < LPW; ++i)
+                    if (n == i * M / LPW) {
+                        load(i, at);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+            });
+            __builtin_amdgcn_sched_barrier(0);
+            advance();
         }
         wait_slab_barrier<0>();  // nothing may land in LDS any more
     } else {
@@ -427,11 +533,13 @@ __global__ void __launch_bounds__(WM *WN * 64) tile_kernel(TileArgs g)
         auto fetch = [&](int t) {
 #pragma unroll
             for (int i = 0; i < LPW; ++i) {
+                int row, chunk;
+                slot(i, row, chunk);
                 const bool kc = (ua[i] ? LA : LB) == KC;
                 const int64_t ld = ua[i] ? g.lda : g.ldb;
                 const int rows = ua[i] ? a_rows : b_rows;
-                const int r = kc ? urow[i] : t * BK + urow[i];
-                const int c = kc ? t * BK + uchunk[i] * EPC : uchunk[i] * EPC;
+                const int r = kc ? row : t * BK + row;
+                const int c = kc ? t * BK + chunk * EPC : chunk * EPC;
                 // First value outside, along the contiguous index.
                 const int lim = kc ? K : ua[i] ? g.M - m0 : g.N - n0;
                 const T *p = reinterpret_cast<const T *>(ua[i] ? pa : pb) + (int64_t)r * ld + c;
@@ -464,7 +572,13 @@ __global__ void __launch_bounds__(WM *WN * 64) tile_kernel(TileArgs g)
         __syncthreads();
         for (int t = 0; t < slabs; ++t) {
             if (t + 1 < slabs) fetch(t + 1);
-            compute(lds + (t & 1) * STAGE);
+            Frag a[KS][FM], b[KS][FN];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) read_op(r, lds + (t & 1) * STAGE, h, a, b);
+                products(a, b, [](int) {});
+            }
             if (t + 1 < slabs) put((t + 1) & 1);
             __syncthreads();
         }
@@ -472,137 +586,179 @@ __global__ void __launch_bounds__(WM *WN * 64) tile_kernel(TileArgs g)
 
     // ---- epilogue
     const int row_end = RG == ROWS ? end - begin : g.M;
-    const int mw = m0 + wr * (BM / WM) + l15;       // row of block 0
-    const int nw = n0 + wc * (BN / WN) + 4 * lg;    // first of its four columns in block 0
+    constexpr int GR = BL * BL / 256;               // groups of four columns in a block
+    const int mw = m0 + wr * (BM / WM) + lrow;      // row of block 0
+    const int nw = n0 + wc * (BN / WN) + 4 * lg;    // first column of group 0, block 0
+    // Group u of the wave's FN * GR: its first column, and its values in row block i.
+    auto column = [&](int u) { return nw + BL * (u / GR) + 8 * (u % GR); };
+    auto value = [&](int i, int u, int q) { return acc[i][u / GR][4 * (u % GR) + q]; };
+    typedef T Vec __attribute__((ext_vector_type(4)));
+    // A tile inside C with vector stores takes copies without per-column tests.
+    const bool whole = n0 + BN <= g.N && g.vec_c;
     if constexpr (EP == STORE) {
         T *C = static_cast<T *>(g.C);
         if constexpr (RG == SUM) C += group * g.group_stride;
         const float alpha = g.alpha, beta = g.beta;
+        auto store = [&](auto inside, auto scaled) {
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            const int m = mw + 16 * i;
-            if (m >= row_end) continue;
-            T *crow = C + (int64_t)(row0 + m) * g.ldc;
+            for (int i = 0; i < FM; ++i) {
+                __builtin_amdgcn_sched_barrier(0);  // one row block at a time: fewer registers
+                const int m = mw + BL * i;
+                if (m >= row_end) continue;
+                T *crow = C + (int64_t)(row0 + m) * g.ldc;
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const int n = nw + 16 * j;
-                if (n >= g.N) continue;
-                float v[4];
+                for (int u = 0; u < FN * GR; ++u) {
+                    const int n = column(u);
+                    float v[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = alpha * acc[i][j][q];
-                if (g.vec_c && n + 4 <= g.N) {
-                    typedef T Vec __attribute__((ext_vector_type(4)));
-                    Vec *p = reinterpret_cast<Vec *>(crow + n);
-                    if (beta != 0.f) {
-                        const Vec old = *p;
+                    for (int q = 0; q < 4; ++q) v[q] = alpha * value(i, u, q);
+                    if (decltype(inside)::value || (g.vec_c && n + 4 <= g.N)) {
+                        Vec *p = reinterpret_cast<Vec *>(crow + n);
+                        if constexpr (decltype(scaled)::value) {
+                            const Vec old = *p;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) v[q] = fmaf(beta, (float)old[q], v[q]);
-                    }
-                    Vec out;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) out[q] = (T)v[q];
-                    *p = out;
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (n + q < g.N) {
-                            if (beta != 0.f) v[q] = fmaf(beta, (float)crow[n + q], v[q]);
-                            crow[n + q] = (T)v[q];
+                            for (int q = 0; q < 4; ++q) v[q] = fmaf(beta, (float)old[q], v[q]);
                         }
+                        Vec out;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) out[q] = (T)v[q];
+                        *p = out;
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (n + q < g.N) {
+                                if constexpr (decltype(scaled)::value)
+                                    v[q] = fmaf(beta, (float)crow[n + q], v[q]);
+                                crow[n + q] = (T)v[q];
+                            }
+                    }
                 }
             }
-        }
+        };
+        if (beta != 0.f)
+            store(std::false_type{}, std::true_type{});
+        else if (whole)
+            store(std::true_type{}, std::false_type{});
+        else
+            store(std::false_type{}, std::false_type{});
     } else if constexpr (EP == PART) {
         float *C = static_cast<float *>(g.C) + blockIdx.z * g.slice_stride;
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
-            const int m = mw + 16 * i;
+            __builtin_amdgcn_sched_barrier(0);
+            const int m = mw + BL * i;
             if (m >= g.M) continue;
             float *crow = C + (int64_t)m * g.ldc;
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const int n = nw + 16 * j;
-                if (n >= g.N) continue;
-                if (g.vec_c && n + 4 <= g.N) {
+            for (int u = 0; u < FN * GR; ++u) {
+                const int n = column(u);
+                if (whole || (g.vec_c && n + 4 <= g.N)) {
                     f32x4 *p = reinterpret_cast<f32x4 *>(crow + n);
-                    *p = g.accumulate ? acc[i][j] + *p : acc[i][j];
+                    f32x4 v;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] = value(i, u, q);
+                    *p = g.accumulate ? v + *p : v;
                 } else {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         if (n + q < g.N)
-                            crow[n + q] = g.accumulate ? acc[i][j][q] + crow[n + q] : acc[i][j][q];
+                            crow[n + q] =
+                                g.accumulate ? value(i, u, q) + crow[n + q] : value(i, u, q);
                 }
             }
         }
     } else if constexpr (EP == GRAD) {
+        // Every value of the tile becomes w exp(z - lse), as 2^(z log2 e - lse log2 e): one
+        // fma and one instruction for the power.  For fp32 the rounding of lse log2 e
+        // is carried along (low); bf16's own rounding hides it.
         T *C = static_cast<T *>(g.C);
-        // Columns up to the next multiple of 8 are written (as zero past N), so
-        // that whole chunks can be read back.
-        const int ncols = (g.N + 7) & ~7;
+        auto store = [&](auto inside) {
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            const int m = mw + 16 * i;
-            if (m >= g.M) continue;
-            const int64_t target = g.targets[m];
-            const float lse = g.lse[m], w = g.dloss[m];
-            const bool counts = target >= 0 && target < g.vocab;
-            const int at = counts ? (int)target - g.col0 : -1;  // past the piece: no column's
-            T *crow = C + (int64_t)m * g.ldc;
+            for (int i = 0; i < FM; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                const int m = mw + BL * i;
+                if (m >= g.M) continue;
+                const int64_t target = g.targets[m];
+                const float w = g.dloss[m], lse = g.lse[m];
+                const float high = lse * kLog2e, low = fmaf(lse, kLog2e, -high);
+                const bool counts = target >= 0 && target < g.vocab;
+                const int at = counts ? (int)target - g.col0 : INT32_MIN;
+                T *crow = C + (int64_t)m * g.ldc;
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const int n = nw + 16 * j;
-                if (n >= ncols) continue;
-                typedef T Vec __attribute__((ext_vector_type(4)));
-                Vec out;
+                for (int u = 0; u < FN * GR; ++u) {
+                    const int n = column(u);
+                    float v[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float z = acc[i][j][q] - lse;
-                    float p;
-                    if constexpr (std::is_same<T, float>::value)
-                        p = expf(z);
-                    else
-                        p = __expf(z);
-                    if (n + q == at) p -= 1.f;
-                    out[q] = (T)(counts && n + q < g.N ? p * w : 0.f);
+                    for (int q = 0; q < 4; ++q) {
+                        float e = fmaf(value(i, u, q), kLog2e, -high);
+                        if constexpr (std::is_same<T, float>::value) e -= low;
+                        v[q] = __builtin_amdgcn_exp2f(e);
+                    }
+                    if ((unsigned)(at - n) < 4u)  // one lane of the row, in one tile
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) v[q] -= at - n == q ? 1.f : 0.f;
+                    Vec out;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        out[q] = (T)(counts && (decltype(inside)::value || n + q < g.N) ? v[q] * w
+                                                                                       : 0.f);
+                    // Columns up to the next multiple of 8 are written, as zero past N, so
+                    // that whole chunks can be read back.
+                    if (decltype(inside)::value || n < ((g.N + 7) & ~7))
+                        *reinterpret_cast<Vec *>(crow + n) = out;
                 }
-                *reinterpret_cast<Vec *>(crow + n) = out;
             }
-        }
+        };
+        if (n0 + BN <= g.N)
+            store(std::true_type{});
+        else
+            store(std::false_type{});
     }
     if constexpr (EP == STATS) {
-        // Row maximum and sum over this wave's columns, then over the waves of
-        // the tile through LDS.  The sums are of exponentials of the distance to
-        // the running maximum, so nothing overflows.
+        // Row maximum and sum over this wave's columns, then over the waves of the
+        // tile through LDS, in powers of two: the sum is of 2^(z log2 e - top), top the
+        // largest z log2 e of the row rounded, so nothing overflows and the pair (top,
+        // sum) stands for top + log2(sum) without the rounding of top.
         float *sm = reinterpret_cast<float *>(lds), *ss = sm + WN * BM;
+        if (n0 + BN > g.N) {  // columns past N never count
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int u = 0; u < FN * GR; ++u)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (column(u) + q >= g.N) acc[i][u / GR][4 * (u % GR) + q] = -INFINITY;
+        }
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
-            const int m = mw + 16 * i;
+            __builtin_amdgcn_sched_barrier(0);
+            const int m = mw + BL * i;
             const int64_t target = m < g.M ? g.targets[m] : -1;
+            const int at = target >= 0 && target < g.N ? (int)target : INT32_MIN;
             float top = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
+            for (int u = 0; u < FN * GR; ++u) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int n = nw + 16 * j + q;
-                    if (n >= g.N) continue;
-                    top = fmaxf(top, acc[i][j][q]);
-                    if (target == n) g.target_value[m] = acc[i][j][q];
-                }
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
+                for (int q = 0; q < 4; ++q) top = fmaxf(top, value(i, u, q));
+                if ((unsigned)(at - column(u)) < 4u)  // one lane of the row, in one tile
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (at - column(u) == q) g.target_value[m] = value(i, u, q);
+            }
+#pragma unroll
+            for (int d = BL; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+            top *= kLog2e;
             // Without a finite maximum the distance is taken to zero: infinities and
             // NaN then reach the sum as they are.
             const float from = isfinite(top) ? top : 0.f;
             float sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
+            for (int u = 0; u < FN * GR; ++u)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int n = nw + 16 * j + q;
-                    if (n < g.N) sum += expf(acc[i][j][q] - from);
-                }
-            sum += __shfl_xor(sum, 16);
-            sum += __shfl_xor(sum, 32);
+                for (int q = 0; q < 4; ++q)
+                    sum += __builtin_amdgcn_exp2f(fmaf(value(i, u, q), kLog2e, -from));
+#pragma unroll
+            for (int d = BL; d < 64; d *= 2) sum += __shfl_xor(sum, d);
             if (lg == 0) {
                 sm[wc * BM + m - m0] = top;
                 ss[wc * BM + m - m0] = sum;
@@ -613,13 +769,7 @@ __global__ void __launch_bounds__(WM *WN * 64) tile_kernel(TileArgs g)
             if (m0 + r >= g.M) continue;
             float top = -INFINITY, sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < WN; ++w) top = fmaxf(top, sm[w * BM + r]);
-            const float from = isfinite(top) ? top : 0.f;
-#pragma unroll
-            for (int w = 0; w < WN; ++w) {
-                const float t = sm[w * BM + r];
-                sum += ss[w * BM + r] * (t == top || !isfinite(t) ? 1.f : expf(t - from));
-            }
+            for (int w = 0; w < WN; ++w) join_sums(top, sum, sm[w * BM + r], ss[w * BM + r]);
             f32x2 *part = reinterpret_cast<f32x2 *>(g.parts) +
                           ((int64_t)(m0 + r) * ((g.N + BN - 1) / BN) + tn);
             *part = f32x2{top, sum};

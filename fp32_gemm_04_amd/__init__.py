@@ -362,14 +362,17 @@ _TYPES = {torch.float32: SGEMM_TYPE_F32, torch.bfloat16: SGEMM_TYPE_BF16}
 
 def _operand(t, name, dtype, device, dim=2, rows=None, cols=None):
     """Checks a tensor of rows with unit column stride; returns its leading dimension."""
-    if t.dtype != dtype or t.dim() != dim:
+    shape = t.shape
+    if t.dtype != dtype or len(shape) != dim:
         raise TypeError("%s must be a %d-D %s tensor, not %d-D %s"
-                        % (name, dim, dtype, t.dim(), t.dtype))
-    if t.device != device or device.type != "cuda":
+                        % (name, dim, dtype, len(shape), t.dtype))
+    if not t.is_cuda or t.device != device:
         raise ValueError("%s is on %s: every operand must be on one GPU" % (name, t.device))
-    r, c = t.shape[-2], t.shape[-1]
+    r, c = shape[-2], shape[-1]
     if (rows is not None and r != rows) or (cols is not None and c != cols):
-        raise ValueError("%s is %s: %s x %s is wanted" % (name, tuple(t.shape), rows, cols))
+        raise ValueError("%s is %s: %s x %s is wanted" % (name, tuple(shape), rows, cols))
+    if t.is_contiguous():
+        return c if c > 1 else 1
     if t.numel() == 0:
         return max(1, c)
     if c > 1 and t.stride(-1) != 1:
@@ -398,15 +401,23 @@ def _type_of(t, name):
     return _TYPES[t.dtype]
 
 
+_current_stream = torch._C._cuda_getCurrentRawStream if hasattr(
+    torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _run(call, device, stream, body):
     """body(stream handle) with ``device`` current and, where a stream is given,
     with it current too, so that what body allocates belongs to that stream."""
-    with torch.cuda.device(device):
-        if stream is None:
-            rc = body(torch.cuda.current_stream().cuda_stream)
-        else:
-            with torch.cuda.stream(stream):
-                rc = body(stream.cuda_stream)
+    if stream is None and device.index == torch.cuda.current_device():
+        rc = body(_current_stream(device.index))  # the usual case, without context managers
+    else:
+        with torch.cuda.device(device):
+            if stream is None:
+                rc = body(_current_stream(device.index))
+            else:
+                with torch.cuda.stream(stream):
+                    rc = body(stream.cuda_stream)
     if rc != 0:
         raise SgemmError(rc, call)
 

@@ -3,6 +3,7 @@
 // here allocates, frees, copies or synchronises.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <climits>
 #include <cstdint>
 
@@ -16,6 +17,25 @@ namespace {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool aligned(const void *p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+// Compute units of the current device (cached; 0 on failure, with the error in *rc).
+int compute_units(int *rc)
+{
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e == hipSuccess && dev >= 0 && dev < 64) {
+        int n = cache[dev].load(std::memory_order_relaxed);
+        if (n > 0) return n;
+        e = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev);
+        if (e == hipSuccess && n > 0) {
+            cache[dev].store(n, std::memory_order_relaxed);
+            return n;
+        }
+    }
+    *rc = e == hipSuccess ? (int)hipErrorInvalidDevice : (int)e;
+    return 0;
+}
+
 struct Form {
     int rt, nt;
 };
@@ -23,10 +43,12 @@ struct Form {
 template <typename T, int BLOCK, bool ALIGNED>
 Q4Fn kernel_of(Form f)
 {
-    if (f.rt == 1) return f.nt == 1 ? q4_kernel<T, BLOCK, 1, 1, ALIGNED>
-                                    : q4_kernel<T, BLOCK, 1, 2, ALIGNED>;
-    if (f.rt == 2) return q4_kernel<T, BLOCK, 2, 2, ALIGNED>;
-    return q4_kernel<T, BLOCK, 4, 2, ALIGNED>;
+    switch (f.rt * 8 + f.nt) {
+    case 9: return q4_kernel<T, BLOCK, 1, 1, ALIGNED>;
+    case 10: return q4_kernel<T, BLOCK, 1, 2, ALIGNED>;
+    case 18: return q4_kernel<T, BLOCK, 2, 2, ALIGNED>;
+    default: return q4_kernel<T, BLOCK, 4, 2, ALIGNED>;
+    }
 }
 
 template <typename T>
@@ -79,33 +101,52 @@ extern "C" int sgemm_q4_matvec(int type, int groups, int rows, int N, int K, int
 
     const int parts = type == SGEMM_TYPE_F32 ? 3 : 1;
     const int used = groups < rows ? groups : rows;
-    const int64_t places = ceil_div(rows, used) * parts;  // of a group, on average
-    const Form f = places > 32 ? Form{4, 2} : places > 16 ? Form{2, 2} : Form{1, N >= 8192 ? 2 : 1};
+    const int64_t mean = ceil_div(rows, used);  // rows of a group
+    // Rows per pass: no more than a group is likely to have, so that more of K is staged
+    // at once.
+    const int64_t likely = offsets ? 2 * mean : rows;
+    const int pass = likely < 64 ? (int)likely : 64;
+    int rc = 0;
+    const int cus = compute_units(&rc);
+    if (cus == 0) return rc;
+    // The more columns a workgroup takes (NT per wave, wn waves), the less often x is
+    // staged and read: until four workgroups remain per compute unit, or 1.5 where
+    // staging x (two bytes a part, against half a byte a weight) would outweigh the
+    // weights.
+    Form f = {pass > 32 ? 4 : pass > 16 ? 2 : 1, pass > 16 ? 2 : 1};
+    const int64_t tiles = used * ceil_div(N, 16);
+    int wn = 1;
+    while (wn < kWaves) {
+        const int cols = 16 * f.nt * wn;
+        const int64_t left = tiles / (f.nt * wn * 2);
+        if (left < (cols < 8 * pass * parts ? cus * 3 / 2 : 4 * cus)) break;
+        if (f.nt == 1)
+            f.nt = 2;
+        else
+            wn *= 2;
+    }
     Q4Args a = {};
     a.X = X, a.Q = Q, a.S = S, a.Z = Z, a.Y = Y, a.offsets = offsets;
     a.ldx = ldx, a.ldy = ldy;
     a.q_stride = (int64_t)N * (K / 2);
     a.s_stride = (int64_t)N * ceil_div(K, block);
     a.rows = rows, a.N = N, a.K = K;
-    a.wn = f.rt == 1 ? 1 : 2;
-    // Rows per pass: what the tiles hold, but no more places than a group is likely to
-    // need, so that more of K is staged at once.
-    const int64_t likely = offsets ? 2 * ceil_div(rows, used) : rows;
-    const int hold = f.rt * 16 / parts;
-    a.pass = likely < hold ? (int)likely : hold;
-    const int wide = a.pass * parts;
-    int64_t slab = (kSlab / wide - 16) / 2 / 128 * 128;
+    a.wn = wn;
+    a.pass = pass;
+    // A row takes two bytes a part and k, four a block (at most 1/8 byte a k), and 16 a part.
+    int64_t slab = (kSlab / pass - 16 * parts) * 8 / (16 * parts + 1) / 128 * 128;
     const int64_t step = 128 * kWaves / a.wn;  // one chunk for every wave
     if (slab > step) slab = slab / step * step;
     const int64_t all = ceil_div(K, 128) * 128;
     a.slab = (int)(slab < all ? slab : all > 0 ? all : 128);
     a.vec_x = aligned(X, 16) && (int64_t)ldx * size % 16 == 0;
-    const bool al = K % 32 == 0 && aligned(Q, 16);
+    const int nb = 128 / block;
+    const bool al = K % 128 == 0 && aligned(Q, 16) && aligned(S, nb * size) && aligned(Z, nb);
     const Q4Fn fn = type == SGEMM_TYPE_BF16 ? kernel_for<bf16>(block, al, f)
                                             : kernel_for<float>(block, al, f);
     const int cols = a.wn * f.nt * 16;
-    const int staged = wide * (a.slab * 2 + 16);
-    const int sums = kWaves / a.wn * f.rt * 16 * cols * 4;
+    const int staged = pass * (parts * (a.slab * 2 + 16) + a.slab / block * 4);
+    const int sums = kWaves / a.wn * pass * cols * 4;
     const int64_t blocks = ceil_div(N, cols);
     fn<<<dim3((unsigned)blocks, (unsigned)groups), dim3(kWaves * 64),
          staged > sums ? staged : sums, stream>>>(a);

@@ -9,14 +9,16 @@
 // one and-or each: nibble i and nibble i + 4 of a 32-bit word, moved to bits 3..6
 // of the halves and or'ed into 0x4180 (16.0, whose last four leading mantissa bits
 // they are), read 16 + q exactly.  So the accumulator of one block holds
-// sum x (16 + q), and one more product by a vector of ones holds sum x:
-//   y += s (sum x (16 + q) - (16 + z) sum x).
-// The constant is small beside q, so the difference loses about two bits of
-// the fp32 sum.
+// sum x (16 + q), and with the sums of x over each block, which staging x leaves in LDS,
+//   y += s sum x (16 + q) - s (16 + z) sum x,
+// whose second part is a product over blocks of its own (v_mfma_f32_16x16x4_f32, a
+// chunk's blocks in one instruction), so that the vector unit is left with the
+// unpacking and one fma per block and sum.  16 is small beside q, so the
+// difference loses about two bits of the fp32 sum.
 //
 // fp32 rows are split into three bf16 rows that add up to them exactly (8 + 8 +
-// 8 leading bits), which take three of the 16 places; the products by 16 + q
-// are exact in fp32, so an fp32 row loses nothing to bf16.
+// 8 leading bits) and go through the matrix cores one after another into the same
+// sums; the products by 16 + q are exact in fp32, so an fp32 row loses nothing to bf16.
 //
 // A chunk is 128 weights along K: lane group g = lane / 16 holds weights
 // 32 g .. 32 g + 31 of its n.  With blocks of 128 an instruction may take any 32 of
@@ -53,7 +55,7 @@ struct Q4Args {
     int rows, N, K;
     int wn;             // waves along n (a power of two, at most 8)
     int slab;           // k per slab, a multiple of 128
-    int pass;           // rows per pass, at most pass_rows<T>(RT)
+    int pass;           // rows per pass, at most 16 RT
     int vec_x;          // rows of X take 16-byte loads
 };
 typedef void (*Q4Fn)(Q4Args);
@@ -61,21 +63,17 @@ typedef void (*Q4Fn)(Q4Args);
 template <typename T> struct Parts { static constexpr int value = 1; };
 template <> struct Parts<float> { static constexpr int value = 3; };
 
-// Rows that RT tiles of 16 places hold.
-template <typename T> constexpr int pass_rows(int rt) { return rt * 16 / Parts<T>::value; }
-
-__device__ __forceinline__ bf16x8 unpack(uint32_t u)
+// mask 0x00780078 and sixteen 0x41804180, kept in registers: as literals they would
+// cost an instruction more each.
+__device__ __forceinline__ bf16x8 unpack(uint32_t u, uint32_t mask, uint32_t sixteen)
 {
     u32x4 v;
-    v[0] = ((u << 3) & 0x00780078u) | 0x41804180u;
-    v[1] = ((u >> 1) & 0x00780078u) | 0x41804180u;
-    v[2] = ((u >> 5) & 0x00780078u) | 0x41804180u;
-    v[3] = ((u >> 9) & 0x00780078u) | 0x41804180u;
+    v[0] = ((u << 3) & mask) | sixteen;
+    v[1] = ((u >> 1) & mask) | sixteen;
+    v[2] = ((u >> 5) & mask) | sixteen;
+    v[3] = ((u >> 9) & mask) | sixteen;
     return __builtin_bit_cast(bf16x8, v);
 }
-
-// Place of value i of eight in the order of the unpacked pairs: 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ constexpr int place(int i) { return i < 4 ? 2 * i : 2 * (i - 4) + 1; }
 
 // The 4 x 4 exchange: lane group g's word j becomes lane group j's word g.
 __device__ __forceinline__ u32x4 exchange(u32x4 v)
@@ -106,15 +104,16 @@ __device__ __forceinline__ void load8(const T *row, int k, int K, bool vec, floa
     }
 }
 
-__device__ __forceinline__ uint16_t top_half(float v)
-{
-    return (uint16_t)(__builtin_bit_cast(uint32_t, v) >> 16);
-}
+// Chunks of weights a wave keeps in flight: 4 KB, which with 16 waves on a compute
+// unit covers the latency of memory at its full rate.
+constexpr int ring_depth(int nt) { return nt == 1 ? 4 : 2; }
 
 template <typename T, int BLOCK, int RT, int NT, bool ALIGNED>
-__global__ void __launch_bounds__(kWaves * 64) q4_kernel(Q4Args g)
+__global__ void __launch_bounds__(kWaves * 64)
+__attribute__((amdgpu_waves_per_eu(RT * NT <= 4 ? 4 : 2))) q4_kernel(Q4Args g)
 {
-    constexpr int P = Parts<T>::value;
+    constexpr int D = ring_depth(NT);
+    constexpr int P = Parts<T>::value;           // bf16 parts of a value
     constexpr int NB = 128 / BLOCK;              // blocks per chunk
     extern __shared__ __attribute__((aligned(16))) char lds[];
 
@@ -132,60 +131,70 @@ __global__ void __launch_bounds__(kWaves * 64) q4_kernel(Q4Args g)
     const int nblk = (g.K + BLOCK - 1) / BLOCK;
     const int chunks = (g.K + 127) / 128;
     const int row_bytes = g.K / 2;
-    const uint8_t *Q = g.Q + group * g.q_stride;
-    const T *S = static_cast<const T *>(g.S) + group * g.s_stride;
-    const uint8_t *Z = g.Z ? g.Z + group * g.s_stride : nullptr;
-
-    // This lane's weight rows (past N: the last one, whose outputs are not stored).
-    const uint8_t *qrow[NT];
-    const T *srow[NT];
-    const uint8_t *zrow[NT];
+    // This lane's weight rows (past N: the last one, whose outputs are not stored), as
+    // offsets from the workgroup's first row: bytes of Q, blocks of S and Z.
+    const uint8_t *Q = g.Q + group * g.q_stride + (int64_t)n_wg * row_bytes;
+    const T *S = static_cast<const T *>(g.S) + group * g.s_stride + (int64_t)n_wg * nblk;
+    const uint8_t *Z = g.Z ? g.Z + group * g.s_stride + (int64_t)n_wg * nblk : nullptr;
+    uint32_t qoff[NT], soff[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        int n = n_wg + (wn * NT + t) * 16 + l15;
-        n = n < g.N ? n : g.N - 1;
-        qrow[t] = Q + (int64_t)n * row_bytes;
-        srow[t] = S + (int64_t)n * nblk;
-        zrow[t] = Z ? Z + (int64_t)n * nblk : nullptr;
+        int n = (wn * NT + t) * 16 + l15;
+        n = n_wg + n < g.N ? n : g.N - 1 - n_wg;
+        qoff[t] = (uint32_t)n * (uint32_t)row_bytes + (uint32_t)lg * 16u;
+        soff[t] = (uint32_t)n * (uint32_t)nblk;
     }
 
+    typedef T Scales __attribute__((ext_vector_type(NB)));
+    typedef uint8_t Zeros __attribute__((ext_vector_type(NB)));
     struct Chunk {
         u32x4 q[NT];
-        float s[NT][NB], z[NT][NB];
+        Scales s[NT];
+        Zeros z[NT];
     };
     auto fetch = [&](int c, Chunk &h) {
-        const int at = c * 64 + lg * 16;  // byte of the row
+        const uint8_t *qc = Q + (int64_t)c * 64;
+        const T *sc = S + (int64_t)c * NB;
+        const uint8_t *zc = Z + (Z ? (int64_t)c * NB : 0);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const uint8_t *p = qrow[t] + at;
-            if (at + 16 <= row_bytes) {
-                if constexpr (ALIGNED)
-                    h.q[t] = *reinterpret_cast<const u32x4 *>(p);
-                else
-                    __builtin_memcpy(&h.q[t], p, 16);
+            if constexpr (ALIGNED) {  // K a multiple of 128: whole chunks, whole vectors of scales
+                h.q[t] = *reinterpret_cast<const u32x4 *>(qc + qoff[t]);
+                h.s[t] = *reinterpret_cast<const Scales *>(sc + soff[t]);
+                if (Z) h.z[t] = *reinterpret_cast<const Zeros *>(zc + soff[t]);
             } else {
-                union {
-                    u32x4 v;
-                    uint8_t b[16];
-                } x;
-                x.v = u32x4{0, 0, 0, 0};
+                const int at = c * 64 + lg * 16;  // byte of the row
+                if (at + 16 <= row_bytes) {
+                    __builtin_memcpy(&h.q[t], qc + qoff[t], 16);
+                } else {
+                    union {
+                        u32x4 v;
+                        uint8_t b[16];
+                    } x;
+                    x.v = u32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (at + j < row_bytes) x.b[j] = p[j];
-                h.q[t] = x.v;
-            }
+                    for (int j = 0; j < 16; ++j)
+                        if (at + j < row_bytes) x.b[j] = qc[qoff[t] + j];
+                    h.q[t] = x.v;
+                }
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                // A block past the last holds only zeros of x: any scale will do.
-                int blk = c * NB + b;
-                blk = blk < nblk ? blk : nblk - 1;
-                h.s[t][b] = (float)srow[t][blk];
-                h.z[t][b] = zrow[t] ? (float)zrow[t][blk] : 8.f;
+                for (int b = 0; b < NB; ++b) {
+                    // A block past the last holds only zeros of x: any scale will do.
+                    int blk = c * NB + b;
+                    blk = blk < nblk ? blk : nblk - 1;
+                    h.s[t][b] = S[soff[t] + blk];
+                    if (Z) h.z[t][b] = Z[soff[t] + blk];
+                }
             }
         }
     };
 
     const int pitch = g.slab * 2 + 16;  // bytes of a staged row: rows start in different banks
+    const int part = g.pass * pitch;    // bytes of a part of x
+    float *xsum = reinterpret_cast<float *>(lds + P * part);  // [block of the slab][row]
+    uint32_t mask = 0x00780078u, sixteen = 0x41804180u;
+    asm("" : "+s"(mask));
+    asm("" : "+v"(sixteen));
     for (int r0 = begin; r0 < end; r0 += g.pass) {
         const int rows = end - r0 < g.pass ? end - r0 : g.pass;
         f32x4 total[RT][NT];
@@ -195,19 +204,18 @@ __global__ void __launch_bounds__(kWaves * 64) q4_kernel(Q4Args g)
             for (int t = 0; t < NT; ++t) total[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
         // The staged row each lane reads (places past the last row: any row; their
         // sums are not stored).
-        int place_row[RT];
+        int my_row[RT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const int p = 16 * i + l15;
-            place_row[i] = p < rows * P ? p : rows * P - 1;
-        }
+        for (int i = 0; i < RT; ++i) my_row[i] = 16 * i + l15 < rows ? 16 * i + l15 : rows - 1;
 
         for (int k0 = 0; k0 < g.K; k0 += g.slab) {
             const int kn = g.K - k0 < g.slab ? g.K - k0 : g.slab;
             const int c0 = k0 / 128, c1 = c0 + (kn + 127) / 128;
-            Chunk cur, nxt;
+            Chunk ring[D];
             const int first = c0 + wk;
-            if (first < c1) fetch(first, cur);
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+                if (first + d * wk_count < c1) fetch(first + d * wk_count, ring[d]);
             __syncthreads();  // the slab (or the sums) before this one have been read
             const int octets = (c1 - c0) * 16;
             for (int i = threadIdx.x; i < rows * octets; i += kWaves * 64) {
@@ -215,91 +223,115 @@ __global__ void __launch_bounds__(kWaves * 64) q4_kernel(Q4Args g)
                 float v[8];
                 load8(static_cast<const T *>(g.X) + (int64_t)(r0 + r) * g.ldx, k0 + 8 * o, g.K,
                       g.vec_x, v);
-                union {
-                    u32x4 v;
-                    uint16_t h[8];
-                } x[P];
+                float sum = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if constexpr (P == 1) {
-                        x[0].h[place(j)] = top_half(v[j]);
-                    } else {
-                        // Leading 8 bits, the next 8 and the rest, each exact; an infinity
-                        // or NaN stays whole in the first.
-                        float a = v[j];
-                        const bool fin = isfinite(a);
-                        if (!fin) a = isinf(a) ? a : __builtin_nanf("");
-                        const uint16_t h0 = top_half(a);
-                        const float r1 =
-                            fin ? a - __builtin_bit_cast(float, (uint32_t)h0 << 16) : 0.f;
-                        const uint16_t h1 = top_half(r1);
-                        const float r2 = r1 - __builtin_bit_cast(float, (uint32_t)h1 << 16);
-                        x[0].h[place(j)] = h0;
-                        x[1].h[place(j)] = h1;
-                        x[2].h[place(j)] = top_half(r2);
+                for (int j = 0; j < 8; ++j) sum += v[j];
+                // Each part in turn: the leading 16 bits of what is left, and the rest
+                // (exact; an infinity leaves a NaN, a NaN stays one).
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    u32x4 out;
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {  // values d and d + 4 share a word
+                        const uint32_t lo = __builtin_bit_cast(uint32_t, v[d]);
+                        const uint32_t hi = __builtin_bit_cast(uint32_t, v[d + 4]);
+                        out[d] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+                        if (p + 1 < P) {
+                            v[d] -= __builtin_bit_cast(float, lo & 0xffff0000u);
+                            v[d + 4] -= __builtin_bit_cast(float, hi & 0xffff0000u);
+                        }
                     }
+                    *reinterpret_cast<u32x4 *>(lds + p * part + r * pitch + o * 16) = out;
                 }
+                // The BLOCK / 8 lanes of a block are neighbours, all of them here.
 #pragma unroll
-                for (int p = 0; p < P; ++p)
-                    *reinterpret_cast<u32x4 *>(lds + (r * P + p) * pitch + o * 16) = x[p].v;
+                for (int d = 1; d < BLOCK / 8; d *= 2) sum += __shfl_xor(sum, d);
+                if (o % (BLOCK / 8) == 0) xsum[o / (BLOCK / 8) * g.pass + r] = sum;
             }
             __syncthreads();
 
-            for (int c = first; c < c1; c += wk_count) {
-                if (c + wk_count < c1) fetch(c + wk_count, nxt);
+            auto chunk = [&](int c, const Chunk &h) {
+                const char *xs = lds + (c - c0) * 256;
                 u32x4 w[NT];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) w[t] = BLOCK == 128 ? cur.q[t] : exchange(cur.q[t]);
-                const u32x4 one_bits = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-                const bf16x8 ones = __builtin_bit_cast(bf16x8, one_bits);
+                for (int t = 0; t < NT; ++t) w[t] = BLOCK == 128 ? h.q[t] : exchange(h.q[t]);
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    f32x4 sum[RT], acc[RT][NT];
+                    __builtin_amdgcn_sched_barrier(0);  // one block's operands at a time
+                    f32x4 acc[RT][NT];
 #pragma unroll
-                    for (int i = 0; i < RT; ++i) {
-                        sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    for (int i = 0; i < RT; ++i)
 #pragma unroll
                         for (int t = 0; t < NT; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    }
 #pragma unroll
                     for (int j = b * 4 / NB; j < (b + 1) * 4 / NB; ++j) {
                         const int k = BLOCK == 128 ? 32 * lg + 8 * j : 32 * j + 8 * lg;
-                        bf16x8 x[RT];
+                        bf16x8 x[RT][P];
 #pragma unroll
-                        for (int i = 0; i < RT; ++i) {
-                            x[i] = *reinterpret_cast<const bf16x8 *>(
-                                lds + place_row[i] * pitch + ((c - c0) * 128 + k) * 2);
-                            sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], ones, sum[i], 0,
-                                                                             0, 0);
-                        }
+                        for (int i = 0; i < RT; ++i)
+#pragma unroll
+                            for (int p = 0; p < P; ++p)
+                                x[i][p] = *reinterpret_cast<const bf16x8 *>(
+                                    xs + p * part + my_row[i] * pitch + k * 2);
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            const bf16x8 q = unpack(w[t][j]);
+                            const bf16x8 q = unpack(w[t][j], mask, sixteen);
 #pragma unroll
-                            for (int i = 0; i < RT; ++i)
-                                acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                    x[i], q, acc[i][t], 0, 0, 0);
+                            for (int p = 0; p < P; ++p)
+#pragma unroll
+                                for (int i = 0; i < RT; ++i)
+                                    acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                        x[i][p], q, acc[i][t], 0, 0, 0);
                         }
                     }
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        const float s = cur.s[t][b], z = 16.f + cur.z[t][b];
+                        const float s = (float)h.s[t][b];
 #pragma unroll
                         for (int i = 0; i < RT; ++i)
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
-                                total[i][t][q] = fmaf(s, fmaf(-z, sum[i][q], acc[i][t][q]),
-                                                      total[i][t][q]);
+                                total[i][t][q] = fmaf(s, acc[i][t][q], total[i][t][q]);
                     }
                 }
-                cur = nxt;
+                __builtin_amdgcn_sched_barrier(0);
+                // Lane group g adds block g's - s (16 + z) sum x; groups past the chunk's
+                // blocks add nothing.
+                const int mine = lg < NB ? lg : 0;
+                float sums[RT];
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+                    sums[i] = xsum[((c - c0) * NB + mine) * g.pass + my_row[i]];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    float s = (float)h.s[t][0], z = Z ? (float)h.z[t][0] : 8.f;
+#pragma unroll
+                    for (int b = 1; b < NB; ++b) {
+                        s = lg == b ? (float)h.s[t][b] : s;
+                        if (Z) z = lg == b ? (float)h.z[t][b] : z;
+                    }
+                    const float sz = lg < NB ? -s * (16.f + z) : 0.f;
+#pragma unroll
+                    for (int i = 0; i < RT; ++i)
+                        total[i][t] =
+                            __builtin_amdgcn_mfma_f32_16x16x4f32(sums[i], sz, total[i][t], 0, 0, 0);
+                }
+            };
+            for (int c = first; c < c1; c += D * wk_count) {
+#pragma unroll
+                for (int d = 0; d < D; ++d) {
+                    const int cd = c + d * wk_count;
+                    if (cd >= c1) break;
+                    chunk(cd, ring[d]);
+                    if (cd + D * wk_count < c1) fetch(cd + D * wk_count, ring[d]);
+                }
             }
         }
 
-        // Sums of the waves that share columns, and of the parts of a row, through
-        // LDS: [wk][place][column of the workgroup].
+        // Sums of the waves that share columns, through LDS: [wk][row][column of the
+        // workgroup].
         const int cols = g.wn * NT * 16;
-        float *sums = reinterpret_cast<float *>(lds);
+        float *join = reinterpret_cast<float *>(lds);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < RT; ++i)
@@ -307,19 +339,16 @@ __global__ void __launch_bounds__(kWaves * 64) q4_kernel(Q4Args g)
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int p = 16 * i + 4 * lg + q;
-                    if (p < rows * P)
-                        sums[(wk * (RT * 16) + p) * cols + (wn * NT + t) * 16 + l15] =
-                            total[i][t][q];
+                    const int r = 16 * i + 4 * lg + q;
+                    if (r < rows)
+                        join[(wk * g.pass + r) * cols + (wn * NT + t) * 16 + l15] = total[i][t][q];
                 }
         __syncthreads();
         for (int i = threadIdx.x; i < rows * cols; i += kWaves * 64) {
             const int r = i / cols, c = i % cols;
             if (n_wg + c >= g.N) continue;
             float v = 0.f;
-            for (int w = 0; w < wk_count; ++w)
-#pragma unroll
-                for (int p = 0; p < P; ++p) v += sums[(w * (RT * 16) + r * P + p) * cols + c];
+            for (int w = 0; w < wk_count; ++w) v += join[(w * g.pass + r) * cols + c];
             static_cast<T *>(g.Y)[(int64_t)(r0 + r) * g.ldy + n_wg + c] = (T)v;
         }
     }

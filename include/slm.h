@@ -150,9 +150,8 @@ int64_t sgemm_xent_workspace(int type, int rows, int vocab, int K, int backward)
  * sgemm_q4_matvec -- rows times weights held in 4 bits: for each group e, on
  * its rows r,
  *     Y[r][n] <- sum_k X[r][k] * (q_e[n][k] - z_e[n][b]) * s_e[n][b],  b = k / block
- * One pass over the weights serves the rows of a group together (16 rows of
- * bf16, 5 of fp32, and up to four times as many where a group has them), so this
- * is meant for single tokens and short batches; any number of rows is computed.
+ * One pass over the weights serves up to 64 rows of a group together, so this is
+ * meant for single tokens and short batches; any number of rows is computed.
  *
  *   type      enum sgemm_type of X, S and Y
  *   groups    sets of weights (1 when offsets is NULL), at most 65535

@@ -43,12 +43,11 @@ struct Form {
 template <typename T, int BLOCK, bool ALIGNED>
 Q4Fn kernel_of(Form f)
 {
-    switch (f.rt * 8 + f.nt) {
-    case 9: return q4_kernel<T, BLOCK, 1, 1, ALIGNED>;
-    case 10: return q4_kernel<T, BLOCK, 1, 2, ALIGNED>;
-    case 18: return q4_kernel<T, BLOCK, 2, 2, ALIGNED>;
-    default: return q4_kernel<T, BLOCK, 4, 2, ALIGNED>;
-    }
+    if (f.rt == 1) return f.nt == 1 ? q4_kernel<T, BLOCK, 1, 1, ALIGNED>
+                                    : q4_kernel<T, BLOCK, 1, 2, ALIGNED>;
+    if constexpr (Parts<T>::value == 1)
+        if (f.rt == 4) return q4_kernel<T, BLOCK, 4, 2, ALIGNED>;
+    return q4_kernel<T, BLOCK, 2, 2, ALIGNED>;
 }
 
 template <typename T>
@@ -105,7 +104,8 @@ extern "C" int sgemm_q4_matvec(int type, int groups, int rows, int N, int K, int
     // Rows per pass: no more than a group is likely to have, so that more of K is staged
     // at once.
     const int64_t likely = offsets ? 2 * mean : rows;
-    const int pass = likely < 64 ? (int)likely : 64;
+    const int most_pass = parts == 1 ? 64 : 24;
+    const int pass = likely < most_pass ? (int)likely : most_pass;
     int rc = 0;
     const int cus = compute_units(&rc);
     if (cus == 0) return rc;
@@ -125,6 +125,17 @@ extern "C" int sgemm_q4_matvec(int type, int groups, int rows, int N, int K, int
         else
             wn *= 2;
     }
+    // What a slab of one chunk per wave needs must fit in 32 KB of LDS beside the rings'
+    // 32 KB (two workgroups per compute unit).  With wn = 8 every pass does.
+    const auto bytes = [&](int64_t slab, int cols) {
+        return type == SGEMM_TYPE_BF16 ? slab_bytes<bf16>((int)slab, block, cols, pass)
+                                       : slab_bytes<float>((int)slab, block, cols, pass);
+    };
+    int room = 32 * 1024;
+    const auto fits = [&](int64_t slab) {
+        return bytes(slab, wn * f.nt * 16) <= room;
+    };
+    while (wn < kWaves && !fits(128 * kWaves / wn)) wn *= 2;
     Q4Args a = {};
     a.X = X, a.Q = Q, a.S = S, a.Z = Z, a.Y = Y, a.offsets = offsets;
     a.ldx = ldx, a.ldy = ldy;
@@ -133,22 +144,21 @@ extern "C" int sgemm_q4_matvec(int type, int groups, int rows, int N, int K, int
     a.rows = rows, a.N = N, a.K = K;
     a.wn = wn;
     a.pass = pass;
-    // A row takes two bytes a part and k, four a block (at most 1/8 byte a k), and 16 a part.
-    int64_t slab = (kSlab / pass - 16 * parts) * 8 / (16 * parts + 1) / 128 * 128;
-    const int64_t step = 128 * kWaves / a.wn;  // one chunk for every wave
-    if (slab > step) slab = slab / step * step;
-    const int64_t all = ceil_div(K, 128) * 128;
-    a.slab = (int)(slab < all ? slab : all > 0 ? all : 128);
+    const int cols = wn * f.nt * 16;
+    const int step = 128 * kWaves / wn;
+    if (used * ceil_div(N, cols) <= cus) room = 124 * 1024;
+    int64_t slab = step;
+    while (slab < K && fits(slab * 2)) slab *= 2;
+    a.slab_log2 = __builtin_ctzll((unsigned long long)slab);
     a.vec_x = aligned(X, 16) && (int64_t)ldx * size % 16 == 0;
-    const int nb = 128 / block;
-    const bool al = K % 128 == 0 && aligned(Q, 16) && aligned(S, nb * size) && aligned(Z, nb);
+    // Whole 16-byte pieces of rows, and offsets inside a workgroup below 2^31.
+    const bool al = K % 32 == 0 && aligned(Q, 16) && K < (1 << 23);
     const Q4Fn fn = type == SGEMM_TYPE_BF16 ? kernel_for<bf16>(block, al, f)
                                             : kernel_for<float>(block, al, f);
-    const int cols = a.wn * f.nt * 16;
-    const int staged = pass * (parts * (a.slab * 2 + 16) + a.slab / block * 4);
-    const int sums = kWaves / a.wn * pass * cols * 4;
+    const int staged = ring_bytes(f.nt) + bytes(slab, cols);
+    const int sums = kWaves / wn * pass * cols * 4;
     const int64_t blocks = ceil_div(N, cols);
-    fn<<<dim3((unsigned)blocks, (unsigned)groups), dim3(kWaves * 64),
+    fn<<<dim3((unsigned)blocks, (unsigned)groups), dim3(kThreads),
          staged > sums ? staged : sums, stream>>>(a);
     return (int)hipGetLastError();
 }

@@ -27,8 +27,12 @@
 // gives instruction j the weights k = 32 j + 8 g + i.
 //
 // A workgroup is 8 waves: WN of them side by side along n, WK = 8 / WN splitting
-// the chunks; their sums meet in LDS.  x is staged in LDS as bf16, up to
-// kSlab bytes at a time, in the order the unpacked pairs have.
+// the chunks; their sums meet in LDS.  Each wave's weights travel to a ring in LDS of
+// its own (buffer_load ... lds), four lanes to the 64 bytes of a row: fetched straight
+// into the lanes that use them, neighbouring lanes would ask for different rows, and
+// the address unit takes such lanes one by one (measured: twice the time).
+// K is walked in slabs: x as bf16 parts in the order the unpacked pairs have, its block
+// sums, and each block's and column's scale and zero.
 #pragma once
 
 #include "lm_tile.hpp"
@@ -41,7 +45,7 @@ using lm::bf16x8;
 using lm::u32x4;
 
 constexpr int kWaves = 8;
-constexpr int kSlab = 64 * 1024;  // bytes of staged x: two workgroups per CU
+constexpr int kThreads = kWaves * 64;
 
 struct Q4Args {
     const void *X;
@@ -54,7 +58,7 @@ struct Q4Args {
     int64_t q_stride, s_stride;  // per group: bytes of Q; elements of S and Z
     int rows, N, K;
     int wn;             // waves along n (a power of two, at most 8)
-    int slab;           // k per slab, a multiple of 128
+    int slab_log2;      // k per slab, at least 128 WK
     int pass;           // rows per pass, at most 16 RT
     int vec_x;          // rows of X take 16-byte loads
 };
@@ -85,116 +89,162 @@ __device__ __forceinline__ u32x4 exchange(u32x4 v)
     return u32x4{c[0], c[1], d[0], d[1]};
 }
 
-// Eight values of a row from k on, zero from K on.
+// Eight values of a row from k on, zero from K on, as they are in memory.
+template <typename T> struct Octet {
+    static constexpr int E = 16 / sizeof(T);
+    union {
+        u32x4 v[8 / E];
+        T e[8];
+    };
+};
+
 template <typename T>
-__device__ __forceinline__ void load8(const T *row, int k, int K, bool vec, float *v)
+__device__ __forceinline__ void load8(const T *row, int k, int K, bool vec, Octet<T> &x)
 {
-    constexpr int E = 16 / sizeof(T);
     if (vec && k + 8 <= K) {
-        typedef T Vec __attribute__((ext_vector_type(E)));
 #pragma unroll
-        for (int h = 0; h < 8 / E; ++h) {
-            const Vec x = *reinterpret_cast<const Vec *>(row + k + h * E);
-#pragma unroll
-            for (int j = 0; j < E; ++j) v[h * E + j] = (float)x[j];
-        }
+        for (int h = 0; h < 8 / Octet<T>::E; ++h)
+            x.v[h] = *reinterpret_cast<const u32x4 *>(row + k + h * Octet<T>::E);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = k + j < K ? (float)row[k + j] : 0.f;
+        for (int j = 0; j < 8; ++j)
+            if (k + j < K) x.e[j] = row[k + j];
     }
 }
 
 // Chunks of weights a wave keeps in flight: 4 KB, which with 16 waves on a compute
 // unit covers the latency of memory at its full rate.
 constexpr int ring_depth(int nt) { return nt == 1 ? 4 : 2; }
+constexpr int ring_bytes(int nt) { return kWaves * ring_depth(nt) * nt * 1024; }
+
+// A scale and 16 + its zero as LDS holds them: bf16 scales as two bf16 values in a word
+// (16 + z is exact), fp32 ones as two floats.
+template <typename T> struct Entry {
+    uint32_t u;
+    __device__ static Entry of(T s, float z)
+    {
+        return {(__builtin_bit_cast(uint32_t, (float)s) & 0xffff0000u) |
+                (__builtin_bit_cast(uint32_t, z) >> 16)};
+    }
+    __device__ float scale() const { return __builtin_bit_cast(float, u & 0xffff0000u); }
+    __device__ float zero() const { return __builtin_bit_cast(float, u << 16); }
+};
+template <> struct Entry<float> {
+    float s, z;
+    __device__ static Entry of(float s, float z) { return {s, z}; }
+    __device__ float scale() const { return s; }
+    __device__ float zero() const { return z; }
+};
+
+// Bytes of LDS after the ring.
+template <typename T>
+inline int slab_bytes(int slab, int block, int cols, int pass)
+{
+    return slab / block * ((cols + 1) * (int)sizeof(Entry<T>) + pass * 4) +
+           Parts<T>::value * pass * (slab * 2 + 16) + 16;
+}
+
+// Every wave's LDS writes are done; global loads stay in flight.
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
 
 template <typename T, int BLOCK, int RT, int NT, bool ALIGNED>
-__global__ void __launch_bounds__(kWaves * 64)
-__attribute__((amdgpu_waves_per_eu(RT * NT <= 4 ? 4 : 2))) q4_kernel(Q4Args g)
+__global__ void __launch_bounds__(kThreads)
+__attribute__((amdgpu_waves_per_eu(RT <= 2 ? 4 : 2))) q4_kernel(Q4Args g)
 {
     constexpr int D = ring_depth(NT);
     constexpr int P = Parts<T>::value;           // bf16 parts of a value
     constexpr int NB = 128 / BLOCK;              // blocks per chunk
-    extern __shared__ __attribute__((aligned(16))) char lds[];
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l15 = lane & 15, lg = lane >> 4;
     const int wk_count = kWaves / g.wn;
     const int wn = wave % g.wn, wk = wave / g.wn;
-    const int n_wg = blockIdx.x * (g.wn * NT * 16);
+    const int cols = g.wn * NT * 16;
+    const int n_wg = blockIdx.x * cols;
     const int group = blockIdx.y;
     int begin = 0, end = g.rows;
-    if (g.offsets) lm::group_rows(g.offsets, group, g.rows, begin, end);
+    if (g.offsets) {
+        lm::group_rows(g.offsets, group, g.rows, begin, end);
+        begin = __builtin_amdgcn_readfirstlane(begin);
+        end = __builtin_amdgcn_readfirstlane(end);
+    }
     if (begin >= end) return;
 
     const int nblk = (g.K + BLOCK - 1) / BLOCK;
     const int chunks = (g.K + 127) / 128;
     const int row_bytes = g.K / 2;
-    // This lane's weight rows (past N: the last one, whose outputs are not stored), as
-    // offsets from the workgroup's first row: bytes of Q, blocks of S and Z.
+    const int ncols = g.N - n_wg < cols ? g.N - n_wg : cols;  // columns that exist
     const uint8_t *Q = g.Q + group * g.q_stride + (int64_t)n_wg * row_bytes;
     const T *S = static_cast<const T *>(g.S) + group * g.s_stride + (int64_t)n_wg * nblk;
     const uint8_t *Z = g.Z ? g.Z + group * g.s_stride + (int64_t)n_wg * nblk : nullptr;
-    uint32_t qoff[NT], soff[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        int n = (wn * NT + t) * 16 + l15;
-        n = n_wg + n < g.N ? n : g.N - 1 - n_wg;
-        qoff[t] = (uint32_t)n * (uint32_t)row_bytes + (uint32_t)lg * 16u;
-        soff[t] = (uint32_t)n * (uint32_t)nblk;
-    }
+    const T *X = static_cast<const T *>(g.X);
 
-    typedef T Scales __attribute__((ext_vector_type(NB)));
-    typedef uint8_t Zeros __attribute__((ext_vector_type(NB)));
-    struct Chunk {
-        u32x4 q[NT];
-        Scales s[NT];
-        Zeros z[NT];
-    };
-    auto fetch = [&](int c, Chunk &h) {
-        const uint8_t *qc = Q + (int64_t)c * 64;
-        const T *sc = S + (int64_t)c * NB;
-        const uint8_t *zc = Z + (Z ? (int64_t)c * NB : 0);
+    // LDS: the rings, the parts of x, per block of the slab and row the sum of x, and per
+    // block and column its entry (one column more than there are, so that consecutive
+    // blocks start in different banks).
+    char *ring = lds + wave * (D * NT * 1024);
+    const uint32_t ring_at = (uint32_t)(uintptr_t)(lm::lds_char *)ring;
+    // All powers of two: a slab's k, octets and blocks.
+    const int slab = 1 << g.slab_log2, oct_log2 = g.slab_log2 - 3;
+    const int blk_log2 = g.slab_log2 - (BLOCK == 128 ? 7 : BLOCK == 64 ? 6 : 5);
+    const int slab_blocks = 1 << blk_log2;
+    const int pitch = slab * 2 + 16;  // bytes of a staged row: rows start in different banks
+    const int part = g.pass * pitch;  // bytes of a part of x
+    char *xs = lds + ring_bytes(NT);
+    Entry<T> *entries = reinterpret_cast<Entry<T> *>(xs + P * part);
+    float *xsum = reinterpret_cast<float *>(entries + slab_blocks * (cols + 1));
+
+    // The ring: slot (row, place) of a 1 KB tile holds the 16 bytes at piece
+    // place ^ (row / 4 & 3) of the row, so that the 16 lanes that later read one piece of
+    // 16 rows meet 16 places of 256 bytes.
+    const int frow = lane >> 2, fpiece = (lane & 3) ^ ((lane >> 4) & 3);
+    uint32_t voff[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if constexpr (ALIGNED) {  // K a multiple of 128: whole chunks, whole vectors of scales
-                h.q[t] = *reinterpret_cast<const u32x4 *>(qc + qoff[t]);
-                h.s[t] = *reinterpret_cast<const Scales *>(sc + soff[t]);
-                if (Z) h.z[t] = *reinterpret_cast<const Zeros *>(zc + soff[t]);
-            } else {
-                const int at = c * 64 + lg * 16;  // byte of the row
-                if (at + 16 <= row_bytes) {
-                    __builtin_memcpy(&h.q[t], qc + qoff[t], 16);
-                } else {
-                    union {
-                        u32x4 v;
-                        uint8_t b[16];
-                    } x;
-                    x.v = u32x4{0, 0, 0, 0};
+    for (int t = 0; t < NT; ++t)
+        voff[t] = (uint32_t)((wn * NT + t) * 16 + frow) * (uint32_t)row_bytes + fpiece * 16u;
+    auto fetch = [&](int c, int d) {  // chunk c into slot d
+        if constexpr (ALIGNED) {
+            // Rows past N, and chunks past K, are outside the descriptor.
+            const int64_t left = c < chunks ? (int64_t)(g.N - n_wg) * row_bytes - c * 64 : 0;
+            u32x4 r = lm::descriptor(reinterpret_cast<const char *>(Q) + (int64_t)c * 64, left);
+            asm volatile("s_nop 4" : "+s"(r));
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (at + j < row_bytes) x.b[j] = qc[qoff[t] + j];
-                    h.q[t] = x.v;
+            for (int t = 0; t < NT; ++t)
+                lm::load_slab16(r, voff[t], ring_at + (d * NT + t) * 1024);
+        } else {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const int n = (wn * NT + t) * 16 + frow, at = c * 64 + fpiece * 16;
+                union {
+                    u32x4 v;
+                    uint8_t b[16];
+                } x;
+                x.v = u32x4{0, 0, 0, 0};
+                if (n < ncols && at < row_bytes) {
+                    const uint8_t *p = Q + (int64_t)n * row_bytes + at;
+                    if (at + 16 <= row_bytes) {
+                        __builtin_memcpy(&x, p, 16);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (at + j < row_bytes) x.b[j] = p[j];
+                    }
                 }
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    // A block past the last holds only zeros of x: any scale will do.
-                    int blk = c * NB + b;
-                    blk = blk < nblk ? blk : nblk - 1;
-                    h.s[t][b] = S[soff[t] + blk];
-                    if (Z) h.z[t][b] = Z[soff[t] + blk];
-                }
+                *reinterpret_cast<u32x4 *>(ring + (d * NT + t) * 1024 + lane * 16) = x.v;
             }
         }
     };
-
-    const int pitch = g.slab * 2 + 16;  // bytes of a staged row: rows start in different banks
-    const int part = g.pass * pitch;    // bytes of a part of x
-    float *xsum = reinterpret_cast<float *>(lds + P * part);  // [block of the slab][row]
     uint32_t mask = 0x00780078u, sixteen = 0x41804180u;
     asm("" : "+s"(mask));
     asm("" : "+v"(sixteen));
+    const int per_slab = slab / 128 / wk_count;                    // chunks a wave takes per slab
+    const int steps = (chunks + wk_count - 1) / wk_count;          // and in all
+
     for (int r0 = begin; r0 < end; r0 += g.pass) {
         const int rows = end - r0 < g.pass ? end - r0 : g.pass;
         f32x4 total[RT][NT];
@@ -208,53 +258,137 @@ __attribute__((amdgpu_waves_per_eu(RT * NT <= 4 ? 4 : 2))) q4_kernel(Q4Args g)
 #pragma unroll
         for (int i = 0; i < RT; ++i) my_row[i] = 16 * i + l15 < rows ? 16 * i + l15 : rows - 1;
 
-        for (int k0 = 0; k0 < g.K; k0 += g.slab) {
-            const int kn = g.K - k0 < g.slab ? g.K - k0 : g.slab;
-            const int c0 = k0 / 128, c1 = c0 + (kn + 127) / 128;
-            Chunk ring[D];
-            const int first = c0 + wk;
+        auto put = [&](int i, const Octet<T> &x) {
+            const int r = i >> oct_log2, o = i & ((1 << oct_log2) - 1);
+            float v[8], sum = 0.f;
 #pragma unroll
-            for (int d = 0; d < D; ++d)
-                if (first + d * wk_count < c1) fetch(first + d * wk_count, ring[d]);
-            __syncthreads();  // the slab (or the sums) before this one have been read
-            const int octets = (c1 - c0) * 16;
-            for (int i = threadIdx.x; i < rows * octets; i += kWaves * 64) {
-                const int r = i / octets, o = i % octets;
-                float v[8];
-                load8(static_cast<const T *>(g.X) + (int64_t)(r0 + r) * g.ldx, k0 + 8 * o, g.K,
-                      g.vec_x, v);
-                float sum = 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sum += v[j];
-                // Each part in turn: the leading 16 bits of what is left, and the rest
-                // (exact; an infinity leaves a NaN, a NaN stays one).
-#pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    u32x4 out;
-#pragma unroll
-                    for (int d = 0; d < 4; ++d) {  // values d and d + 4 share a word
-                        const uint32_t lo = __builtin_bit_cast(uint32_t, v[d]);
-                        const uint32_t hi = __builtin_bit_cast(uint32_t, v[d + 4]);
-                        out[d] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
-                        if (p + 1 < P) {
-                            v[d] -= __builtin_bit_cast(float, lo & 0xffff0000u);
-                            v[d + 4] -= __builtin_bit_cast(float, hi & 0xffff0000u);
-                        }
-                    }
-                    *reinterpret_cast<u32x4 *>(lds + p * part + r * pitch + o * 16) = out;
-                }
-                // The BLOCK / 8 lanes of a block are neighbours, all of them here.
-#pragma unroll
-                for (int d = 1; d < BLOCK / 8; d *= 2) sum += __shfl_xor(sum, d);
-                if (o % (BLOCK / 8) == 0) xsum[o / (BLOCK / 8) * g.pass + r] = sum;
+            for (int j = 0; j < 8; ++j) {
+                v[j] = (float)x.e[j];
+                sum += v[j];
             }
-            __syncthreads();
+            // The BLOCK / 8 lanes of a block are neighbours, and here together.
+#pragma unroll
+            for (int d = 1; d < BLOCK / 8; d *= 2) sum += __shfl_xor(sum, d);
+            if (o % (BLOCK / 8) == 0) xsum[o / (BLOCK / 8) * g.pass + r] = sum;
+            // Each part in turn: the leading 16 bits of what is left, and the rest (exact;
+            // an infinity leaves a NaN, a NaN stays one).
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                u32x4 out;
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {  // values d and d + 4 share a word
+                    const uint32_t lo = __builtin_bit_cast(uint32_t, v[d]);
+                    const uint32_t hi = __builtin_bit_cast(uint32_t, v[d + 4]);
+                    out[d] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+                    if (p + 1 < P) {
+                        v[d] -= __builtin_bit_cast(float, lo & 0xffff0000u);
+                        v[d + 4] -= __builtin_bit_cast(float, hi & 0xffff0000u);
+                    }
+                }
+                *reinterpret_cast<u32x4 *>(xs + p * part + r * pitch + o * 16) = out;
+            }
+        };
+        // Scales and zeros kLot at a time, the first lot on its way while x is staged;
+        // columns past N and blocks past K (which meet no output, or zeros of x) take the
+        // last ones.
+        constexpr int kLot = 4;
+        T hs[kLot];
+        uint8_t hz[kLot];
+        const int count_s = cols << blk_log2;
+        auto load_lot = [&](int i0, int k0) {
+#pragma unroll
+            for (int q = 0; q < kLot; ++q) {
+                const int i = i0 + lane + q * kThreads;
+                int n = i >> blk_log2, b = k0 / BLOCK + (i & (slab_blocks - 1));
+                n = n < ncols ? n : ncols - 1;
+                b = b < nblk ? b : nblk - 1;
+                const uint32_t at = (uint32_t)n * (uint32_t)nblk + (uint32_t)b;
+                hs[q] = S[at];
+                hz[q] = Z ? Z[at] : 8;
+            }
+        };
+        auto put_lot = [&](int i0) {
+#pragma unroll
+            for (int q = 0; q < kLot; ++q) {
+                const int i = i0 + lane + q * kThreads;
+                if (i < count_s)
+                    entries[(i & (slab_blocks - 1)) * (cols + 1) + (i >> blk_log2)] =
+                        Entry<T>::of(hs[q], 16.f + (float)hz[q]);
+            }
+        };
+        // Rolled loops: values held in registers for the next slab, or unrolled copies
+        // with their conditions, cost the main loop its registers (measured: twice the
+        // time).
+        auto stage = [&](int k0) {
+            const int count = rows << oct_log2;
+            int i0 = threadIdx.x & ~63;
+            load_lot(i0, k0);
+            if (g.vec_x && k0 + slab <= g.K) {
+                // Four octets' loads at a time; past the end, the last octet again.
+#pragma unroll 1
+                for (int x0 = threadIdx.x & ~63; x0 < count; x0 += 4 * kThreads) {
+                    Octet<T> x[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        int i = x0 + lane + q * kThreads;
+                        i = i < count ? i : count - 1;
+                        const T *p = X + (int64_t)(r0 + (i >> oct_log2)) * g.ldx + k0 +
+                                     8 * (i & ((1 << oct_log2) - 1));
+#pragma unroll
+                        for (int h = 0; h < 8 / Octet<T>::E; ++h)
+                            x[q].v[h] = *reinterpret_cast<const u32x4 *>(p + h * Octet<T>::E);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (x0 + lane + q * kThreads < count) put(x0 + lane + q * kThreads, x[q]);
+                }
+            } else {
+#pragma unroll 1
+                for (int i = threadIdx.x; i < count; i += kThreads) {
+                    Octet<T> x;
+#pragma unroll
+                    for (int h = 0; h < 8 / Octet<T>::E; ++h) x.v[h] = u32x4{0, 0, 0, 0};
+                    load8(X + (int64_t)(r0 + (i >> oct_log2)) * g.ldx,
+                          k0 + 8 * (i & ((1 << oct_log2) - 1)), g.K, g.vec_x, x);
+                    put(i, x);
+                }
+            }
+            put_lot(i0);
+#pragma unroll 1
+            for (i0 += kLot * kThreads; i0 < count_s; i0 += kLot * kThreads) {
+                load_lot(i0, k0);
+                put_lot(i0);
+            }
+        };
 
-            auto chunk = [&](int c, const Chunk &h) {
-                const char *xs = lds + (c - c0) * 256;
+        lds_barrier();  // the last rows' sums have been read
+#pragma unroll
+        for (int d = 0; d < D; ++d) fetch(d * wk_count + wk, d);
+        int step = 0, slot = 0;
+        for (int k0 = 0; k0 < g.K; k0 += slab) {
+            lds_barrier();  // the slab before has been read
+            stage(k0);
+            lds_barrier();
+            const int last = step + per_slab < steps ? step + per_slab : steps;
+            for (; step < last; ++step) {
+                const int c = step * wk_count + wk;
+                asm volatile("s_waitcnt vmcnt(%0)" : : "n"((D - 1) * NT) : "memory");
                 u32x4 w[NT];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) w[t] = BLOCK == 128 ? h.q[t] : exchange(h.q[t]);
+                for (int t = 0; t < NT; ++t)
+                    w[t] = *reinterpret_cast<const u32x4 *>(
+                        ring + (slot * NT + t) * 1024 + l15 * 64 + ((lg ^ (l15 >> 2)) << 4));
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before refilled
+                fetch(c + D * wk_count, slot);
+                slot = slot + 1 == D ? 0 : slot + 1;
+                if (c >= chunks) continue;  // of the last step
+                if constexpr (BLOCK != 128) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) w[t] = exchange(w[t]);
+                }
+                const int cs = c - k0 / 128;  // in the slab
+                const char *xc = xs + cs * 256;
+                const Entry<T> *sc = entries + cs * NB * (cols + 1) + wn * NT * 16 + l15;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     __builtin_amdgcn_sched_barrier(0);  // one block's operands at a time
@@ -272,7 +406,7 @@ __attribute__((amdgpu_waves_per_eu(RT * NT <= 4 ? 4 : 2))) q4_kernel(Q4Args g)
 #pragma unroll
                             for (int p = 0; p < P; ++p)
                                 x[i][p] = *reinterpret_cast<const bf16x8 *>(
-                                    xs + p * part + my_row[i] * pitch + k * 2);
+                                    xc + p * part + my_row[i] * pitch + k * 2);
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
                             const bf16x8 q = unpack(w[t][j], mask, sixteen);
@@ -286,7 +420,7 @@ __attribute__((amdgpu_waves_per_eu(RT * NT <= 4 ? 4 : 2))) q4_kernel(Q4Args g)
                     }
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        const float s = (float)h.s[t][b];
+                        const float s = sc[b * (cols + 1) + t * 16].scale();
 #pragma unroll
                         for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -300,39 +434,24 @@ __attribute__((amdgpu_waves_per_eu(RT * NT <= 4 ? 4 : 2))) q4_kernel(Q4Args g)
                 const int mine = lg < NB ? lg : 0;
                 float sums[RT];
 #pragma unroll
-                for (int i = 0; i < RT; ++i)
-                    sums[i] = xsum[((c - c0) * NB + mine) * g.pass + my_row[i]];
+                for (int i = 0; i < RT; ++i) sums[i] = xsum[(cs * NB + mine) * g.pass + my_row[i]];
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    float s = (float)h.s[t][0], z = Z ? (float)h.z[t][0] : 8.f;
-#pragma unroll
-                    for (int b = 1; b < NB; ++b) {
-                        s = lg == b ? (float)h.s[t][b] : s;
-                        if (Z) z = lg == b ? (float)h.z[t][b] : z;
-                    }
-                    const float sz = lg < NB ? -s * (16.f + z) : 0.f;
+                    const Entry<T> e = sc[mine * (cols + 1) + t * 16];
+                    const float sz = lg < NB ? -e.scale() * e.zero() : 0.f;
 #pragma unroll
                     for (int i = 0; i < RT; ++i)
                         total[i][t] =
                             __builtin_amdgcn_mfma_f32_16x16x4f32(sums[i], sz, total[i][t], 0, 0, 0);
                 }
-            };
-            for (int c = first; c < c1; c += D * wk_count) {
-#pragma unroll
-                for (int d = 0; d < D; ++d) {
-                    const int cd = c + d * wk_count;
-                    if (cd >= c1) break;
-                    chunk(cd, ring[d]);
-                    if (cd + D * wk_count < c1) fetch(cd + D * wk_count, ring[d]);
-                }
             }
         }
 
         // Sums of the waves that share columns, through LDS: [wk][row][column of the
-        // workgroup].
-        const int cols = g.wn * NT * 16;
+        // workgroup], where the rings were.
         float *join = reinterpret_cast<float *>(lds);
-        __syncthreads();
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing lands in the rings any more
+        lds_barrier();
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -343,10 +462,10 @@ __attribute__((amdgpu_waves_per_eu(RT * NT <= 4 ? 4 : 2))) q4_kernel(Q4Args g)
                     if (r < rows)
                         join[(wk * g.pass + r) * cols + (wn * NT + t) * 16 + l15] = total[i][t][q];
                 }
-        __syncthreads();
-        for (int i = threadIdx.x; i < rows * cols; i += kWaves * 64) {
+        lds_barrier();
+        for (int i = threadIdx.x; i < rows * cols; i += kThreads) {
             const int r = i / cols, c = i % cols;
-            if (n_wg + c >= g.N) continue;
+            if (c >= ncols) continue;
             float v = 0.f;
             for (int w = 0; w < wk_count; ++w) v += join[(w * g.pass + r) * cols + c];
             static_cast<T *>(g.Y)[(int64_t)(r0 + r) * g.ldy + n_wg + c] = (T)v;

@@ -39,11 +39,11 @@ int compute_units(int *rc)
     return 0;
 }
 
-// An operand the direct loads take: 16-byte rows, and tile offsets below 2^31.
-bool fast_operand(const void *p, int64_t ld, int64_t cols, int64_t group_stride, int size)
+// An operand the direct loads take: rows at 4-byte addresses, and tile offsets below 2^31.
+bool fast_operand(const void *p, int64_t ld, int64_t group_stride, int size)
 {
-    return aligned(p, 16) && ld * size % 16 == 0 && cols * size % 16 == 0 &&
-           group_stride * size % 16 == 0 && ld * size < ((int64_t)1 << 22);
+    return aligned(p, 4) && ld * size % 4 == 0 && group_stride * size % 4 == 0 &&
+           ld * size < ((int64_t)1 << 22);
 }
 
 TileKernel kernel_for(int type, int form, int tile, bool fast)
@@ -58,14 +58,46 @@ int launch(const TileKernel &k, TileArgs &a, int64_t blocks, int slices, hipStre
     return (int)hipGetLastError();
 }
 
-// Tile for one product of M x N outputs: the largest whose tiles still give
-// every compute unit one.
-int plain_tile(int type, int64_t M, int64_t N, int cus)
+// What a tile costs: outputs times contraction over `rate`, the rate its kernel reaches
+// on a compute unit relative to the largest tile's, `lead` being the contraction's worth
+// of time that filling the ring and writing the tile take when nothing else runs on the
+// unit (the 256 tile leaves no room for a second workgroup).  Measured, bf16: T 8192, H 2048, V
+// 131072 with gradients 15.9 ms with the 256 tile, 16.9 with 128 x 192; T 384, H 1024, V
+// 50021 369 and 277 us; 16 experts' backward pass of 16384 rows 381 and 349 us (128 x
+// 128: 403, 64 x 128: 477).  fp32: T 1023, H 1000, V 49999 3.22 ms with the 128 tile,
+// 3.35 with 64 x 64; 24 experts' backward pass of 1500 rows 93 and 63 us.
+struct TileCost {
+    int bm, bn;
+    double rate;
+    int lead;
+};
+const TileCost kBf16Tiles[NUM_TILES] = {
+    {16, 64, 0.2, 64}, {64, 128, 0.65, 64}, {128, 128, 0.8, 64}, {128, 192, 0.88, 64}, {256, 256, 1.0, 256}};
+const TileCost kF32Tiles[NUM_TILES] = {
+    {16, 64, 0.5, 64}, {64, 64, 0.87, 64}, {128, 128, 1.0, 64}, {0, 0, 0, 0}, {0, 0, 0, 0}};
+
+// The tile that finishes first when every compute unit takes the same number of tiles:
+// `groups` products of N columns and contraction K, whose rows split into row_tiles(bm)
+// tiles in all.
+template <typename RowTiles>
+int choose_tile(int type, bool fast, RowTiles row_tiles, int64_t N, int64_t K, int cus)
 {
-    if (M <= 16) return S16;
-    if (type == SGEMM_TYPE_BF16 && ceil_div(M, 256) * ceil_div(N, 256) >= cus) return T256;
-    if (ceil_div(M, 128) * ceil_div(N, 128) >= cus) return T128;
-    return M64;
+    const TileCost *t = type == SGEMM_TYPE_BF16 ? kBf16Tiles : kF32Tiles;
+    int best = S16;
+    double least = 0;
+    for (int i = 0; i < (fast ? (int)NUM_TILES : T128 + 1); ++i) {
+        if (t[i].bm == 0) continue;
+        const int64_t tiles = row_tiles(t[i].bm) * ceil_div(N, t[i].bn);
+        const double cost = (double)ceil_div(tiles, cus) * t[i].bm * t[i].bn * (K + t[i].lead) / t[i].rate;
+        if (i == 0 || cost < least) best = i, least = cost;
+    }
+    return best;
+}
+
+// For one product of M x N outputs.
+int plain_tile(int type, bool fast, int64_t M, int64_t N, int64_t K, int cus)
+{
+    return choose_tile(type, fast, [&](int bm) { return ceil_div(M, bm); }, N, K, cus);
 }
 
 }  // namespace
@@ -100,18 +132,18 @@ extern "C" int sgemm_grouped(int type, int trans, int groups, int rows, int N, i
     const int used = groups < rows ? groups : rows;  // groups with rows, at most
     if ((rows + (int64_t)used * 15) / 16 * ceil_div(N, 64) > INT_MAX) return -5;
 
-    const int64_t mean = ceil_div(rows, used);
     int rc = 0;
     const int cus = compute_units(&rc);
     if (cus == 0) return rc;
-    int tile = mean <= 16 ? S16 : mean <= 64 ? M64 : T128;
-    if (type == SGEMM_TYPE_BF16 && mean > 192 &&
-        (ceil_div(rows, 256) + used / 2) * ceil_div(N, 256) >= cus)
-        tile = T256;
     const int kk = reads ? K : 0;
-    const bool fast = kk == 0 || (fast_operand(X, ldx, K, 0, size) &&
-                                  fast_operand(W, ldw, wcols, stride_w, size));
-    if (!fast && tile == T256) tile = T128;
+    const bool fast = kk == 0 || (fast_operand(X, ldx, 0, size) &&
+                                  fast_operand(W, ldw, stride_w, size));
+    // A group's last tile is half full on average.
+    const auto row_tiles = [&](int bm) {
+        const int64_t t = rows / bm + used / 2;
+        return t > used ? t : (int64_t)used;
+    };
+    const int tile = choose_tile(type, fast, row_tiles, N, kk, cus);
     const TileKernel k = kernel_for(type, trans ? F_ROWS_T : F_ROWS_N, tile, fast);
     // Every group's last tile may be part full.
     const int64_t most = (rows + (int64_t)used * (k.bm - 1)) / k.bm;
@@ -158,13 +190,10 @@ extern "C" int sgemm_grouped_wgrad(int type, int groups, int rows, int M, int N,
     const int cus = compute_units(&rc);
     if (cus == 0) return rc;
     const int kk = reads ? rows : 0;  // 0: every group is empty
-    const bool fast = kk == 0 || (fast_operand(X, ldx, M, 0, size) &&
-                                  fast_operand(G, ldg, N, 0, size));
-    int tile = M64;
-    if (type == SGEMM_TYPE_BF16 && fast && ceil_div(M, 256) * ceil_div(N, 256) * groups >= cus)
-        tile = T256;
-    else if (ceil_div(M, 128) * ceil_div(N, 128) * groups >= cus)
-        tile = T128;
+    const bool fast = kk == 0 || (fast_operand(X, ldx, 0, size) &&
+                                  fast_operand(G, ldg, 0, size));
+    const auto row_tiles = [&](int bm) { return ceil_div(M, bm) * groups; };
+    const int tile = choose_tile(type, fast, row_tiles, N, kk / groups, cus);
     const TileKernel k = kernel_for(type, F_SUM, tile, fast);
     const int64_t blocks = ceil_div(M, k.bm) * ceil_div(N, k.bn) * groups;
     TileArgs a = {};
@@ -213,18 +242,33 @@ __global__ void __launch_bounds__(256) xent_join_kernel(int rows, int tiles, int
     }
 }
 
-// dX <- the slices' fp32 sums added in order, rounded once.
+// dX <- the slices' fp32 sums added in order, rounded once; four columns a thread.
 template <typename T>
 __global__ void __launch_bounds__(256) xent_sum_kernel(int rows, int K, int slices,
                                                        int64_t slice_stride, const float *parts,
                                                        T *dX, int64_t lddx)
 {
-    const int64_t n = (int64_t)rows * K;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n;
-         i += (int64_t)gridDim.x * 256) {
-        float v = parts[i];
-        for (int s = 1; s < slices; ++s) v += parts[s * slice_stride + i];
-        dX[i / K * lddx + i % K] = (T)v;
+    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+        const int c = (blockIdx.x * 256 + threadIdx.x) * 4;
+        if (c >= K) continue;
+        const float *p = parts + (int64_t)row * K + c;
+        const int n = K - c < 4 ? K - c : 4;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (K % 4 == 0) {  // 16-byte rows
+            for (int s = 0; s < slices; ++s, p += slice_stride) {
+                const f32x4 x = *reinterpret_cast<const f32x4 *>(p);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] += x[q];
+            }
+        } else {
+            for (int s = 0; s < slices; ++s, p += slice_stride)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (q < n) v[q] += p[q];
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (q < n) dX[(int64_t)row * lddx + c + q] = (T)v[q];
     }
 }
 
@@ -233,12 +277,12 @@ __global__ void __launch_bounds__(256) xent_sum_kernel(int rows, int K, int slic
 // leave compute units idle otherwise).
 struct XentPlan {
     int64_t piece, pieces, ld;  // ld: leading dimension of the piece's derivatives
-    int slices;
+    int slices, dx_tile;
     bool sums;                  // dX goes through fp32 sums in the workspace
     int64_t d_bytes, bytes;
 };
 
-XentPlan xent_plan(int type, int rows, int vocab, int K, int cus)
+XentPlan xent_plan(int type, bool fast, int rows, int vocab, int K, int cus)
 {
     XentPlan p;
     const int size = elem_size(type);
@@ -246,15 +290,22 @@ XentPlan xent_plan(int type, int rows, int vocab, int K, int cus)
     // piece is never narrower than 2048 columns.
     int64_t most = ((int64_t)256 << 20) / ((int64_t)rows * size) / 256 * 256;
     if (most < 2048) most = 2048;
+    if (most > (1 << 20) - 256) most = (1 << 20) - 256;  // fast_operand's limit for its rows
     p.pieces = ceil_div(vocab, most);
     p.piece = round_up(ceil_div(vocab, p.pieces), 256);
     p.pieces = ceil_div(vocab, p.piece);
     p.ld = p.piece + 64;
     p.d_bytes = round_up((int64_t)rows * p.ld * size, 256);
-    const int64_t tiles = ceil_div(rows, 128) * ceil_div(K, 128);
-    int64_t s = tiles >= cus ? 1 : cus / tiles;
-    if (s > p.piece / 1024) s = p.piece / 1024;
-    p.slices = s < 1 ? 1 : s > 64 ? 64 : (int)s;
+    // dX has few tiles and a long sum: the tile is chosen as if the sum were cut as finely
+    // as it may be (1024 columns a slice), and cut until each compute unit has two.
+    const int64_t most_slices = p.piece / 1024 < 1 ? 1 : p.piece / 1024 > 64 ? 64 : p.piece / 1024;
+    p.dx_tile = choose_tile(
+        type, fast, [&](int bm) { return ceil_div(rows, bm) * most_slices; }, K,
+        p.piece / most_slices, cus);
+    const TileCost &t = (type == SGEMM_TYPE_BF16 ? kBf16Tiles : kF32Tiles)[p.dx_tile];
+    const int64_t tiles = ceil_div(rows, t.bm) * ceil_div(K, t.bn);
+    const int64_t s = tiles >= cus ? 1 : 2 * cus / tiles;
+    p.slices = (int)(s > most_slices ? most_slices : s);
     p.sums = p.slices > 1 || (p.pieces > 1 && type != SGEMM_TYPE_F32);
     p.bytes = p.d_bytes + (p.sums ? (int64_t)p.slices * rows * K * 4 : 0);
     return p;
@@ -301,7 +352,10 @@ extern "C" int64_t sgemm_xent_workspace(int type, int rows, int vocab, int K, in
     int rc = 0;
     int cus = compute_units(&rc);
     if (cus == 0) cus = 256;  // no device: the plan of a whole MI355X
-    return xent_plan(type, rows, vocab, K, cus).bytes;
+    // Whichever operands the call gets.
+    const int64_t a = xent_plan(type, true, rows, vocab, K, cus).bytes;
+    const int64_t b = xent_plan(type, false, rows, vocab, K, cus).bytes;
+    return a > b ? a : b;
 }
 
 extern "C" int sgemm_xent(int type, int rows, int vocab, int K, const void *X, int ldx,
@@ -319,10 +373,9 @@ extern "C" int sgemm_xent(int type, int rows, int vocab, int K, const void *X, i
     const int cus = compute_units(&rc);
     if (cus == 0) return rc;
     const int size = elem_size(type);
-    const bool fast = K == 0 || (fast_operand(X, ldx, K, 0, size) &&
-                                 fast_operand(W, ldw, K, 0, size));
-    int tile = plain_tile(type, rows, vocab, cus);
-    if (!fast && tile == T256) tile = T128;
+    const bool fast = K == 0 || (fast_operand(X, ldx, 0, size) &&
+                                 fast_operand(W, ldw, 0, size));
+    const int tile = plain_tile(type, fast, rows, vocab, K, cus);
     const TileKernel k = kernel_for(type, F_STATS, tile, fast);
     float *value = static_cast<float *>(ws);
     float *parts = value + round_up((int64_t)rows * 4, 256) / 4;
@@ -366,12 +419,10 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
         const TileKernel k = kernel_for(type, F_DW, M64, true);
         return launch(k, a, ceil_div(vocab, k.bm) * ceil_div(K, k.bn), 1, stream);
     }
-    const XentPlan p = xent_plan(type, rows, vocab, K, cus);
+    const bool fast_x = fast_operand(X, ldx, 0, size), fast_w = fast_operand(W, ldw, 0, size);
+    const XentPlan p = xent_plan(type, fast_w, rows, vocab, K, cus);
     if (ws_bytes < p.bytes) return -17;
     float *sums = reinterpret_cast<float *>(static_cast<char *>(ws) + p.d_bytes);
-    const bool fast_x = fast_operand(X, ldx, K, 0, size), fast_w = fast_operand(W, ldw, K, 0, size);
-    // The piece's derivatives are read with their own leading dimension.
-    const bool fast_d = p.ld * size < ((int64_t)1 << 22);
 
     for (int64_t c = 0; c < p.pieces; ++c) {
         const int64_t col0 = c * p.piece;
@@ -380,8 +431,7 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
         const char *Wc = static_cast<const char *>(W) + col0 * ldw * size;
         {
             const bool fast = fast_x && fast_w;
-            int tile = plain_tile(type, rows, n, cus);
-            if (!fast && tile == T256) tile = T128;
+            const int tile = plain_tile(type, fast, rows, n, K, cus);
             const TileKernel k = kernel_for(type, F_GRAD, tile, fast);
             a = TileArgs{};
             a.A = X, a.B = Wc, a.C = ws;
@@ -394,9 +444,8 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
             if (rc) return rc;
         }
         if (dW) {
-            const bool fast = fast_d && fast_x;
-            int tile = plain_tile(type, n, K, cus);
-            if (tile == S16 || (!fast && tile == T256)) tile = tile == S16 ? M64 : T128;
+            const bool fast = fast_x;
+            const int tile = plain_tile(type, fast, n, K, rows, cus);
             const TileKernel k = kernel_for(type, F_DW, tile, fast);
             a = TileArgs{};
             a.A = ws, a.B = X, a.C = static_cast<char *>(dW) + col0 * lddw * size;
@@ -409,17 +458,14 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
             if (rc) return rc;
         }
         if (dX) {
-            const bool fast = fast_d && fast_w;
-            int tile = plain_tile(type, rows, K, cus);
-            if (tile == M64 && p.slices > 1 && rows > 64) tile = T128;
-            if (!fast && tile == T256) tile = T128;
+            const bool fast = fast_w;
             a = TileArgs{};
             a.A = ws, a.B = Wc;
             a.lda = p.ld, a.ldb = ldw;
             a.M = rows, a.N = K, a.K = n;
             a.a_cols = n8, a.b_cols = K, a.b_rows = n;
             const bool direct = !p.sums && p.pieces == 1;
-            const TileKernel k = kernel_for(type, direct ? F_DX : F_PART, tile, fast);
+            const TileKernel k = kernel_for(type, direct ? F_DX : F_PART, p.dx_tile, fast);
             if (direct) {
                 a.C = dX, a.ldc = lddx, a.alpha = 1.f;
                 a.vec_c = aligned(dX, 4 * size) && lddx % 4 == 0;
@@ -437,8 +483,7 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
         }
     }
     if (dX && p.sums) {
-        const int64_t blocks = ceil_div((int64_t)rows * K, 1024);
-        const dim3 grid((unsigned)(blocks < 16 * cus ? blocks : 16 * cus));
+        const dim3 grid((unsigned)ceil_div(K, 1024), (unsigned)(rows < 65535 ? rows : 65535));
         const int64_t stride = (int64_t)rows * K;
         if (type == SGEMM_TYPE_BF16)
             xent_sum_kernel<bf16><<<grid, dim3(256), 0, stream>>>(rows, K, p.slices, stride, sums,

@@ -15,6 +15,7 @@ TileKernel bf16_kernel(int form, int tile, bool fast)
     case S16: return tile_entry<bf16, 16, 64, 1, 4, 4, 16, 4, true>(form);
     case M64: return tile_entry<bf16, 64, 128, 2, 2, 3, 16, 2, true>(form);
     case T128: return tile_entry<bf16, 128, 128, 2, 2, 2, 16, 2, true>(form);
+    case T192: return tile_entry<bf16, 128, 192, 2, 2, 2, 16, 2, true>(form);
     default: return tile_entry<bf16, 256, 256, 2, 2, 2, 32, 1, true>(form);
     }
 }

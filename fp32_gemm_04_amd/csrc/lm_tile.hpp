@@ -11,13 +11,14 @@
 //
 // A slab travels from memory to an LDS ring of NBUF buffers with
 // buffer_load_dwordx4 ... lds (the wave's 64 x 16 bytes land in lane order),
-// so no registers hold it.  The buffer descriptor ends where the operand
-// ends: a row past the end reads as zero without any per-lane test, and a
-// slab issued past the last one touches no memory, so the ring needs no
-// special tail.  Only the last slab of a KC operand whose K is not a multiple
-// of BK moves single lanes out of the descriptor's range.
-// When an operand is not 16-byte aligned throughout (FAST false), the same
-// slabs go through registers, each value tested against the operand's ends.
+// so no registers hold it.  The addresses need 4-byte alignment only, and the buffer
+// descriptor, which checks each 4 bytes, ends where the operand ends: what lies past
+// the end reads as zero without any per-lane test, and a slab issued past the last one
+// touches no memory, so the ring needs no special tail.  Only in the last slab of a KC
+// operand whose K is not a multiple of BK do lanes past K leave the descriptor's range,
+// and where K is no multiple of a chunk its values past K are cleared in LDS.
+// bf16 operands with rows at odd addresses (FAST false) go through registers, each
+// value tested against the operand's ends.
 //
 // LDS layouts, in 16-byte chunks; the permutation is applied to which chunk a
 // lane fetches, since the DMA writes lanes in order:
@@ -142,7 +143,9 @@ constexpr uint32_t kOutside = 0x80000000u;  // beyond every descriptor's range
 __device__ __forceinline__ u32x4 descriptor(const char *p, int64_t left)
 {
     const uint64_t a = reinterpret_cast<uint64_t>(p);
-    const uint32_t n = left <= 0 ? 0u : left > (int64_t)kOutside ? kOutside : (uint32_t)left;
+    // Whole words: the last may end past the operand (never past a word it has part of).
+    const uint32_t n =
+        left <= 0 ? 0u : left > (int64_t)kOutside ? kOutside : ((uint32_t)left + 3u) & ~3u;
     u32x4 r;
     r[0] = __builtin_amdgcn_readfirstlane((uint32_t)a);
     r[1] = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32)) & 0xffffu;
@@ -159,19 +162,22 @@ struct Slab {
     static constexpr int BYTES = B * 128;
     static constexpr int RC = B / EPC;             // MC: chunks per slab row
 
+    // Rows of a multiple of 256 bytes all start in bank 0; rows of an odd multiple of 128
+    // alternate between two halves by themselves, and their chunks stay inside 128 bytes.
     __device__ static __forceinline__ int swizzle(int k)
     {
-        // Rows shorter than 256 bytes already alternate between places.
-        constexpr int ROWS = RC >= 16 ? 1 : 16 / RC;  // rows per 256 bytes
-        const int j = k / ROWS;
-        int p;
-        if constexpr (std::is_same<T, float>::value)
-            p = BL == 16 ? 4 * ((k >> 2) & 3) : 8 * ((k >> 2) & 1);
-        else if constexpr (BL == 32)
-            p = 4 * (j & 3);
-        else
-            p = ROWS == 1 ? 2 * ((k & 3) + ((k >> 1) & 4)) : 2 * ((j & 1) + ((k >> 2) & 2));
-        return p & (RC - 1);
+        static_assert(L == KC || RC % 8 == 0 || RC <= 4, "a slab row is whole 128-byte groups");
+        constexpr bool WHOLE = RC % 16 == 0;
+        if constexpr (RC <= 4)
+            return 0;
+        else if constexpr (std::is_same<T, float>::value) {
+            static_assert(L == KC || WHOLE, "fp32 slab rows are whole 256-byte groups");
+            return BL == 16 ? 4 * ((k >> 2) & 3) : 8 * ((k >> 2) & 1);
+        } else if constexpr (BL == 32) {
+            return WHOLE ? 4 * (k & 3) : 4 * ((k >> 1) & 1);
+        } else {
+            return WHOLE ? 2 * ((k & 3) + ((k >> 1) & 4)) : 2 * (((k >> 1) & 1) + ((k >> 2) & 2));
+        }
     }
     // Row (KC: of the tile; MC: of the slab) and chunk that slot s fetches.
     __device__ static __forceinline__ void slot(int s, int &row, int &chunk)
@@ -489,7 +495,23 @@ tile_kernel(TileArgs g)
             for (int i = 0; i < LPW; ++i) load(i, base + (uint32_t)b * STAGE);
             advance();
         }
+        // Values past K in the last slab's last chunk (KC: row r of an operand, MC: no
+        // need, rows past K are past the descriptor).
+        const int ragged = K % EPC;
+        auto clear_tail = [&](char *slab) {
+            auto clear = [&](char *rows, int count) {
+                const int chunk = K % BK / EPC;
+                for (int r = threadIdx.x; r < count; r += NW * 64) {
+                    T *p = reinterpret_cast<T *>(rows + r * 128 + ((chunk ^ ((r >> 1) & 7)) << 4));
+                    for (int j = ragged; j < EPC; ++j) p[j] = (T)0.f;
+                }
+            };
+            if constexpr (LA == KC) clear(slab, BM);
+            if constexpr (LB == KC) clear(slab + SA::BYTES, BN);
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        };
         wait_slab_barrier<LPW *(NBUF - 1)>();
+        if ((LA == KC || LB == KC) && ragged && slabs == 1) clear_tail(lds);
         Frag a0[KS][FM], b0[KS][FN], a1[KS][FM], b1[KS][FN];
 #pragma unroll
         for (int r = 0; r < R; ++r) read_op(r, lds, 0, a0, b0);
@@ -508,7 +530,8 @@ tile_kernel(TileArgs g)
             wait_slab_barrier<LPW *(NBUF - 2)>();
             const uint32_t at = base + (uint32_t)buf * STAGE;
             buf = buf + 1 == NBUF ? 0 : buf + 1;
-            const char *there = lds + buf * STAGE;
+            char *there = lds + buf * STAGE;
+            if ((LA == KC || LB == KC) && ragged && t + 2 == slabs) clear_tail(there);
             next_slab();
             products(a1, b1, [&](int n) {
 #pragma unroll

@@ -17,10 +17,9 @@
  *
  * Types.  Matrices hold fp32 or bf16 values (one type per call); every sum is
  * held in fp32, and a bf16 result is rounded once, to nearest even.
- * Pointers need the alignment of their element.  Operands that are 16-byte
- * aligned, with a leading dimension (and a contiguous extent) that is a
- * multiple of 16 bytes, take the direct-to-LDS load path; others are loaded
- * through registers.
+ * Pointers need the alignment of their element.  Rows at 4-byte addresses
+ * (always so for fp32) are loaded straight to LDS; bf16 operands with an odd leading
+ * dimension, group stride or address go through registers, more slowly.
  */
 #ifndef LIBSGEMM_SLM_H
 #define LIBSGEMM_SLM_H

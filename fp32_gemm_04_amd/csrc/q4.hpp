@@ -112,6 +112,23 @@ __device__ __forceinline__ void load8(const T *row, int k, int K, bool vec, Octe
     }
 }
 
+// The sum over the BLOCK / 8 neighbouring lanes that hold a block, in each of them: within
+// four lanes, then mirrored eights and sixteens (whose quarters are already equal).
+template <int BLOCK>
+__device__ __forceinline__ float block_sum(float v)
+{
+    const auto add = [&](auto ctrl) {
+        v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                           0, __builtin_bit_cast(int, v), decltype(ctrl)::value,
+                                           0xf, 0xf, true));
+    };
+    add(std::integral_constant<int, 0xb1>{});                          // lanes 1 0 3 2
+    add(std::integral_constant<int, 0x4e>{});                          // lanes 2 3 0 1
+    if constexpr (BLOCK >= 64) add(std::integral_constant<int, 0x141>{});   // 7 .. 0
+    if constexpr (BLOCK == 128) add(std::integral_constant<int, 0x140>{});  // 15 .. 0
+    return v;
+}
+
 // Chunks of weights a wave keeps in flight: 4 KB, which with 16 waves on a compute
 // unit covers the latency of memory at its full rate.
 constexpr int ring_depth(int nt) { return nt == 1 ? 4 : 2; }
@@ -262,16 +279,11 @@ __attribute__((amdgpu_waves_per_eu(RT <= 2 ? 4 : 2))) q4_kernel(Q4Args g)
             const int r = i >> oct_log2, o = i & ((1 << oct_log2) - 1);
             float v[8], sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[j] = (float)x.e[j];
-                sum += v[j];
-            }
-            // The BLOCK / 8 lanes of a block are neighbours, and here together.
-#pragma unroll
-            for (int d = 1; d < BLOCK / 8; d *= 2) sum += __shfl_xor(sum, d);
-            if (o % (BLOCK / 8) == 0) xsum[o / (BLOCK / 8) * g.pass + r] = sum;
+            for (int j = 0; j < 8; ++j) v[j] = (float)x.e[j];
             // Each part in turn: the leading 16 bits of what is left, and the rest (exact;
-            // an infinity leaves a NaN, a NaN stays one).
+            // an infinity leaves a NaN, a NaN stays one).  The block's sum of x is formed
+            // part by part, since sums of so few bits hardly round: it is multiplied by up to
+            // 31, so its own roundings would outweigh those of the product.
 #pragma unroll
             for (int p = 0; p < P; ++p) {
                 u32x4 out;
@@ -285,8 +297,15 @@ __attribute__((amdgpu_waves_per_eu(RT <= 2 ? 4 : 2))) q4_kernel(Q4Args g)
                         v[d + 4] -= __builtin_bit_cast(float, hi & 0xffff0000u);
                     }
                 }
+                float part_sum = 0.f;
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    part_sum += __builtin_bit_cast(float, out[d] << 16) +
+                                __builtin_bit_cast(float, out[d] & 0xffff0000u);
+                sum += block_sum<BLOCK>(part_sum);
                 *reinterpret_cast<u32x4 *>(xs + p * part + r * pitch + o * 16) = out;
             }
+            if (o % (BLOCK / 8) == 0) xsum[o / (BLOCK / 8) * g.pass + r] = sum;
         };
         // Scales and zeros kLot at a time, the first lot on its way while x is staged;
         // columns past N and blocks past K (which meet no output, or zeros of x) take the

@@ -76,9 +76,10 @@ const TileCost kBf16Tiles[NUM_TILES] = {
 const TileCost kF32Tiles[NUM_TILES] = {
     {16, 64, 0.5, 64}, {64, 64, 0.87, 64}, {128, 128, 1.0, 64}, {0, 0, 0, 0}, {0, 0, 0, 0}};
 
-// The tile that finishes first when every compute unit takes the same number of tiles:
-// `groups` products of N columns and contraction K, whose rows split into row_tiles(bm)
-// tiles in all.
+// The tile that finishes first when every compute unit takes the same number of tiles
+// (a last one that has the unit to itself counts half where two fit beside each other):
+// products of N columns and contraction K, whose rows split into row_tiles(bm) tiles in
+// all.
 template <typename RowTiles>
 int choose_tile(int type, bool fast, RowTiles row_tiles, int64_t N, int64_t K, int cus)
 {
@@ -88,7 +89,9 @@ int choose_tile(int type, bool fast, RowTiles row_tiles, int64_t N, int64_t K, i
     for (int i = 0; i < (fast ? (int)NUM_TILES : T128 + 1); ++i) {
         if (t[i].bm == 0) continue;
         const int64_t tiles = row_tiles(t[i].bm) * ceil_div(N, t[i].bn);
-        const double cost = (double)ceil_div(tiles, cus) * t[i].bm * t[i].bn * (K + t[i].lead) / t[i].rate;
+        const bool pairs = t[i].lead == 64 && tiles > cus;
+        const double rounds = pairs ? 0.5 * ceil_div(2 * tiles, cus) : (double)ceil_div(tiles, cus);
+        const double cost = rounds * t[i].bm * t[i].bn * (K + t[i].lead) / t[i].rate;
         if (i == 0 || cost < least) best = i, least = cost;
     }
     return best;
@@ -296,16 +299,20 @@ XentPlan xent_plan(int type, bool fast, int rows, int vocab, int K, int cus)
     p.pieces = ceil_div(vocab, p.piece);
     p.ld = p.piece + 64;
     p.d_bytes = round_up((int64_t)rows * p.ld * size, 256);
-    // dX has few tiles and a long sum: the tile is chosen as if the sum were cut as finely
-    // as it may be (1024 columns a slice), and cut until each compute unit has two.
+    // dX may have few tiles and a long sum: where its tiles would not fill the compute
+    // units, the tile is chosen as if the sum were cut as finely as it may be (1024
+    // columns a slice), and cut until each unit has two.
     const int64_t most_slices = p.piece / 1024 < 1 ? 1 : p.piece / 1024 > 64 ? 64 : p.piece / 1024;
-    p.dx_tile = choose_tile(
-        type, fast, [&](int bm) { return ceil_div(rows, bm) * most_slices; }, K,
-        p.piece / most_slices, cus);
-    const TileCost &t = (type == SGEMM_TYPE_BF16 ? kBf16Tiles : kF32Tiles)[p.dx_tile];
-    const int64_t tiles = ceil_div(rows, t.bm) * ceil_div(K, t.bn);
-    const int64_t s = tiles >= cus ? 1 : 2 * cus / tiles;
-    p.slices = (int)(s > most_slices ? most_slices : s);
+    p.dx_tile = plain_tile(type, fast, rows, K, p.piece, cus);
+    p.slices = 1;
+    if (ceil_div(rows, 128) * ceil_div(K, 128) < cus) {
+        p.dx_tile = choose_tile(
+            type, fast, [&](int bm) { return ceil_div(rows, bm) * most_slices; }, K,
+            p.piece / most_slices, cus);
+        const TileCost &t = (type == SGEMM_TYPE_BF16 ? kBf16Tiles : kF32Tiles)[p.dx_tile];
+        const int64_t s = 2 * cus / (ceil_div(rows, t.bm) * ceil_div(K, t.bn));
+        p.slices = (int)(s < 1 ? 1 : s > most_slices ? most_slices : s);
+    }
     p.sums = p.slices > 1 || (p.pieces > 1 && type != SGEMM_TYPE_F32);
     p.bytes = p.d_bytes + (p.sums ? (int64_t)p.slices * rows * K * 4 : 0);
     return p;

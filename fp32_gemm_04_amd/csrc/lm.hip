@@ -46,6 +46,14 @@ bool fast_operand(const void *p, int64_t ld, int64_t group_stride, int size)
            ld * size < ((int64_t)1 << 22);
 }
 
+// How wide the stores to an output may be: TileArgs::vec_c.
+int vector_rows(const void *p, int64_t ld, int64_t group_stride, int size)
+{
+    for (int v = 2; v > 0; --v)
+        if (aligned(p, 4 * v * size) && ld % (4 * v) == 0 && group_stride % (4 * v) == 0) return v;
+    return 0;
+}
+
 TileKernel kernel_for(int type, int form, int tile, bool fast)
 {
     return type == SGEMM_TYPE_BF16 ? bf16_kernel(form, tile, fast) : f32_kernel(form, tile, fast);
@@ -72,9 +80,10 @@ struct TileCost {
     int lead;
 };
 const TileCost kBf16Tiles[NUM_TILES] = {
-    {16, 64, 0.2, 64}, {64, 128, 0.65, 64}, {128, 128, 0.8, 64}, {128, 192, 0.88, 64}, {256, 256, 1.0, 256}};
+    {16, 64, 0.2, 64}, {32, 128, 0.45, 64}, {64, 128, 0.65, 64}, {128, 128, 0.8, 64}, {128, 192, 0.88, 64},
+    {256, 256, 1.0, 256}};
 const TileCost kF32Tiles[NUM_TILES] = {
-    {16, 64, 0.5, 64}, {64, 64, 0.87, 64}, {128, 128, 1.0, 64}, {0, 0, 0, 0}, {0, 0, 0, 0}};
+    {16, 64, 0.5, 64}, {32, 64, 0.75, 64}, {64, 64, 0.87, 64}, {128, 128, 1.0, 64}, {0, 0, 0, 0}, {0, 0, 0, 0}};
 
 // The tile that finishes first when every compute unit takes the same number of tiles
 // (a last one that has the unit to itself counts half where two fit beside each other):
@@ -159,7 +168,7 @@ extern "C" int sgemm_grouped(int type, int trans, int groups, int rows, int N, i
     a.a_cols = K, a.b_cols = wcols, a.b_rows = kk;
     a.groups = groups, a.offsets = offsets, a.most_tiles = (int)most;
     a.alpha = alpha, a.beta = beta;
-    a.vec_c = aligned(Y, 4 * size) && ldy % 4 == 0;
+    a.vec_c = vector_rows(Y, ldy, 0, size);
     return launch(k, a, blocks, 1, stream);
 }
 
@@ -207,7 +216,7 @@ extern "C" int sgemm_grouped_wgrad(int type, int groups, int rows, int M, int N,
     a.a_cols = M, a.b_cols = N;
     a.groups = groups, a.offsets = offsets;
     a.alpha = alpha, a.beta = beta;
-    a.vec_c = aligned(D, 4 * size) && ldd % 4 == 0 && stride_d % 4 == 0;
+    a.vec_c = vector_rows(D, ldd, stride_d, size);
     return launch(k, a, blocks, 1, stream);
 }
 
@@ -422,7 +431,7 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
     if (rows == 0) {  // no row: dW is zero
         a.C = dW, a.ldc = lddw;
         a.M = vocab, a.N = K;
-        a.vec_c = aligned(dW, 4 * size) && lddw % 4 == 0;
+        a.vec_c = vector_rows(dW, lddw, 0, size);
         const TileKernel k = kernel_for(type, F_DW, M64, true);
         return launch(k, a, ceil_div(vocab, k.bm) * ceil_div(K, k.bn), 1, stream);
     }
@@ -460,7 +469,7 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
             a.M = n, a.N = K, a.K = rows;
             a.a_cols = n8, a.b_cols = K, a.b_rows = rows;
             a.alpha = 1.f;
-            a.vec_c = aligned(dW, 4 * size) && lddw % 4 == 0;
+            a.vec_c = vector_rows(dW, lddw, 0, size);
             rc = launch(k, a, ceil_div(n, k.bm) * ceil_div(K, k.bn), 1, stream);
             if (rc) return rc;
         }
@@ -475,7 +484,7 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
             const TileKernel k = kernel_for(type, direct ? F_DX : F_PART, p.dx_tile, fast);
             if (direct) {
                 a.C = dX, a.ldc = lddx, a.alpha = 1.f;
-                a.vec_c = aligned(dX, 4 * size) && lddx % 4 == 0;
+                a.vec_c = vector_rows(dX, lddx, 0, size);
             } else {
                 a.C = p.sums ? static_cast<void *>(sums) : dX;
                 a.ldc = p.sums ? K : lddx;

@@ -8,11 +8,13 @@ TileKernel bf16_kernel(int form, int tile, bool fast)
 {
     if (!fast) {
         if (tile == S16) return tile_entry<bf16, 16, 64, 1, 4, 2, 16, 2, false>(form);
+        if (tile == M32) return tile_entry<bf16, 32, 128, 1, 4, 2, 16, 2, false>(form);
         if (tile == M64) return tile_entry<bf16, 64, 128, 2, 2, 2, 16, 2, false>(form);
         return tile_entry<bf16, 128, 128, 2, 2, 2, 16, 2, false>(form);
     }
     switch (tile) {
     case S16: return tile_entry<bf16, 16, 64, 1, 4, 4, 16, 4, true>(form);
+    case M32: return tile_entry<bf16, 32, 128, 1, 4, 4, 16, 2, true>(form);
     case M64: return tile_entry<bf16, 64, 128, 2, 2, 3, 16, 2, true>(form);
     case T128: return tile_entry<bf16, 128, 128, 2, 2, 2, 16, 2, true>(form);
     case T192: return tile_entry<bf16, 128, 192, 2, 2, 2, 16, 2, true>(form);

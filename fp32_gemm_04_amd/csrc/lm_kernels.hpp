@@ -7,7 +7,7 @@
 namespace sgemm {
 namespace lm {
 
-enum Tile { S16, M64, T128, T192, T256, NUM_TILES };
+enum Tile { S16, M32, M64, T128, T192, T256, NUM_TILES };
 // The operand layouts and epilogues of the products.
 enum Form {
     F_ROWS_T,   // grouped rows, weights N x K

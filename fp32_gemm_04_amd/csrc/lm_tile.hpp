@@ -31,8 +31,8 @@
 //       of one column: 16 lanes read 32 bytes of each of 4 rows.  With BL = 16 the two
 //       halves of 32 lanes are 8 rows apart, so 8 rows must differ in their 32-byte
 //       place; with BL = 32 they are neighbours, so 4 rows in their 64-byte place.
-//       fp32 operands need one k per lane and step: the lane groups read 64 (BL = 32:
-//       128) bytes of rows 4 apart.
+//       fp32 operands (BL = 16) need one k per lane and step: the lane groups read 64
+//       bytes of rows 4 apart.
 //
 // Both operands of a matrix instruction use the same assignment of k to lanes.
 // With blocks of BL = 16 and g = lane / 16, bf16 16x16x32 takes k = 8 g .. 8 g + 7, and
@@ -81,7 +81,7 @@ struct TileArgs {
     const int *offsets;          // groups + 1 row numbers (ROWS, SUM)
     int most_tiles;              // ROWS: row tiles that increasing offsets can give
     float alpha, beta;
-    int vec_c;                   // C's rows take vector stores
+    int vec_c;                   // C's rows take stores of 4 values (1), or of 8 bf16 (2)
     int accumulate;              // PART: add to what is there
     int split_k;                 // PART: contraction per z-slice (multiple of the slab)
     int64_t slice_stride;        // PART: elements between slices of C
@@ -171,8 +171,9 @@ struct Slab {
         if constexpr (RC <= 4)
             return 0;
         else if constexpr (std::is_same<T, float>::value) {
-            static_assert(L == KC || WHOLE, "fp32 slab rows are whole 256-byte groups");
-            return BL == 16 ? 4 * ((k >> 2) & 3) : 8 * ((k >> 2) & 1);
+            static_assert(BL == 16, "fp32 operands are read in blocks of 16");
+            // (128-byte rows have room for two places only: reads in pairs.)
+            return WHOLE ? 4 * ((k >> 2) & 3) : 4 * ((k >> 2) & 1);
         } else if constexpr (BL == 32) {
             return WHOLE ? 4 * (k & 3) : 4 * ((k >> 1) & 1);
         } else {
@@ -616,8 +617,22 @@ tile_kernel(TileArgs g)
     auto column = [&](int u) { return nw + BL * (u / GR) + 8 * (u % GR); };
     auto value = [&](int i, int u, int q) { return acc[i][u / GR][4 * (u % GR) + q]; };
     typedef T Vec __attribute__((ext_vector_type(4)));
+    // bf16 blocks of 32: two neighbouring groups of a row lie in a lane pair (l, l + 32) as
+    // columns 0-3, 8-11 and 4-7, 12-15; exchanged, each lane stores eight in a row, half as
+    // many and twice as wide stores.
+    constexpr bool PAIRED = BL == 32 && SZ == 2;
+    auto store_pair = [&](T *crow, int u, auto first, auto second) {
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        if constexpr (sizeof(first) == sizeof(u32x2)) {
+            const u32x2 x = __builtin_bit_cast(u32x2, first), y = __builtin_bit_cast(u32x2, second);
+            const auto p = __builtin_amdgcn_permlane32_swap(x[0], y[0], false, false);
+            const auto q = __builtin_amdgcn_permlane32_swap(x[1], y[1], false, false);
+            const int n = column(u) + 4 * lg;
+            *reinterpret_cast<u32x4 *>(crow + n) = u32x4{p[0], q[0], p[1], q[1]};
+        }
+    };
     // A tile inside C with vector stores takes copies without per-column tests.
-    const bool whole = n0 + BN <= g.N && g.vec_c;
+    const bool whole = n0 + BN <= g.N && g.vec_c >= (PAIRED ? 2 : 1);
     if constexpr (EP == STORE) {
         T *C = static_cast<T *>(g.C);
         if constexpr (RG == SUM) C += group * g.group_stride;
@@ -629,6 +644,19 @@ tile_kernel(TileArgs g)
                 const int m = mw + BL * i;
                 if (m >= row_end) continue;
                 T *crow = C + (int64_t)(row0 + m) * g.ldc;
+                if constexpr (PAIRED && decltype(inside)::value) {
+#pragma unroll
+                    for (int u = 0; u < FN * GR; u += 2) {
+                        Vec x, y;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            x[q] = (T)(alpha * value(i, u, q));
+                            y[q] = (T)(alpha * value(i, u + 1, q));
+                        }
+                        store_pair(crow, u, x, y);
+                    }
+                    continue;
+                }
 #pragma unroll
                 for (int u = 0; u < FN * GR; ++u) {
                     const int n = column(u);
@@ -707,6 +735,7 @@ tile_kernel(TileArgs g)
                 const bool counts = target >= 0 && target < g.vocab;
                 const int at = counts ? (int)target - g.col0 : INT32_MIN;
                 T *crow = C + (int64_t)m * g.ldc;
+                Vec before;
 #pragma unroll
                 for (int u = 0; u < FN * GR; ++u) {
                     const int n = column(u);
@@ -725,10 +754,16 @@ tile_kernel(TileArgs g)
                     for (int q = 0; q < 4; ++q)
                         out[q] = (T)(counts && (decltype(inside)::value || n + q < g.N) ? v[q] * w
                                                                                        : 0.f);
-                    // Columns up to the next multiple of 8 are written, as zero past N, so
-                    // that whole chunks can be read back.
-                    if (decltype(inside)::value || n < ((g.N + 7) & ~7))
+                    if constexpr (PAIRED && decltype(inside)::value) {
+                        if (u % 2 == 0)
+                            before = out;
+                        else
+                            store_pair(crow, u - 1, before, out);
+                    } else if (decltype(inside)::value || n < ((g.N + 7) & ~7)) {
+                        // Columns up to the next multiple of 8 are written, as zero past N,
+                        // so that whole chunks can be read back.
                         *reinterpret_cast<Vec *>(crow + n) = out;
+                    }
                 }
             }
         };

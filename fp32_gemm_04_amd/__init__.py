@@ -406,18 +406,24 @@ _current_stream = torch._C._cuda_getCurrentRawStream if hasattr(
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _run(call, device, stream, body):
+def _run(call, device, stream, operands, body):
     """body(stream handle) with ``device`` current and, where a stream is given,
-    with it current too, so that what body allocates belongs to that stream."""
+    with it current too, so that what body allocates belongs to that stream;
+    the operands' memory is then kept from reuse until that stream is past the call."""
     if stream is None and device.index == torch.cuda.current_device():
         rc = body(_current_stream(device.index))  # the usual case, without context managers
     else:
+        if stream is not None and stream.device != device:
+            raise ValueError("the stream is on %s, the operands on %s" % (stream.device, device))
         with torch.cuda.device(device):
             if stream is None:
                 rc = body(_current_stream(device.index))
             else:
                 with torch.cuda.stream(stream):
                     rc = body(stream.cuda_stream)
+                for t in operands:
+                    if t is not None:
+                        t.record_stream(stream)
     if rc != 0:
         raise SgemmError(rc, call)
 
@@ -450,7 +456,7 @@ def grouped_gemm(X, W, offsets, Y=None, trans: bool = False, alpha: float = 1.0,
             Y = torch.zeros((rows, N), dtype=X.dtype, device=dev)
         return _lib.sgemm_grouped(t, int(trans), groups, rows, N, K, alpha, X.data_ptr(), ldx,
                                   W.data_ptr(), ldw, _groups_of(W), beta, Y.data_ptr(), ldy, off, s)
-    _run("sgemm_grouped", dev, stream, body)
+    _run("sgemm_grouped", dev, stream, (X, W, offsets, Y), body)
     return Y
 
 
@@ -486,7 +492,7 @@ def grouped_wgrad(X, G, offsets, D=None, alpha: float = 1.0, beta: float = 0.0, 
         return _lib.sgemm_grouped_wgrad(t, groups, rows, M, N, alpha, X.data_ptr(), ldx,
                                         G.data_ptr(), ldg, beta, D.data_ptr(), ldd, _groups_of(D),
                                         off, s)
-    _run("sgemm_grouped_wgrad", dev, stream, body)
+    _run("sgemm_grouped_wgrad", dev, stream, (X, G, offsets, D), body)
     return D
 
 
@@ -521,7 +527,7 @@ def linear_cross_entropy(X, W, targets, stream=None):
         ws = torch.empty((n,), dtype=torch.uint8, device=dev)
         return _lib.sgemm_xent(t, rows, vocab, K, X.data_ptr(), ldx, W.data_ptr(), ldw, tg,
                                loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), n, s)
-    _run("sgemm_xent", dev, stream, body)
+    _run("sgemm_xent", dev, stream, (X, W, targets), body)
     return loss, lse
 
 
@@ -550,7 +556,7 @@ def linear_cross_entropy_backward(dloss, X, W, targets, lse, dX=None, dW=None, n
         return _lib.sgemm_xent_backward(t, rows, vocab, K, X.data_ptr(), ldx, W.data_ptr(), ldw, tg,
                                         pl, pd, dX.data_ptr() if need_dX else 0, lddx,
                                         dW.data_ptr() if need_dW else 0, lddw, ws.data_ptr(), n, s)
-    _run("sgemm_xent_backward", dev, stream, body)
+    _run("sgemm_xent_backward", dev, stream, (dloss, X, W, targets, lse, dX, dW), body)
     return dX, dW
 
 
@@ -593,7 +599,7 @@ def q4_quantize(W, block: int = 128, zeros: bool = True, stream=None):
         Z = torch.empty(lead + (N, blocks), dtype=torch.uint8, device=dev) if zeros else None
         return _lib.sgemm_q4_quantize(t, rows, K, block, W.data_ptr(), ldw, Q.data_ptr(),
                                       S.data_ptr(), Z.data_ptr() if zeros else 0, s)
-    _run("sgemm_q4_quantize", dev, stream, body)
+    _run("sgemm_q4_quantize", dev, stream, (W,), body)
     return Q, S, Z
 
 
@@ -631,5 +637,5 @@ def q4_matvec(X, Q, scales, zeros=None, block: int = 128, Y=None, offsets=None, 
             Y = new((rows, N), dtype=X.dtype, device=dev)
         return _lib.sgemm_q4_matvec(t, groups, rows, N, K, block, X.data_ptr(), ldx, pq, ps, pz,
                                     Y.data_ptr(), ldy, off, s)
-    _run("sgemm_q4_matvec", dev, stream, body)
+    _run("sgemm_q4_matvec", dev, stream, (X, Q, scales, zeros, Y, offsets), body)
     return Y

@@ -15,6 +15,12 @@ namespace sgemm {
 namespace lm {
 namespace {
 
+// Without a device, sizes are those of a whole MI355X (the call then fails).
+constexpr int kNoDeviceUnits = 256;
+
+// Largest extent taken: tile edges past the end of a matrix stay within int.
+constexpr int kMostExtent = INT_MAX - 1024;
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 int elem_size(int type) { return type == SGEMM_TYPE_BF16 ? 2 : 4; }
@@ -125,9 +131,9 @@ extern "C" int sgemm_grouped(int type, int trans, int groups, int rows, int N, i
     if (type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16) return -1;
     if (trans != 0 && trans != 1) return -2;
     if (groups < 0) return -3;
-    if (rows < 0) return -4;
-    if (N < 0) return -5;
-    if (K < 0) return -6;
+    if (rows < 0 || rows > kMostExtent) return -4;
+    if (N < 0 || N > kMostExtent) return -5;
+    if (K < 0 || K > kMostExtent) return -6;
     const int size = elem_size(type);
     const bool work = groups > 0 && rows > 0 && N > 0;
     const bool reads = work && K > 0 && alpha != 0.f;
@@ -179,9 +185,9 @@ extern "C" int sgemm_grouped_wgrad(int type, int groups, int rows, int M, int N,
 {
     if (type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16) return -1;
     if (groups < 0) return -2;
-    if (rows < 0) return -3;
-    if (M < 0) return -4;
-    if (N < 0) return -5;
+    if (rows < 0 || rows > kMostExtent) return -3;
+    if (M < 0 || M > kMostExtent) return -4;
+    if (N < 0 || N > kMostExtent) return -5;
     const int size = elem_size(type);
     const bool work = groups > 0 && M > 0 && N > 0;
     const bool reads = work && rows > 0 && alpha != 0.f;
@@ -327,20 +333,23 @@ XentPlan xent_plan(int type, bool fast, int rows, int vocab, int K, int cus)
     return p;
 }
 
-// Row statistics of the narrowest tile's columns, so that the workspace fits
-// whichever tile runs, and each row's value at its target.
-int64_t stats_bytes(int rows, int vocab)
+// Each row's value at its target, and its statistics over the columns of each tile, of
+// the narrower of the tiles that run with and without direct loads.
+int64_t stats_bytes(int type, int rows, int vocab, int K, int cus)
 {
-    return round_up((int64_t)rows * 4, 256) + (int64_t)rows * ceil_div(vocab, 64) * 8;
+    const TileCost *t = type == SGEMM_TYPE_BF16 ? kBf16Tiles : kF32Tiles;
+    const int a = t[plain_tile(type, true, rows, vocab, K, cus)].bn;
+    const int b = t[plain_tile(type, false, rows, vocab, K, cus)].bn;
+    return round_up((int64_t)rows * 4, 256) + (int64_t)rows * ceil_div(vocab, a < b ? a : b) * 8;
 }
 
 int check_xent(int type, int rows, int vocab, int K, const void *X, int ldx, const void *W, int ldw,
                const int64_t *targets)
 {
     if (type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16) return -1;
-    if (rows < 0) return -2;
-    if (vocab < 0 || (vocab == 0 && rows > 0)) return -3;
-    if (K < 0) return -4;
+    if (rows < 0 || rows > kMostExtent) return -2;
+    if (vocab < 0 || vocab > kMostExtent || (vocab == 0 && rows > 0)) return -3;
+    if (K < 0 || K > kMostExtent) return -4;
     const int size = elem_size(type);
     const bool reads = rows > 0 && K > 0;
     if ((reads && !X) || !aligned(X, size)) return -5;
@@ -359,15 +368,15 @@ int check_xent(int type, int rows, int vocab, int K, const void *X, int ldx, con
 extern "C" int64_t sgemm_xent_workspace(int type, int rows, int vocab, int K, int backward)
 {
     if (type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16) return -1;
-    if (rows < 0) return -2;
-    if (vocab < 0) return -3;
-    if (K < 0) return -4;
+    if (rows < 0 || rows > kMostExtent) return -2;
+    if (vocab < 0 || vocab > kMostExtent) return -3;
+    if (K < 0 || K > kMostExtent) return -4;
     if (backward != 0 && backward != 1) return -5;
     if (rows == 0 || vocab == 0) return 0;
-    if (!backward) return stats_bytes(rows, vocab);
     int rc = 0;
     int cus = compute_units(&rc);
-    if (cus == 0) cus = 256;  // no device: the plan of a whole MI355X
+    if (cus == 0) cus = kNoDeviceUnits;
+    if (!backward) return stats_bytes(type, rows, vocab, K, cus);
     // Whichever operands the call gets.
     const int64_t a = xent_plan(type, true, rows, vocab, K, cus).bytes;
     const int64_t b = xent_plan(type, false, rows, vocab, K, cus).bytes;
@@ -383,10 +392,9 @@ extern "C" int sgemm_xent(int type, int rows, int vocab, int K, const void *X, i
     if ((rows > 0 && !lse) || !aligned(lse, 4)) return -11;
     if ((rows > 0 && !ws) || !aligned(ws, 16)) return -12;
     if (rows == 0) return 0;
-    if (ws_bytes < stats_bytes(rows, vocab)) return -13;
-
     int rc = 0;
     const int cus = compute_units(&rc);
+    if (ws_bytes < stats_bytes(type, rows, vocab, K, cus ? cus : kNoDeviceUnits)) return -13;
     if (cus == 0) return rc;
     const int size = elem_size(type);
     const bool fast = K == 0 || (fast_operand(X, ldx, 0, size) &&
@@ -426,7 +434,6 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
     if (K == 0 || vocab == 0 || (!dX && !dW) || (rows == 0 && !dW)) return 0;
     int rc = 0;
     const int cus = compute_units(&rc);
-    if (cus == 0) return rc;
     TileArgs a = {};
     if (rows == 0) {  // no row: dW is zero
         a.C = dW, a.ldc = lddw;
@@ -436,8 +443,9 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
         return launch(k, a, ceil_div(vocab, k.bm) * ceil_div(K, k.bn), 1, stream);
     }
     const bool fast_x = fast_operand(X, ldx, 0, size), fast_w = fast_operand(W, ldw, 0, size);
-    const XentPlan p = xent_plan(type, fast_w, rows, vocab, K, cus);
+    const XentPlan p = xent_plan(type, fast_w, rows, vocab, K, cus ? cus : kNoDeviceUnits);
     if (ws_bytes < p.bytes) return -17;
+    if (cus == 0) return rc;
     float *sums = reinterpret_cast<float *>(static_cast<char *>(ws) + p.d_bytes);
 
     for (int64_t c = 0; c < p.pieces; ++c) {

@@ -14,6 +14,9 @@ namespace sgemm {
 namespace q4 {
 namespace {
 
+// Largest extents taken: a workgroup's offsets stay within 32 bits.
+constexpr int kMostExtent = INT_MAX - 1024, kMostK = 1 << 27;
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool aligned(const void *p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
@@ -83,9 +86,9 @@ extern "C" int sgemm_q4_matvec(int type, int groups, int rows, int N, int K, int
 {
     if (type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16) return -1;
     if (groups < 0 || (!offsets && groups != 1) || groups > 65535) return -2;
-    if (rows < 0) return -3;
-    if (N < 0) return -4;
-    if (K < 0 || K % 2 != 0) return -5;
+    if (rows < 0 || rows > kMostExtent) return -3;
+    if (N < 0 || N > kMostExtent) return -4;
+    if (K < 0 || K % 2 != 0 || K > kMostK) return -5;
     if (block != 32 && block != 64 && block != 128) return -6;
     const int size = type == SGEMM_TYPE_BF16 ? 2 : 4;
     const bool work = groups > 0 && rows > 0 && N > 0, reads = work && K > 0;
@@ -151,8 +154,8 @@ extern "C" int sgemm_q4_matvec(int type, int groups, int rows, int N, int K, int
     while (slab < K && fits(slab * 2)) slab *= 2;
     a.slab_log2 = __builtin_ctzll((unsigned long long)slab);
     a.vec_x = aligned(X, 16) && (int64_t)ldx * size % 16 == 0;
-    // Whole 16-byte pieces of rows, and offsets inside a workgroup below 2^31.
-    const bool al = K % 32 == 0 && aligned(Q, 16) && K < (1 << 23);
+    // Direct loads: rows at 4-byte addresses, and offsets inside a workgroup below 2^31.
+    const bool al = K % 8 == 0 && aligned(Q, 4) && K < (1 << 23);
     const Q4Fn fn = type == SGEMM_TYPE_BF16 ? kernel_for<bf16>(block, al, f)
                                             : kernel_for<float>(block, al, f);
     const int staged = ring_bytes(f.nt) + bytes(slab, cols);
@@ -167,8 +170,8 @@ extern "C" int sgemm_q4_quantize(int type, int N, int K, int block, const void *
                                  uint8_t *Q, void *S, uint8_t *Z, hipStream_t stream)
 {
     if (type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16) return -1;
-    if (N < 0) return -2;
-    if (K < 0 || K % 2 != 0) return -3;
+    if (N < 0 || N > kMostExtent) return -2;
+    if (K < 0 || K % 2 != 0 || K > kMostK) return -3;
     if (block != 32 && block != 64 && block != 128) return -4;
     const int size = type == SGEMM_TYPE_BF16 ? 2 : 4;
     const bool work = N > 0 && K > 0;

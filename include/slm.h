@@ -15,6 +15,8 @@
  * caller's, one per call in flight (also one per captured graph that may run
  * beside another).
  *
+ * Extents are at most 2^31 - 1025.
+ *
  * Types.  Matrices hold fp32 or bf16 values (one type per call); every sum is
  * held in fp32, and a bf16 result is rounded once, to nearest even.
  * Pointers need the alignment of their element.  Rows at 4-byte addresses
@@ -154,7 +156,7 @@ int64_t sgemm_xent_workspace(int type, int rows, int vocab, int K, int backward)
  *
  *   type      enum sgemm_type of X, S and Y
  *   groups    sets of weights (1 when offsets is NULL), at most 65535
- *   rows, N, K   K even
+ *   rows, N, K   K even, at most 2^27
  *   block     weights along K that share a scale and a zero: 32, 64 or 128; the
  *             last block of a row may be short
  *   X, ldx    rows x K

@@ -41,8 +41,12 @@ def call(fn, good, kw):
     ("sgemm_grouped", GROUPED, dict(stride_w=-1), -12), ("sgemm_grouped", GROUPED, dict(Y=0), -14),
     ("sgemm_grouped", GROUPED, dict(ldy=31), -15), ("sgemm_grouped", GROUPED, dict(offsets=0), -16),
     ("sgemm_grouped", GROUPED, dict(offsets=16386), -16),
-    ("sgemm_grouped", GROUPED, dict(rows=2 ** 31 - 1, N=2 ** 31 - 1, ldw=2 ** 31 - 1,
+    ("sgemm_grouped", GROUPED, dict(rows=2 ** 31 - 1025, N=2 ** 31 - 1025, ldw=2 ** 31 - 1,
                                     ldy=2 ** 31 - 1), -5),
+    ("sgemm_grouped", GROUPED, dict(rows=2 ** 31 - 1024), -4),
+    ("sgemm_grouped", GROUPED, dict(K=2 ** 31 - 1024), -6),
+    ("sgemm_grouped_wgrad", WGRAD, dict(M=2 ** 31 - 1024), -4),
+    ("sgemm_xent", XENT, dict(vocab=2 ** 31 - 1024), -3),
     ("sgemm_grouped_wgrad", WGRAD, dict(type=-1), -1),
     ("sgemm_grouped_wgrad", WGRAD, dict(groups=-1), -2),
     ("sgemm_grouped_wgrad", WGRAD, dict(rows=-1), -3),
@@ -65,10 +69,12 @@ def call(fn, good, kw):
     ("sgemm_xent_backward", BACK, dict(dX=20482), -12),
     ("sgemm_xent_backward", BACK, dict(lddx=15), -13),
     ("sgemm_xent_backward", BACK, dict(dW=24577), -14),
+    ("sgemm_xent_backward", BACK, dict(ws_bytes=16), -17),
     ("sgemm_xent_backward", BACK, dict(lddw=15), -15), ("sgemm_xent_backward", BACK, dict(ws=0), -16),
     ("sgemm_q4_matvec", Q4, dict(type=3), -1), ("sgemm_q4_matvec", Q4, dict(groups=2), -2),
     ("sgemm_q4_matvec", Q4, dict(groups=65536, offsets=16384), -2),
     ("sgemm_q4_matvec", Q4, dict(rows=-1), -3), ("sgemm_q4_matvec", Q4, dict(N=-1), -4),
+    ("sgemm_q4_matvec", Q4, dict(K=2 ** 27 + 2, ldx=2 ** 28), -5),
     ("sgemm_q4_matvec", Q4, dict(K=63), -5), ("sgemm_q4_matvec", Q4, dict(block=16), -6),
     ("sgemm_q4_matvec", Q4, dict(X=0), -7), ("sgemm_q4_matvec", Q4, dict(ldx=63), -8),
     ("sgemm_q4_matvec", Q4, dict(Q=0), -9), ("sgemm_q4_matvec", Q4, dict(S=1), -10),

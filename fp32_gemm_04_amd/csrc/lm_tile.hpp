@@ -117,6 +117,16 @@ __device__ __forceinline__ void load_slab16(u32x4 rsrc, uint32_t voff, uint32_t 
                  : "memory", "m0");
 }
 
+// voff leaves every descriptor's range unless k < left.  In assembly, like the loads that
+// hold voff: compiled code never touches an address register while a load is in flight.
+__device__ __forceinline__ void leave_range(uint32_t &voff, int k, int left)
+{
+    asm volatile("v_cmp_gt_i32_e32 vcc, %2, %1\n\tv_cndmask_b32_e32 %0, %3, %0, vcc"
+                 : "+v"(voff)
+                 : "v"(k), "s"(left), "v"(0x80000000u)
+                 : "vcc");
+}
+
 template <int N>
 __device__ __forceinline__ void wait_slab_barrier()
 {
@@ -466,7 +476,7 @@ tile_kernel(TileArgs g)
                 for (int i = 0; i < LPW; ++i) {
                     int row, chunk;
                     slot(i, row, chunk);
-                    if ((ua[i] ? LA : LB) == KC && chunk * EPC >= kleft) voff[i] = kOutside;
+                    if ((ua[i] ? LA : LB) == KC) leave_range(voff[i], chunk * EPC, kleft);
                 }
             }
             // Wait states between a vector unit's write of a descriptor and its use.

@@ -229,10 +229,11 @@ __attribute__((amdgpu_waves_per_eu(RT <= 2 ? 4 : 2))) q4_kernel(Q4Args g)
             // Rows past N, and chunks past K, are outside the descriptor.
             const int64_t left = c < chunks ? (int64_t)(g.N - n_wg) * row_bytes - c * 64 : 0;
             u32x4 r = lm::descriptor(reinterpret_cast<const char *>(Q) + (int64_t)c * 64, left);
-            asm volatile("s_nop 4" : "+s"(r));
+            uint32_t at = __builtin_amdgcn_readfirstlane(ring_at + d * (NT * 1024));
+            // Wait states between a vector unit's write of a scalar and a load's use of it.
+            asm volatile("s_nop 4" : "+s"(r), "+s"(at));
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                lm::load_slab16(r, voff[t], ring_at + (d * NT + t) * 1024);
+            for (int t = 0; t < NT; ++t) lm::load_slab16(r, voff[t], at + t * 1024);
         } else {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {

@@ -260,9 +260,10 @@ __global__ void __launch_bounds__(256) xent_join_kernel(int rows, int tiles, int
     }
 }
 
-// dX <- the slices' fp32 sums added in order, rounded once; four columns a thread.
+// dX <- the slices' fp32 sums added in order, each with its remainders' sum low_rows further
+// on, rounded once; four columns a thread.
 template <typename T>
-__global__ void __launch_bounds__(256) xent_sum_kernel(int rows, int K, int slices,
+__global__ void __launch_bounds__(256) xent_sum_kernel(int rows, int low_rows, int K, int slices,
                                                        int64_t slice_stride, const float *parts,
                                                        T *dX, int64_t lddx)
 {
@@ -272,17 +273,18 @@ __global__ void __launch_bounds__(256) xent_sum_kernel(int rows, int K, int slic
         const float *p = parts + (int64_t)row * K + c;
         const int n = K - c < 4 ? K - c : 4;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (K % 4 == 0) {  // 16-byte rows
-            for (int s = 0; s < slices; ++s, p += slice_stride) {
-                const f32x4 x = *reinterpret_cast<const f32x4 *>(p);
+        const int64_t low = (int64_t)low_rows * K;
+        for (int s = 0; s < slices; ++s, p += slice_stride) {
+            if (K % 4 == 0) {  // 16-byte rows
+                f32x4 x = *reinterpret_cast<const f32x4 *>(p);
+                if (low_rows) x += *reinterpret_cast<const f32x4 *>(p + low);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[q] += x[q];
-            }
-        } else {
-            for (int s = 0; s < slices; ++s, p += slice_stride)
+            } else {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    if (q < n) v[q] += p[q];
+                    if (q < n) v[q] += low_rows ? p[q] + p[q + low] : p[q];
+            }
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -296,6 +298,7 @@ __global__ void __launch_bounds__(256) xent_sum_kernel(int rows, int K, int slic
 struct XentPlan {
     int64_t piece, pieces, ld;  // ld: leading dimension of the piece's derivatives
     int slices, dx_tile;
+    int low_rows, d_rows;       // rows to the rounding's remainders (0: not kept); rows in all
     bool sums;                  // dX goes through fp32 sums in the workspace
     int64_t d_bytes, bytes;
 };
@@ -313,23 +316,34 @@ XentPlan xent_plan(int type, bool fast, int rows, int vocab, int K, int cus)
     p.piece = round_up(ceil_div(vocab, p.pieces), 256);
     p.pieces = ceil_div(vocab, p.piece);
     p.ld = p.piece + 64;
-    p.d_bytes = round_up((int64_t)rows * p.ld * size, 256);
+    // Few rows: a row's gradient is mostly one derivative's (its target's), whose rounding
+    // to bf16 would shift the whole row by up to 2^-8.  So what the rounding leaves over is
+    // kept as further rows; with many rows the roundings average out (T 384: 0.0022 off
+    // against 0.0017 of an fp32 sum rounded once; one row: 0.0034), and here the time is
+    // that of reading W and writing dW, whatever the rows.
+    p.low_rows = type != SGEMM_TYPE_BF16 || rows > 128 ? 0
+                 : rows <= 8                           ? 8
+                 : rows <= 16                          ? 16
+                 : rows <= 32                          ? 32
+                                                       : (int)round_up(rows, 64);
+    p.d_rows = p.low_rows ? 2 * p.low_rows : rows;
+    p.d_bytes = round_up((int64_t)p.d_rows * p.ld * size, 256);
     // dX may have few tiles and a long sum: where its tiles would not fill the compute
     // units, the tile is chosen as if the sum were cut as finely as it may be (1024
     // columns a slice), and cut until each unit has two.
     const int64_t most_slices = p.piece / 1024 < 1 ? 1 : p.piece / 1024 > 64 ? 64 : p.piece / 1024;
-    p.dx_tile = plain_tile(type, fast, rows, K, p.piece, cus);
+    p.dx_tile = plain_tile(type, fast, p.d_rows, K, p.piece, cus);
     p.slices = 1;
-    if (ceil_div(rows, 128) * ceil_div(K, 128) < cus) {
+    if (ceil_div(p.d_rows, 128) * ceil_div(K, 128) < cus) {
         p.dx_tile = choose_tile(
-            type, fast, [&](int bm) { return ceil_div(rows, bm) * most_slices; }, K,
+            type, fast, [&](int bm) { return ceil_div(p.d_rows, bm) * most_slices; }, K,
             p.piece / most_slices, cus);
         const TileCost &t = (type == SGEMM_TYPE_BF16 ? kBf16Tiles : kF32Tiles)[p.dx_tile];
-        const int64_t s = 2 * cus / (ceil_div(rows, t.bm) * ceil_div(K, t.bn));
+        const int64_t s = 2 * cus / (ceil_div(p.d_rows, t.bm) * ceil_div(K, t.bn));
         p.slices = (int)(s < 1 ? 1 : s > most_slices ? most_slices : s);
     }
-    p.sums = p.slices > 1 || (p.pieces > 1 && type != SGEMM_TYPE_F32);
-    p.bytes = p.d_bytes + (p.sums ? (int64_t)p.slices * rows * K * 4 : 0);
+    p.sums = p.low_rows > 0 || p.slices > 1 || (p.pieces > 1 && type != SGEMM_TYPE_F32);
+    p.bytes = p.d_bytes + (p.sums ? (int64_t)p.slices * p.d_rows * K * 4 : 0);
     return p;
 }
 
@@ -455,7 +469,9 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
         const char *Wc = static_cast<const char *>(W) + col0 * ldw * size;
         {
             const bool fast = fast_x && fast_w;
-            const int tile = plain_tile(type, fast, rows, n, K, cus);
+            const int stored = p.low_rows ? p.low_rows : rows;
+            int tile = plain_tile(type, fast, stored, n, K, cus);
+            if (p.low_rows && tile == T256) tile = T192;  // the 256 tile keeps no remainders
             const TileKernel k = kernel_for(type, F_GRAD, tile, fast);
             a = TileArgs{};
             a.A = X, a.B = Wc, a.C = ws;
@@ -464,18 +480,20 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
             a.a_cols = a.b_cols = K;
             a.targets = targets, a.lse = lse, a.dloss = dloss;
             a.col0 = (int)col0, a.vocab = vocab;
-            rc = launch(k, a, ceil_div(rows, k.bm) * ceil_div(n, k.bn), 1, stream);
+            a.store_rows = stored, a.low_rows = p.low_rows;
+            rc = launch(k, a, ceil_div(stored, k.bm) * ceil_div(n, k.bn), 1, stream);
             if (rc) return rc;
         }
         if (dW) {
             const bool fast = fast_x;
-            const int tile = plain_tile(type, fast, n, K, rows, cus);
+            const int tile = plain_tile(type, fast, n, K, p.d_rows, cus);
             const TileKernel k = kernel_for(type, F_DW, tile, fast);
             a = TileArgs{};
             a.A = ws, a.B = X, a.C = static_cast<char *>(dW) + col0 * lddw * size;
             a.lda = p.ld, a.ldb = ldx, a.ldc = lddw;
-            a.M = n, a.N = K, a.K = rows;
+            a.M = n, a.N = K, a.K = p.d_rows;
             a.a_cols = n8, a.b_cols = K, a.b_rows = rows;
+            a.wrap = p.low_rows;
             a.alpha = 1.f;
             a.vec_c = vector_rows(dW, lddw, 0, size);
             rc = launch(k, a, ceil_div(n, k.bm) * ceil_div(K, k.bn), 1, stream);
@@ -486,7 +504,7 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
             a = TileArgs{};
             a.A = ws, a.B = Wc;
             a.lda = p.ld, a.ldb = ldw;
-            a.M = rows, a.N = K, a.K = n;
+            a.M = p.d_rows, a.N = K, a.K = n;
             a.a_cols = n8, a.b_cols = K, a.b_rows = n;
             const bool direct = !p.sums && p.pieces == 1;
             const TileKernel k = kernel_for(type, direct ? F_DX : F_PART, p.dx_tile, fast);
@@ -499,21 +517,21 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
                 a.vec_c = aligned(a.C, 16) && a.ldc % 4 == 0;
                 a.accumulate = c > 0;
                 a.split_k = (int)round_up(ceil_div(n, p.slices), 64);
-                a.slice_stride = (int64_t)rows * K;
+                a.slice_stride = (int64_t)p.d_rows * K;
             }
-            rc = launch(k, a, ceil_div(rows, k.bm) * ceil_div(K, k.bn), direct ? 1 : p.slices,
+            rc = launch(k, a, ceil_div(p.d_rows, k.bm) * ceil_div(K, k.bn), direct ? 1 : p.slices,
                         stream);
             if (rc) return rc;
         }
     }
     if (dX && p.sums) {
         const dim3 grid((unsigned)ceil_div(K, 1024), (unsigned)(rows < 65535 ? rows : 65535));
-        const int64_t stride = (int64_t)rows * K;
+        const int64_t stride = (int64_t)p.d_rows * K;
         if (type == SGEMM_TYPE_BF16)
-            xent_sum_kernel<bf16><<<grid, dim3(256), 0, stream>>>(rows, K, p.slices, stride, sums,
+            xent_sum_kernel<bf16><<<grid, dim3(256), 0, stream>>>(rows, p.low_rows, K, p.slices, stride, sums,
                                                                   static_cast<bf16 *>(dX), lddx);
         else
-            xent_sum_kernel<float><<<grid, dim3(256), 0, stream>>>(rows, K, p.slices, stride, sums,
+            xent_sum_kernel<float><<<grid, dim3(256), 0, stream>>>(rows, p.low_rows, K, p.slices, stride, sums,
                                                                    static_cast<float *>(dX), lddx);
         return (int)hipGetLastError();
     }

@@ -91,6 +91,12 @@ struct TileArgs {
     float *parts;                // STATS: (maximum, sum) of [row][tile along N]
     float *target_value;
     int col0, vocab;
+    // GRAD, split: rows written (those from M on as zeros), and the distance in rows to
+    // what rounding each derivative to bf16 leaves over, written as rows of their own (0:
+    // not kept).  Sums over both (A MC): B starts over after `wrap` rows, a power of two
+    // below a slab's rows or a multiple of them (0: never).
+    int store_rows, low_rows;
+    int wrap;
 };
 
 typedef void (*TileFn)(TileArgs);
@@ -347,7 +353,8 @@ tile_kernel(TileArgs g)
         end = __builtin_amdgcn_readfirstlane(end);
         tm = __builtin_amdgcn_readfirstlane(tm);
     } else {
-        const int tiles_m = (g.M + BM - 1) / BM, tiles_n = (g.N + BN - 1) / BN;
+        const int tiles_m = ((EP == GRAD ? g.store_rows : g.M) + BM - 1) / BM;
+        const int tiles_n = (g.N + BN - 1) / BN;
         int bid = blockIdx.x;
         if constexpr (RG == SUM) {
             const int per = tiles_m * tiles_n;
@@ -460,10 +467,12 @@ tile_kernel(TileArgs g)
         for (int i = 0; i < LPW; ++i) {
             int row, chunk;
             slot(i, row, chunk);
+            if (RG == PLAIN && LA == MC && !ua[i] && g.wrap > 0 && g.wrap < BK) row &= g.wrap - 1;
             voff[i] = (uint32_t)row * (uint32_t)((ua[i] ? g.lda : g.ldb) * SZ) + (uint32_t)chunk * 16u;
         }
         const uint32_t base = (uint32_t)(uintptr_t)(lds_char *)lds;
         int kleft = K;  // of the next slab to issue
+        int issued = 0;
         u32x4 ra, rb;
         auto next_slab = [&]() {  // descriptors of the slab whose loads come next
             ra = descriptor(pa, LA == MC ? left_a : kleft > 0 ? left_a : 0);
@@ -494,6 +503,12 @@ tile_kernel(TileArgs g)
             left_a -= step_a;
             left_b -= step_b;
             kleft -= BK;
+            if constexpr (RG == PLAIN && LA == MC) {
+                if (++issued * BK == g.wrap) {
+                    pb -= issued * step_b;
+                    left_b += issued * step_b;
+                }
+            }
         };
         // Half a slab ahead: while the products of one half run, the operands of the
         // next are read.  In the middle of slab t every wave has read all of it, so
@@ -572,7 +587,8 @@ tile_kernel(TileArgs g)
                 const bool kc = (ua[i] ? LA : LB) == KC;
                 const int64_t ld = ua[i] ? g.lda : g.ldb;
                 const int rows = ua[i] ? a_rows : b_rows;
-                const int r = kc ? row : t * BK + row;
+                int r = kc ? row : t * BK + row;
+                if (RG == PLAIN && LA == MC && !ua[i] && g.wrap > 0) r %= g.wrap;
                 const int c = kc ? t * BK + chunk * EPC : chunk * EPC;
                 // First value outside, along the contiguous index.
                 const int lim = kc ? K : ua[i] ? g.M - m0 : g.N - n0;
@@ -733,14 +749,14 @@ tile_kernel(TileArgs g)
         // fma and one instruction for the power.  For fp32 the rounding of lse log2 e
         // is carried along (low); bf16's own rounding hides it.
         T *C = static_cast<T *>(g.C);
-        auto store = [&](auto inside) {
+        auto store = [&](auto inside, auto split) {
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
                 __builtin_amdgcn_sched_barrier(0);
                 const int m = mw + BL * i;
-                if (m >= g.M) continue;
-                const int64_t target = g.targets[m];
-                const float w = g.dloss[m], lse = g.lse[m];
+                if (m >= g.store_rows) continue;
+                const int64_t target = m < g.M ? g.targets[m] : -1;
+                const float w = m < g.M ? g.dloss[m] : 0.f, lse = m < g.M ? g.lse[m] : 0.f;
                 const float high = lse * kLog2e, low = fmaf(lse, kLog2e, -high);
                 const bool counts = target >= 0 && target < g.vocab;
                 const int at = counts ? (int)target - g.col0 : INT32_MIN;
@@ -761,9 +777,17 @@ tile_kernel(TileArgs g)
                         for (int q = 0; q < 4; ++q) v[q] -= at - n == q ? 1.f : 0.f;
                     Vec out;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        out[q] = (T)(counts && (decltype(inside)::value || n + q < g.N) ? v[q] * w
-                                                                                       : 0.f);
+                    for (int q = 0; q < 4; ++q) {
+                        v[q] = counts && (decltype(inside)::value || n + q < g.N) ? v[q] * w : 0.f;
+                        out[q] = (T)v[q];
+                    }
+                    if constexpr (decltype(split)::value) {
+                        Vec low;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) low[q] = (T)(v[q] - (float)out[q]);
+                        if (n < ((g.N + 7) & ~7))
+                            *reinterpret_cast<Vec *>(crow + g.low_rows * g.ldc + n) = low;
+                    }
                     if constexpr (PAIRED && decltype(inside)::value) {
                         if (u % 2 == 0)
                             before = out;
@@ -777,10 +801,16 @@ tile_kernel(TileArgs g)
                 }
             }
         };
+        if constexpr (std::is_same<T, bf16>::value && BM * BN < 256 * 256) {
+            if (g.low_rows) {
+                store(std::false_type{}, std::true_type{});
+                return;
+            }
+        }
         if (n0 + BN <= g.N)
-            store(std::true_type{});
+            store(std::true_type{}, std::false_type{});
         else
-            store(std::false_type{});
+            store(std::false_type{}, std::false_type{});
     }
     if constexpr (EP == STATS) {
         // Row maximum and sum over this wave's columns, then over the waves of the

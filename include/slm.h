@@ -124,9 +124,11 @@ int sgemm_xent(int type, int rows, int vocab, int K, const void *X, int ldx, con
  * (0 in rows that do not count, whatever z holds):
  *     dX[t][k] = sum_v d[t][v] W[v][k]      dW[v][k] = sum_t d[t][v] X[t][k]
  * The logits are computed again, a piece of the vocabulary at a time; d is
- * held in `type` for one piece (bf16 rounds each d once, to 2^-9 of itself,
- * which is what a stored gradient of that type carries), and both products
- * sum in fp32 over all pieces.
+ * held in `type` for one piece (bf16 rounds each d once, by at most 2^-8 of
+ * itself, as a stored gradient of that type would; with up to 128 rows, where the
+ * roundings would not average out, what they leave over is kept beside it), and
+ * both products sum in fp32 over all pieces.  A row that does not count adds 0 *
+ * X[t][k] to dW: X must be finite there.
  *
  *   lse       as sgemm_xent gave it
  *   dloss     rows floats, the gradient of each row's loss

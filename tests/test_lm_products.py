@@ -204,10 +204,10 @@ def check_loss(X, W, targets, loss, lse):
     assert ((loss.double() - ref_loss).abs() <= tol).all()
 
 
-def check_gradients(X, W, targets, dloss, dX, dW):
+def check_gradients(X, W, targets, dloss, dX, dW, half_d=None):
     """d is off by a relative eps_d = e + 2^-23 |z - lse| + 4 2^-24 (exponent and its argument,
-    e as above for the logit and again for lse), and rounded to the type: 2^-8 for bf16.
-    The sums over V or T then add (n + 2) 2^-24."""
+    e as above for the logit and again for lse), and rounded to the type: 2^-8 for bf16
+    (half_d: less).  The sums over V or T then add (n + 2) 2^-24."""
     z, _, lse, d = xent_reference(X, W, targets, dloss)
     K, V, T = X.shape[1], W.shape[0], X.shape[0]
     half = 2.0 ** -8 if X.dtype == BF16 else 0.0
@@ -215,7 +215,7 @@ def check_gradients(X, W, targets, dloss, dX, dW):
     p = (z - lse[:, None]).exp() * dloss.double()[:, None].abs()
     counts = ((targets >= 0) & (targets < V))[:, None]
     off = 2 * e + ((z - lse[:, None]).abs() + (V + 16) / 2 + 2 * lse[:, None].abs()) * 2.0 ** -23
-    dd = torch.where(counts, p * off, torch.zeros_like(p)) + d.abs() * (half + 2.0 ** -22)
+    dd = torch.where(counts, p * off, torch.zeros_like(p)) + d.abs() * ((half if half_d is None else half_d) + 2.0 ** -22)
     for out, a, b, n, what in ((dX, (d, dd), W.double(), V, "dX"), (dW, (d.t(), dd.t()), X.double(), T, "dW")):
         if out is None:
             continue

@@ -83,6 +83,21 @@ def test_xent_in_several_pieces(dtype):
     check(dW, ref, mag, (off * 2.0 ** 24) + T + 2, "dW")
 
 
+@pytest.mark.parametrize("T", [1, 2, 8, 9, 16, 31, 33, 64, 65, 128, 129])
+@pytest.mark.parametrize("K", [64, 75])
+def test_xent_few_rows_keep_their_derivatives(T, K):
+    """bf16 with up to 128 rows: each derivative keeps 16 bits (its rounding, 2^-8 of itself,
+    and that of the remainder, 2^-8 of at most that), so that the gradients are those of
+    unrounded derivatives rounded once; from 129 rows on, each derivative is rounded."""
+    V = 700
+    X, W = rand((T, K), BF16, 1), rand((V, K), BF16, 2, 2.0 / K ** 0.5)
+    targets = torch.randint(0, V, (T,), device="cuda")
+    loss, lse = sg.linear_cross_entropy(X, W, targets)
+    dloss = torch.rand(T, device="cuda") + 0.1
+    dX, dW = sg.linear_cross_entropy_backward(dloss, X, W, targets, lse)
+    check_gradients(X, W, targets, dloss, dX, dW, half_d=2.0 ** -16 if T <= 128 else 2.0 ** -8)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_xent_strides_and_outside(dtype):
     """Padded and misaligned rows; only the gradients' own windows are written."""

@@ -21,6 +21,9 @@ constexpr int kNoDeviceUnits = 256;
 // Largest extent taken: tile edges past the end of a matrix stay within int.
 constexpr int kMostExtent = INT_MAX - 1024;
 
+// Most workgroups of 256 a launch takes along x: below 2^32 work items.
+constexpr int kMostBlocks = (1 << 24) - 1;
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 int elem_size(int type) { return type == SGEMM_TYPE_BF16 ? 2 : 4; }
@@ -67,7 +70,7 @@ TileKernel kernel_for(int type, int form, int tile, bool fast)
 
 int launch(const TileKernel &k, TileArgs &a, int64_t blocks, int slices, hipStream_t stream)
 {
-    if (blocks > INT_MAX) return (int)hipErrorInvalidConfiguration;
+    if (blocks > kMostBlocks) return (int)hipErrorInvalidConfiguration;
     k.fn<<<dim3((unsigned)blocks, 1, (unsigned)slices), dim3(k.threads), 0, stream>>>(a);
     return (int)hipGetLastError();
 }
@@ -198,6 +201,10 @@ extern "C" int sgemm_grouped_wgrad(int type, int groups, int rows, int M, int N,
     if ((work && !D) || !aligned(D, size)) return -12;
     if (ldd < (N > 1 ? N : 1)) return -13;
     if (stride_d < 0) return -14;
+    // Groups' outputs one after another, or between each other's rows; never shared.
+    if (work && groups > 1 && stride_d < (int64_t)(M - 1) * ldd + N &&
+        (stride_d < N || stride_d > ((int64_t)ldd - N) / (groups - 1)))
+        return -14;
     if ((work && !offsets) || !aligned(offsets, 4)) return -15;
     if (!work) return 0;
     // In parts, so that the product of three extents cannot overflow.
@@ -241,22 +248,23 @@ __global__ void __launch_bounds__(256) xent_join_kernel(int rows, int tiles, int
                                                         float *lse)
 {
     const int lane = threadIdx.x & 63;
-    const int row = blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= rows) return;
-    const f32x2 *p = parts + (int64_t)row * tiles;
-    float top = -INFINITY, sum = 0.f;
-    for (int t = lane; t < tiles; t += 64) {
-        const f32x2 v = p[t];
-        join_sums(top, sum, v[0], v[1]);
-    }
+    for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < rows;
+         row += (int64_t)gridDim.x * 4) {
+        const f32x2 *p = parts + row * tiles;
+        float top = -INFINITY, sum = 0.f;
+        for (int t = lane; t < tiles; t += 64) {
+            const f32x2 v = p[t];
+            join_sums(top, sum, v[0], v[1]);
+        }
 #pragma unroll
-    for (int d = 32; d; d /= 2) join_sums(top, sum, __shfl_xor(top, d), __shfl_xor(sum, d));
-    if (lane == 0) {
-        constexpr float ln2 = 0.693147180559945309417f;
-        const float v = ((isfinite(top) ? top : 0.f) + log2f(sum)) * ln2;
-        lse[row] = v;
-        const int64_t target = targets[row];
-        loss[row] = target >= 0 && target < vocab ? v - target_value[row] : 0.f;
+        for (int d = 32; d; d /= 2) join_sums(top, sum, __shfl_xor(top, d), __shfl_xor(sum, d));
+        if (lane == 0) {
+            constexpr float ln2 = 0.693147180559945309417f;
+            const float v = ((isfinite(top) ? top : 0.f) + log2f(sum)) * ln2;
+            lse[row] = v;
+            const int64_t target = targets[row];
+            loss[row] = target >= 0 && target < vocab ? v - target_value[row] : 0.f;
+        }
     }
 }
 
@@ -426,7 +434,8 @@ extern "C" int sgemm_xent(int type, int rows, int vocab, int K, const void *X, i
     a.targets = targets, a.parts = parts, a.target_value = value;
     rc = launch(k, a, ceil_div(rows, k.bm) * tiles, 1, stream);
     if (rc) return rc;
-    xent_join_kernel<<<dim3((unsigned)ceil_div(rows, 4)), dim3(256), 0, stream>>>(
+    const int64_t joins = ceil_div(rows, 4);
+    xent_join_kernel<<<dim3((unsigned)(joins < kMostBlocks ? joins : kMostBlocks)), dim3(256), 0, stream>>>(
         rows, tiles, vocab, reinterpret_cast<const sgemm::f32x2 *>(parts), value, targets, loss, lse);
     return (int)hipGetLastError();
 }

@@ -37,7 +37,7 @@
 // Both operands of a matrix instruction use the same assignment of k to lanes.
 // With blocks of BL = 16 and g = lane / 16, bf16 16x16x32 takes k = 8 g .. 8 g + 7, and
 // four fp32 16x16x4 steps s = 0..3 take k = 4 g + s; with BL = 32 and g = lane / 32, two
-// bf16 32x32x16 (eight fp32 32x32x2) cover the same half slab.  The larger block
+// bf16 32x32x16 cover the same half slab.  The larger block
 // halves the instructions a wave issues, which the largest tile needs: its
 // accumulators leave one wave per SIMD.  B is the instruction's first operand, so
 // a lane holds groups of four consecutive columns of one row of C:
@@ -254,12 +254,10 @@ __device__ __forceinline__ typename AccOf<BL>::Type mfma_step(const typename Ele
                                                               typename AccOf<BL>::Type c)
 {
     if constexpr (std::is_same<T, float>::value) {
+        static_assert(BL == 16, "fp32 tiles have blocks of 16");
 #pragma unroll
         for (int s = 0; s < 4; ++s)
-            if constexpr (BL == 16)
-                c = __builtin_amdgcn_mfma_f32_16x16x4f32(b[s], a[s], c, 0, 0, 0);
-            else
-                c = __builtin_amdgcn_mfma_f32_32x32x2f32(b[s], a[s], c, 0, 0, 0);
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(b[s], a[s], c, 0, 0, 0);
         return c;
     } else if constexpr (BL == 16) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
@@ -662,7 +660,8 @@ tile_kernel(TileArgs g)
     if constexpr (EP == STORE) {
         T *C = static_cast<T *>(g.C);
         if constexpr (RG == SUM) C += group * g.group_stride;
-        const float alpha = g.alpha, beta = g.beta;
+        // An empty contraction is 0 whatever alpha holds.
+        const float alpha = K > 0 ? g.alpha : 0.f, beta = g.beta;
         auto store = [&](auto inside, auto scaled) {
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
@@ -759,7 +758,7 @@ tile_kernel(TileArgs g)
                 const float w = m < g.M ? g.dloss[m] : 0.f, lse = m < g.M ? g.lse[m] : 0.f;
                 const float high = lse * kLog2e, low = fmaf(lse, kLog2e, -high);
                 const bool counts = target >= 0 && target < g.vocab;
-                const int at = counts ? (int)target - g.col0 : INT32_MIN;
+                const int at = counts ? (int)target - g.col0 : -1;  // below every column: none
                 T *crow = C + (int64_t)m * g.ldc;
                 Vec before;
 #pragma unroll
@@ -832,7 +831,7 @@ tile_kernel(TileArgs g)
             __builtin_amdgcn_sched_barrier(0);
             const int m = mw + BL * i;
             const int64_t target = m < g.M ? g.targets[m] : -1;
-            const int at = target >= 0 && target < g.N ? (int)target : INT32_MIN;
+            const int at = target >= 0 && target < g.N ? (int)target : -1;  // none
             float top = -INFINITY;
 #pragma unroll
             for (int u = 0; u < FN * GR; ++u) {

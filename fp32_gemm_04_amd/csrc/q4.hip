@@ -181,9 +181,9 @@ extern "C" int sgemm_q4_quantize(int type, int N, int K, int block, const void *
     if ((work && !S) || !aligned(S, size)) return -8;
     if (!work) return 0;
     const int nblk = (int)ceil_div(K, block);
+    constexpr int64_t kMostBlocks = (1 << 24) - 1;  // of 256: below 2^32 work items
     const int64_t blocks = ceil_div((int64_t)N * nblk, 16);
-    if (blocks > INT_MAX) return -2;
-    const dim3 grid((unsigned)blocks);
+    const dim3 grid((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks));
     if (type == SGEMM_TYPE_BF16)
         quantize<bf16>(grid, N, K, block, nblk, W, ldw, Q, S, Z, stream);
     else

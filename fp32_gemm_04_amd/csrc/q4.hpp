@@ -499,41 +499,43 @@ __global__ void __launch_bounds__(256) q4_quantize_kernel(int N, int K, int nblk
                                                           int64_t ldw, uint8_t *Q, T *S, uint8_t *Z)
 {
     constexpr int E = BLOCK / 16;
-    const int64_t item = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4;
     const int l = threadIdx.x & 15;
-    if (item >= (int64_t)N * nblk) return;  // the 16 lanes of an item together
-    const int n = (int)(item / nblk), b = (int)(item % nblk);
-    const int k0 = b * BLOCK + l * E;
-    float w[E], lo = 0.f, hi = 0.f;
+    // The 16 lanes of an item together.
+    for (int64_t item = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4; item < (int64_t)N * nblk;
+         item += (int64_t)gridDim.x * 16) {
+        const int n = (int)(item / nblk), b = (int)(item % nblk);
+        const int k0 = b * BLOCK + l * E;
+        float w[E], lo = 0.f, hi = 0.f;
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-        w[j] = k0 + j < K ? (float)W[(int64_t)n * ldw + k0 + j] : 0.f;
-        lo = fminf(lo, w[j]);
-        hi = fmaxf(hi, w[j]);
-    }
-#pragma unroll
-    for (int d = 1; d < 16; d *= 2) {
-        lo = fminf(lo, __shfl_xor(lo, d));
-        hi = fmaxf(hi, __shfl_xor(hi, d));
-    }
-    // The scale as it will be read back; a block of zeros keeps scale 0.
-    const T scale = (T)(ZEROS ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f);
-    const float s = (float)scale;
-    float zero = 8.f;
-    if (ZEROS) zero = s > 0.f ? fminf(fmaxf(rintf(-lo / s), 0.f), 15.f) : 0.f;
-#pragma unroll
-    for (int j = 0; j < E; j += 2) {
-        uint32_t byte = 0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float q = s > 0.f ? fminf(fmaxf(rintf(w[j + h] / s) + zero, 0.f), 15.f) : zero;
-            byte |= (uint32_t)q << (4 * h);
+        for (int j = 0; j < E; ++j) {
+            w[j] = k0 + j < K ? (float)W[(int64_t)n * ldw + k0 + j] : 0.f;
+            lo = fminf(lo, w[j]);
+            hi = fmaxf(hi, w[j]);
         }
-        if (k0 + j < K) Q[(int64_t)n * (K / 2) + (k0 + j) / 2] = (uint8_t)byte;
-    }
-    if (l == 0) {
-        S[item] = scale;
-        if (ZEROS) Z[item] = (uint8_t)zero;
+#pragma unroll
+        for (int d = 1; d < 16; d *= 2) {
+            lo = fminf(lo, __shfl_xor(lo, d));
+            hi = fmaxf(hi, __shfl_xor(hi, d));
+        }
+        // The scale as it will be read back; a block of zeros keeps scale 0.
+        const T scale = (T)(ZEROS ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f);
+        const float s = (float)scale;
+        float zero = 8.f;
+        if (ZEROS) zero = s > 0.f ? fminf(fmaxf(rintf(-lo / s), 0.f), 15.f) : 0.f;
+#pragma unroll
+        for (int j = 0; j < E; j += 2) {
+            uint32_t byte = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float q = s > 0.f ? fminf(fmaxf(rintf(w[j + h] / s) + zero, 0.f), 15.f) : zero;
+                byte |= (uint32_t)q << (4 * h);
+            }
+            if (k0 + j < K) Q[(int64_t)n * (K / 2) + (k0 + j) / 2] = (uint8_t)byte;
+        }
+        if (l == 0) {
+            S[item] = scale;
+            if (ZEROS) Z[item] = (uint8_t)zero;
+        }
     }
 }
 

@@ -15,7 +15,8 @@
  * caller's, one per call in flight (also one per captured graph that may run
  * beside another).
  *
- * Extents are at most 2^31 - 1025.
+ * Extents are at most 2^31 - 1025.  A product of more than 2^24 - 1 tiles is
+ * answered with hipErrorInvalidConfiguration.
  *
  * Types.  Matrices hold fp32 or bf16 values (one type per call); every sum is
  * held in fp32, and a bf16 result is rounded once, to nearest even.
@@ -80,14 +81,16 @@ int sgemm_grouped(int type, int trans, int groups, int rows, int N, int K, float
  *
  *   X, ldx    rows x M, ldx >= max(1, M)
  *   G, ldg    rows x N, ldg >= max(1, N)
- *   D, ldd, stride_d   D_e is M x N, at D[e*stride_d + m*ldd + n]
+ *   D, ldd, stride_d   D_e is M x N, at D[e*stride_d + m*ldd + n]; no two groups'
+ *             share an element (they follow one another, or lie side by side
+ *             in rows of all groups)
  * A group without rows gets D_e <- beta*D_e.  For weights stored K x N, X is
  * the product's input and G the gradient of its output (M = K); for weights
  * stored N x K, exchange the two.  Types, offsets, alpha and beta as in
  * sgemm_grouped.
  * Returns -1 type, -2 groups < 0, -3 rows < 0, -4 M < 0, -5 N < 0 (or more
  * than 2^31 - 1 tiles), -7 X, -8 ldx, -9 G, -10 ldg, -12 D, -13 ldd, -14
- * stride_d < 0, -15 offsets.
+ * stride_d < 0 or outputs that overlap, -15 offsets.
  */
 int sgemm_grouped_wgrad(int type, int groups, int rows, int M, int N, float alpha, const void *X,
                         int ldx, const void *G, int ldg, float beta, void *D, int ldd,

@@ -149,3 +149,15 @@ def test_python_refuses_what_does_not_fit():
 def test_errors_name_the_call():
     assert "sgemm_xent failed with status -5: invalid parameter 5" in str(sg.SgemmError(-5, "sgemm_xent"))
     assert "invalid M" in str(sg.SgemmError(-1))
+
+
+@pytest.mark.parametrize("ldd,stride_d,code", [
+    (32, 0, -14), (32, 511, -14), (64, 31, -14), (65, 34, -14),  # groups that share elements
+    (32, 512, 0), (64, 32, 0), (65, 33, 0), (32, 1 << 62, 0)])
+def test_wgrad_outputs_must_not_overlap(ldd, stride_d, code):
+    args = dict(WGRAD, ldd=ldd, stride_d=stride_d)
+    if code == 0:
+        args["offsets"] = 0  # the next check, so that no call reaches a device
+        code = -15
+    assert sg.sgemm_grouped_wgrad(*args.values()) == code
+    assert sg.sgemm_grouped_wgrad(*dict(args, groups=1, offsets=0).values()) == -15

@@ -322,3 +322,50 @@ def test_offsets_past_32_bits():
     Y = sg.grouped_gemm(X, W, off, trans=True)
     x, w = X.double(), W[-1].double().t()
     check(Y, x @ w, x.abs() @ w.abs(), K + 2, "weights")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_empty_contraction_is_zero_whatever_alpha(dtype):
+    say("empty contraction", dtype)
+    off = torch.tensor([0, 3, 3], dtype=torch.int32, device="cuda")
+    inf = float("inf")
+    Y = sg.grouped_gemm(rand((3, 0), dtype, 1), rand((2, 0, 7), dtype, 2), off,
+                        torch.ones((3, 7), dtype=dtype, device="cuda"), alpha=inf, beta=2.0)
+    assert torch.equal(Y, torch.full_like(Y, 2.0))
+    D = sg.grouped_wgrad(rand((3, 5), dtype, 3), rand((3, 7), dtype, 4), off, alpha=inf)
+    assert torch.equal(D[1], torch.zeros_like(D[1]))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_wgrad_groups_side_by_side(dtype):
+    """D_e in the columns of one matrix with rows of all groups."""
+    say("side by side", dtype)
+    ends, off = offsets_of([70, 0, 33])
+    X, G = rand((ends[-1], 50), dtype, 1), rand((ends[-1], 24), dtype, 2)
+    D = torch.full((50, 3, 24), 9.0, dtype=dtype, device="cuda")
+    sg.grouped_wgrad(X, G, off, D.permute(1, 0, 2))
+    assert torch.equal(D.permute(1, 0, 2), sg.grouped_wgrad(X, G, off))
+    with pytest.raises(sg.SgemmError, match="parameter 14"):
+        sg.grouped_wgrad(X, G, off, D[:, :1].permute(1, 0, 2).expand(3, 50, 24))
+
+
+def test_more_than_2_to_32_work_items():
+    say("many blocks to quantise")
+    n = (1 << 28) + 37
+    W = torch.tensor([3.0, -1.0], dtype=BF16, device="cuda").repeat(n, 1)
+    W[-1] = torch.tensor([7.0, 0.5], dtype=BF16, device="cuda")
+    Q, S, _ = sg.q4_quantize(W, 32, zeros=False)
+    assert Q[-1, 0].item() == 15 + 16 * 8 and S[-1].item() == 1.0  # 0.5 rounds to even
+    assert torch.equal(Q[:-1], Q[:1].expand(n - 1, 1)) and torch.equal(S[:-1], S[:1].expand(n - 1, 1))
+    del W, Q, S
+    say("many rows of a loss")
+    n = (1 << 26) + 5
+    X = torch.full((n, 1), 2.0, device="cuda")
+    X[-1] = -1.0
+    W = torch.tensor([[1.0], [0.0]], device="cuda")
+    loss, lse = sg.linear_cross_entropy(X, W, torch.zeros(n, dtype=torch.int64, device="cuda"))
+    one = torch.log(torch.exp(torch.tensor([2.0, -1.0], dtype=torch.float64)) + 1)
+    # lse of two terms, each a few roundings of its logarithm.
+    assert (lse[:-1] - one[0]).abs().max() < 8 * 2.0 ** -24 * 2.2 and abs(lse[-1] - one[1]) < 8 * 2.0 ** -24
+    assert torch.equal(loss[:-1], loss[:1].expand(n - 1))
+    assert abs(loss[-1].item() - (one[1].item() + 1.0)) < 8 * 2.0 ** -24 * 1.4

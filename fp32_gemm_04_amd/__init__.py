@@ -363,7 +363,7 @@ _TYPES = {torch.float32: SGEMM_TYPE_F32, torch.bfloat16: SGEMM_TYPE_BF16}
 def _operand(t, name, dtype, device, dim=2, rows=None, cols=None):
     """Checks a tensor of rows with unit column stride; returns its leading dimension."""
     shape = t.shape
-    if t.dtype != dtype or len(shape) != dim:
+    if t.dtype is not dtype or len(shape) != dim:
         raise TypeError("%s must be a %d-D %s tensor, not %d-D %s"
                         % (name, dim, dtype, len(shape), t.dtype))
     if not t.is_cuda or t.device != device:
@@ -390,27 +390,29 @@ def _groups_of(t):
 
 
 def _vector(t, name, dtype, device, n):
-    if t.dtype != dtype or tuple(t.shape) != (n,) or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != (n,) or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a packed %s vector of %d on %s" % (name, dtype, n, device))
     return t.data_ptr()
 
 
 def _type_of(t, name):
-    if t.dtype not in _TYPES:
+    code = _TYPES.get(t.dtype)
+    if code is None:
         raise TypeError("%s must be float32 or bfloat16, not %s" % (name, t.dtype))
-    return _TYPES[t.dtype]
+    return code
 
 
 _current_stream = torch._C._cuda_getCurrentRawStream if hasattr(
     torch._C, "_cuda_getCurrentRawStream") else (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _run(call, device, stream, operands, body):
     """body(stream handle) with ``device`` current and, where a stream is given,
     with it current too, so that what body allocates belongs to that stream;
     the operands' memory is then kept from reuse until that stream is past the call."""
-    if stream is None and device.index == torch.cuda.current_device():
+    if stream is None and device.index == _current_device():
         rc = body(_current_stream(device.index))  # the usual case, without context managers
     else:
         if stream is not None and stream.device != device:
@@ -453,7 +455,7 @@ def grouped_gemm(X, W, offsets, Y=None, trans: bool = False, alpha: float = 1.0,
     def body(s):
         nonlocal Y
         if Y is None:
-            Y = torch.zeros((rows, N), dtype=X.dtype, device=dev)
+            Y = X.new_zeros(rows, N)
         return _lib.sgemm_grouped(t, int(trans), groups, rows, N, K, alpha, X.data_ptr(), ldx,
                                   W.data_ptr(), ldw, _groups_of(W), beta, Y.data_ptr(), ldy, off, s)
     _run("sgemm_grouped", dev, stream, (X, W, offsets, Y), body)
@@ -486,9 +488,7 @@ def grouped_wgrad(X, G, offsets, D=None, alpha: float = 1.0, beta: float = 0.0, 
     def body(s):
         nonlocal D
         if D is None:
-            D = torch.empty((groups, M, N), dtype=X.dtype, device=dev)
-            if beta != 0.0:
-                D.zero_()
+            D = (X.new_empty if beta == 0.0 else X.new_zeros)(groups, M, N)
         return _lib.sgemm_grouped_wgrad(t, groups, rows, M, N, alpha, X.data_ptr(), ldx,
                                         G.data_ptr(), ldg, beta, D.data_ptr(), ldd, _groups_of(D),
                                         off, s)
@@ -522,9 +522,9 @@ def linear_cross_entropy(X, W, targets, stream=None):
 
     def body(s):
         nonlocal loss, lse
-        loss, lse = torch.empty((2, rows), dtype=torch.float32, device=dev)
+        loss, lse = (X.new_empty(rows, dtype=torch.float32) for _ in range(2))
         n = _lib.sgemm_xent_workspace(t, rows, vocab, K, 0)
-        ws = torch.empty((n,), dtype=torch.uint8, device=dev)
+        ws = X.new_empty(n, dtype=torch.uint8)
         return _lib.sgemm_xent(t, rows, vocab, K, X.data_ptr(), ldx, W.data_ptr(), ldw, tg,
                                loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), n, s)
     _run("sgemm_xent", dev, stream, (X, W, targets), body)
@@ -548,11 +548,11 @@ def linear_cross_entropy_backward(dloss, X, W, targets, lse, dX=None, dW=None, n
     def body(s):
         nonlocal dX, dW
         if need_dX and dX is None:
-            dX = torch.empty((rows, K), dtype=X.dtype, device=dev)
+            dX = X.new_empty(rows, K)
         if need_dW and dW is None:
-            dW = torch.empty((vocab, K), dtype=X.dtype, device=dev)
+            dW = X.new_empty(vocab, K)
         n = _lib.sgemm_xent_workspace(t, rows, vocab, K, 1)
-        ws = torch.empty((n,), dtype=torch.uint8, device=dev)
+        ws = X.new_empty(n, dtype=torch.uint8)
         return _lib.sgemm_xent_backward(t, rows, vocab, K, X.data_ptr(), ldx, W.data_ptr(), ldw, tg,
                                         pl, pd, dX.data_ptr() if need_dX else 0, lddx,
                                         dW.data_ptr() if need_dW else 0, lddw, ws.data_ptr(), n, s)
@@ -564,7 +564,7 @@ Q4_BLOCKS = (32, 64, 128)
 
 
 def _packed(t, name, dtype, device, shape):
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a packed %s tensor of %s on %s" % (name, dtype, shape, device))
     return t.data_ptr()
 
@@ -594,9 +594,9 @@ def q4_quantize(W, block: int = 128, zeros: bool = True, stream=None):
 
     def body(s):
         nonlocal Q, S, Z
-        Q = torch.empty(lead + (N, K // 2), dtype=torch.uint8, device=dev)
-        S = torch.empty(lead + (N, blocks), dtype=W.dtype, device=dev)
-        Z = torch.empty(lead + (N, blocks), dtype=torch.uint8, device=dev) if zeros else None
+        Q = W.new_empty(lead + (N, K // 2), dtype=torch.uint8)
+        S = W.new_empty(lead + (N, blocks))
+        Z = W.new_empty(lead + (N, blocks), dtype=torch.uint8) if zeros else None
         return _lib.sgemm_q4_quantize(t, rows, K, block, W.data_ptr(), ldw, Q.data_ptr(),
                                       S.data_ptr(), Z.data_ptr() if zeros else 0, s)
     _run("sgemm_q4_quantize", dev, stream, (W,), body)
@@ -620,21 +620,23 @@ def q4_matvec(X, Q, scales, zeros=None, block: int = 128, Y=None, offsets=None, 
         raise ValueError("block must be one of %s" % (Q4_BLOCKS,))
     if K % 2:
         raise ValueError("K must be even")
-    if Q.dim() != (2 if offsets is None else 3):
+    *lead, N, bytes_ = Q.shape if Q.dim() > 1 else (0, 0, 0, 0)
+    if len(lead) != (0 if offsets is None else 1):
         raise ValueError("Q must be (N, K/2), or (groups, N, K/2) with offsets")
-    lead, N = tuple(Q.shape[:-2]), Q.shape[-2]
-    groups, blocks = lead[0] if lead else 1, -(-K // block)
-    pq = _packed(Q, "Q", torch.uint8, dev, lead + (N, K // 2))
-    ps = _packed(scales, "scales", X.dtype, dev, lead + (N, blocks))
-    pz = _packed(zeros, "zeros", torch.uint8, dev, lead + (N, blocks)) if zeros is not None else 0
+    groups = lead[0] if lead else 1
+    if bytes_ != K // 2:
+        raise ValueError("Q holds %d weights a row, X %d values" % (2 * bytes_, K))
+    per_block = (*lead, N, -(-K // block))
+    pq = _packed(Q, "Q", torch.uint8, dev, Q.shape)
+    ps = _packed(scales, "scales", X.dtype, dev, per_block)
+    pz = _packed(zeros, "zeros", torch.uint8, dev, per_block) if zeros is not None else 0
     off = _vector(offsets, "offsets", torch.int32, dev, groups + 1) if offsets is not None else 0
     ldy = _operand(Y, "Y", X.dtype, dev, 2, rows, N) if Y is not None else max(1, N)
 
     def body(s):
         nonlocal Y
         if Y is None:
-            new = torch.empty if offsets is None else torch.zeros
-            Y = new((rows, N), dtype=X.dtype, device=dev)
+            Y = (X.new_empty if offsets is None else X.new_zeros)(rows, N)
         return _lib.sgemm_q4_matvec(t, groups, rows, N, K, block, X.data_ptr(), ldx, pq, ps, pz,
                                     Y.data_ptr(), ldy, off, s)
     _run("sgemm_q4_matvec", dev, stream, (X, Q, scales, zeros, Y, offsets), body)

@@ -82,30 +82,31 @@ int launch(const TileKernel &k, TileArgs &a, int64_t blocks, int slices, hipStre
 // 131072 with gradients 15.9 ms with the 256 tile, 16.9 with 128 x 192; T 384, H 1024, V
 // 50021 369 and 277 us; 16 experts' backward pass of 16384 rows 381 and 349 us (128 x
 // 128: 403, 64 x 128: 477).  fp32: T 1023, H 1000, V 49999 3.22 ms with the 128 tile,
-// 3.35 with 64 x 64; 24 experts' backward pass of 1500 rows 93 and 63 us.
+// 3.35 with 64 x 64; 24 experts' backward pass of 1500 rows 93 and 63 us; the loss of 37
+// rows (H 1024, V 32000) 45.9 us with 64 x 64 and 39.6 with 48 x 128, of 140 rows 114 and 90.
 struct TileCost {
     int bm, bn;
     double rate;
     int lead;
 };
 const TileCost kBf16Tiles[NUM_TILES] = {
-    {16, 64, 0.2, 64}, {32, 128, 0.45, 64}, {64, 128, 0.65, 64}, {128, 128, 0.8, 64}, {128, 192, 0.88, 64},
+    {16, 64, 0.2, 64}, {32, 128, 0.45, 64}, {0, 0, 0, 0}, {64, 128, 0.65, 64}, {128, 128, 0.8, 64}, {128, 192, 0.88, 64},
     {256, 256, 1.0, 256}};
 const TileCost kF32Tiles[NUM_TILES] = {
-    {16, 64, 0.5, 64}, {32, 64, 0.75, 64}, {64, 64, 0.87, 64}, {128, 128, 1.0, 64}, {0, 0, 0, 0}, {0, 0, 0, 0}};
+    {16, 64, 0.5, 64}, {32, 64, 0.75, 64}, {48, 128, 0.9, 64}, {64, 64, 0.87, 64}, {128, 128, 1.0, 64}, {0, 0, 0, 0}, {0, 0, 0, 0}};
 
 // The tile that finishes first when every compute unit takes the same number of tiles
 // (a last one that has the unit to itself counts half where two fit beside each other):
 // products of N columns and contraction K, whose rows split into row_tiles(bm) tiles in
 // all.
 template <typename RowTiles>
-int choose_tile(int type, bool fast, RowTiles row_tiles, int64_t N, int64_t K, int cus)
+int choose_tile(int type, int form, bool fast, RowTiles row_tiles, int64_t N, int64_t K, int cus)
 {
     const TileCost *t = type == SGEMM_TYPE_BF16 ? kBf16Tiles : kF32Tiles;
     int best = S16;
     double least = 0;
     for (int i = 0; i < (fast ? (int)NUM_TILES : T128 + 1); ++i) {
-        if (t[i].bm == 0) continue;
+        if (t[i].bm == 0 || (i == M48 && (form == F_SUM || form == F_DW))) continue;
         const int64_t tiles = row_tiles(t[i].bm) * ceil_div(N, t[i].bn);
         const bool pairs = t[i].lead == 64 && tiles > cus;
         const double rounds = pairs ? 0.5 * ceil_div(2 * tiles, cus) : (double)ceil_div(tiles, cus);
@@ -116,9 +117,9 @@ int choose_tile(int type, bool fast, RowTiles row_tiles, int64_t N, int64_t K, i
 }
 
 // For one product of M x N outputs.
-int plain_tile(int type, bool fast, int64_t M, int64_t N, int64_t K, int cus)
+int plain_tile(int type, int form, bool fast, int64_t M, int64_t N, int64_t K, int cus)
 {
-    return choose_tile(type, fast, [&](int bm) { return ceil_div(M, bm); }, N, K, cus);
+    return choose_tile(type, form, fast, [&](int bm) { return ceil_div(M, bm); }, N, K, cus);
 }
 
 }  // namespace
@@ -164,7 +165,7 @@ extern "C" int sgemm_grouped(int type, int trans, int groups, int rows, int N, i
         const int64_t t = rows / bm + used / 2;
         return t > used ? t : (int64_t)used;
     };
-    const int tile = choose_tile(type, fast, row_tiles, N, kk, cus);
+    const int tile = choose_tile(type, F_ROWS_N, fast, row_tiles, N, kk, cus);
     const TileKernel k = kernel_for(type, trans ? F_ROWS_T : F_ROWS_N, tile, fast);
     // Every group's last tile may be part full.
     const int64_t most = (rows + (int64_t)used * (k.bm - 1)) / k.bm;
@@ -218,7 +219,7 @@ extern "C" int sgemm_grouped_wgrad(int type, int groups, int rows, int M, int N,
     const bool fast = kk == 0 || (fast_operand(X, ldx, 0, size) &&
                                   fast_operand(G, ldg, 0, size));
     const auto row_tiles = [&](int bm) { return ceil_div(M, bm) * groups; };
-    const int tile = choose_tile(type, fast, row_tiles, N, kk / groups, cus);
+    const int tile = choose_tile(type, F_SUM, fast, row_tiles, N, kk / groups, cus);
     const TileKernel k = kernel_for(type, F_SUM, tile, fast);
     const int64_t blocks = ceil_div(M, k.bm) * ceil_div(N, k.bn) * groups;
     TileArgs a = {};
@@ -340,11 +341,11 @@ XentPlan xent_plan(int type, bool fast, int rows, int vocab, int K, int cus)
     // units, the tile is chosen as if the sum were cut as finely as it may be (1024
     // columns a slice), and cut until each unit has two.
     const int64_t most_slices = p.piece / 1024 < 1 ? 1 : p.piece / 1024 > 64 ? 64 : p.piece / 1024;
-    p.dx_tile = plain_tile(type, fast, p.d_rows, K, p.piece, cus);
+    p.dx_tile = plain_tile(type, F_PART, fast, p.d_rows, K, p.piece, cus);
     p.slices = 1;
     if (ceil_div(p.d_rows, 128) * ceil_div(K, 128) < cus) {
         p.dx_tile = choose_tile(
-            type, fast, [&](int bm) { return ceil_div(p.d_rows, bm) * most_slices; }, K,
+            type, F_PART, fast, [&](int bm) { return ceil_div(p.d_rows, bm) * most_slices; }, K,
             p.piece / most_slices, cus);
         const TileCost &t = (type == SGEMM_TYPE_BF16 ? kBf16Tiles : kF32Tiles)[p.dx_tile];
         const int64_t s = 2 * cus / (ceil_div(p.d_rows, t.bm) * ceil_div(K, t.bn));
@@ -360,8 +361,8 @@ XentPlan xent_plan(int type, bool fast, int rows, int vocab, int K, int cus)
 int64_t stats_bytes(int type, int rows, int vocab, int K, int cus)
 {
     const TileCost *t = type == SGEMM_TYPE_BF16 ? kBf16Tiles : kF32Tiles;
-    const int a = t[plain_tile(type, true, rows, vocab, K, cus)].bn;
-    const int b = t[plain_tile(type, false, rows, vocab, K, cus)].bn;
+    const int a = t[plain_tile(type, F_STATS, true, rows, vocab, K, cus)].bn;
+    const int b = t[plain_tile(type, F_STATS, false, rows, vocab, K, cus)].bn;
     return round_up((int64_t)rows * 4, 256) + (int64_t)rows * ceil_div(vocab, a < b ? a : b) * 8;
 }
 
@@ -421,7 +422,7 @@ extern "C" int sgemm_xent(int type, int rows, int vocab, int K, const void *X, i
     const int size = elem_size(type);
     const bool fast = K == 0 || (fast_operand(X, ldx, 0, size) &&
                                  fast_operand(W, ldw, 0, size));
-    const int tile = plain_tile(type, fast, rows, vocab, K, cus);
+    const int tile = plain_tile(type, F_STATS, fast, rows, vocab, K, cus);
     const TileKernel k = kernel_for(type, F_STATS, tile, fast);
     float *value = static_cast<float *>(ws);
     float *parts = value + round_up((int64_t)rows * 4, 256) / 4;
@@ -479,7 +480,7 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
         {
             const bool fast = fast_x && fast_w;
             const int stored = p.low_rows ? p.low_rows : rows;
-            int tile = plain_tile(type, fast, stored, n, K, cus);
+            int tile = plain_tile(type, F_GRAD, fast, stored, n, K, cus);
             if (p.low_rows && tile == T256) tile = T192;  // the 256 tile keeps no remainders
             const TileKernel k = kernel_for(type, F_GRAD, tile, fast);
             a = TileArgs{};
@@ -495,7 +496,7 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
         }
         if (dW) {
             const bool fast = fast_x;
-            const int tile = plain_tile(type, fast, n, K, p.d_rows, cus);
+            const int tile = plain_tile(type, F_DW, fast, n, K, p.d_rows, cus);
             const TileKernel k = kernel_for(type, F_DW, tile, fast);
             a = TileArgs{};
             a.A = ws, a.B = X, a.C = static_cast<char *>(dW) + col0 * lddw * size;

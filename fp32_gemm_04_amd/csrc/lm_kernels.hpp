@@ -7,7 +7,7 @@
 namespace sgemm {
 namespace lm {
 
-enum Tile { S16, M32, M64, T128, T192, T256, NUM_TILES };
+enum Tile { S16, M32, M48, M64, T128, T192, T256, NUM_TILES };
 // The operand layouts and epilogues of the products.
 enum Form {
     F_ROWS_T,   // grouped rows, weights N x K
@@ -26,7 +26,8 @@ struct TileKernel {
     int bm, bn, threads;
 };
 
-// null fn: that tile is not built for the form and type.
+// null fn: that tile is not built for the form and type (48 rows: fp32 only, and not
+// where A's rows are contiguous in memory, since they make no whole 128-byte LDS rows).
 TileKernel bf16_kernel(int form, int tile, bool fast);
 TileKernel f32_kernel(int form, int tile, bool fast);
 
@@ -37,12 +38,16 @@ TileKernel tile_entry(int form)
     switch (form) {
     case F_ROWS_T: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, BL, WPE, KC, KC, ROWS, STORE, FAST>; break;
     case F_ROWS_N: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, BL, WPE, KC, MC, ROWS, STORE, FAST>; break;
-    case F_SUM: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, BL, WPE, MC, MC, SUM, STORE, FAST>; break;
+    case F_SUM:
+        if constexpr (BM != 48) fn = tile_kernel<T, BM, BN, WM, WN, NBUF, BL, WPE, MC, MC, SUM, STORE, FAST>;
+        break;
     case F_STATS: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, BL, WPE, KC, KC, PLAIN, STATS, FAST>; break;
     case F_GRAD: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, BL, WPE, KC, KC, PLAIN, GRAD, FAST>; break;
     case F_PART: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, BL, WPE, KC, MC, PLAIN, PART, FAST>; break;
     case F_DX: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, BL, WPE, KC, MC, PLAIN, STORE, FAST>; break;
-    case F_DW: fn = tile_kernel<T, BM, BN, WM, WN, NBUF, BL, WPE, MC, MC, PLAIN, STORE, FAST>; break;
+    case F_DW:
+        if constexpr (BM != 48) fn = tile_kernel<T, BM, BN, WM, WN, NBUF, BL, WPE, MC, MC, PLAIN, STORE, FAST>;
+        break;
     default: break;
     }
     return TileKernel{fn, BM, BN, WM * WN * 64};

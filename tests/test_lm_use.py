@@ -369,3 +369,13 @@ def test_more_than_2_to_32_work_items():
     assert (lse[:-1] - one[0]).abs().max() < 8 * 2.0 ** -24 * 2.2 and abs(lse[-1] - one[1]) < 8 * 2.0 ** -24
     assert torch.equal(loss[:-1], loss[:1].expand(n - 1))
     assert abs(loss[-1].item() - (one[1].item() + 1.0)) < 8 * 2.0 ** -24 * 1.4
+
+
+@pytest.mark.parametrize("trans", [False, True])
+def test_grouped_48_row_tiles(trans):
+    test_grouped_every_tile(F32, trans, [90, 0, 48, 133, 90, 91, 90, 97, 96], 5003, 67)
+
+
+@pytest.mark.parametrize("T,K,V", [(37, 70, 26001), (48, 130, 30000), (140, 72, 31000)])
+def test_xent_48_row_tiles(T, K, V):
+    test_xent_every_tile(F32, T, K, V)

@@ -296,6 +296,16 @@ __device__ __forceinline__ int64_t scan_tiles(const int *offsets, int groups, in
     return sum;  // inclusive
 }
 
+// WM x WN waves share the tile, NBUF slabs the ring; WPE waves per SIMD bound the registers.
+// What bounds it: the matrix cores where tiles have many rows (256 x 256, T 8192, H 2048, V
+// 131072: logits to row statistics 3.70-3.85 ms, 1140-1190 TF/s, the cores 56% busy at 2.0
+// GHz; derivatives 503-519 us a piece of 16384 columns, dW and dX 453-468; fp32 128 x 128,
+// T 1023, H 1000, V 49999: 794-817 us a product, 126-129 TF/s), memory where they have few
+// (16 x 64, 24 rows on 14 experts' 2048 x 1408 weights: 17.4 us, 4.6 TB/s).
+// Why this form: slabs of 128 bytes, since 64 with twice the buffers doubled the barriers
+// and were slower; operands half a slab ahead, so that reads of LDS hide behind products
+// of one wave per SIMD; no workgroup stays for a second tile (no gain, and the 256 tile
+// spilled).
 template <typename T, int BM, int BN, int WM, int WN, int NBUF, int BL, int WPE, Layout LA,
           Layout LB, Ragged RG, Epilogue EP, bool FAST>
 __global__ void __launch_bounds__(WM *WN * 64) __attribute__((amdgpu_waves_per_eu(WPE)))

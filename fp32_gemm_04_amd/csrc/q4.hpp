@@ -167,6 +167,10 @@ __device__ __forceinline__ void lds_barrier()
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+// RT groups of 16 rows and NT of 16 columns a wave.  What bounds it: one row, 4096 x 4096:
+// 7.0 us, a launch and one pass of memory latency; 12 fp32 rows, 8192 x 28001, blocks of 32:
+// 63 us for 145 MB (43 without staging x and scales, 56 without products); 48 bf16 rows on
+// 23 experts' 2048 x 5632, blocks of 64: 51 us for 146 MB (38 and 49).
 template <typename T, int BLOCK, int RT, int NT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads)
 __attribute__((amdgpu_waves_per_eu(RT <= 2 ? 4 : 2))) q4_kernel(Q4Args g)
@@ -493,7 +497,8 @@ __attribute__((amdgpu_waves_per_eu(RT <= 2 ? 4 : 2))) q4_kernel(Q4Args g)
     }
 }
 
-// Quantisation: 16 lanes per block of BLOCK weights, BLOCK / 16 each.
+// Quantisation: 16 lanes per block of BLOCK weights, BLOCK / 16 each; one pass over W, done
+// once per weight, so nothing beyond coalesced reads is arranged.
 template <typename T, int BLOCK, bool ZEROS>
 __global__ void __launch_bounds__(256) q4_quantize_kernel(int N, int K, int nblk, const T *W,
                                                           int64_t ldw, uint8_t *Q, T *S, uint8_t *Z)

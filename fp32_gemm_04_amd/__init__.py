@@ -573,7 +573,8 @@ def q4_quantize(W, block: int = 128, zeros: bool = True, stream=None):
     """(Q, scales, zeros): W in 4 bits with a scale, and with ``zeros`` a zero, for
     each ``block`` (32, 64 or 128) of weights along K (``sgemm_q4_quantize``).
 
-    W: (N, K) or (groups, N, K), packed groups, float32 or bfloat16, K even.  Q: uint8 of (..., N,
+    W: (N, K) or (groups, N, K), packed groups, float32 or bfloat16, values below 2^127
+    in magnitude, K even.  Q: uint8 of (..., N,
     K/2), two weights a byte, the even one in the low half; scales: W's type,
     (..., N, ceil(K/block)); zeros: uint8 likewise, or None.
     """

@@ -127,7 +127,8 @@ __device__ __forceinline__ void load_slab16(u32x4 rsrc, uint32_t voff, uint32_t 
 // hold voff: compiled code never touches an address register while a load is in flight.
 __device__ __forceinline__ void leave_range(uint32_t &voff, int k, int left)
 {
-    asm volatile("v_cmp_gt_i32_e32 vcc, %2, %1\n\tv_cndmask_b32_e32 %0, %3, %0, vcc"
+    asm volatile("v_cmp_gt_i32_e32 vcc, %2, %1\n\ts_nop 1\n\t"
+                 "v_cndmask_b32_e32 %0, %3, %0, vcc"
                  : "+v"(voff)
                  : "v"(k), "s"(left), "v"(0x80000000u)
                  : "vcc");

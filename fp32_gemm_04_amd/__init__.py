@@ -360,6 +360,15 @@ def sgemm_q4_quantize(type, N, K, block, W, ldw, Q, S, Z, stream=0) -> int:
 _TYPES = {torch.float32: SGEMM_TYPE_F32, torch.bfloat16: SGEMM_TYPE_BF16}
 
 
+_MOST_INT = 2 ** 31 - 1  # ctypes passes larger numbers on without their high bits
+
+
+def _extent(n, name):
+    if n > _MOST_INT:
+        raise ValueError("%s has an extent or stride of %d: the calls take int" % (name, n))
+    return n
+
+
 def _operand(t, name, dtype, device, dim=2, rows=None, cols=None):
     """Checks a tensor of rows with unit column stride; returns its leading dimension."""
     shape = t.shape
@@ -371,6 +380,8 @@ def _operand(t, name, dtype, device, dim=2, rows=None, cols=None):
     r, c = shape[-2], shape[-1]
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError("%s is %s: %s x %s is wanted" % (name, tuple(shape), rows, cols))
+    if r > _MOST_INT or c > _MOST_INT or shape[0] > _MOST_INT:
+        _extent(max(shape), name)
     if t.is_contiguous():
         return c if c > 1 else 1
     if t.numel() == 0:
@@ -380,7 +391,7 @@ def _operand(t, name, dtype, device, dim=2, rows=None, cols=None):
     if r > 1:
         if t.stride(-2) < c:
             raise ValueError("%s has overlapping rows" % name)
-        return t.stride(-2)
+        return _extent(t.stride(-2), name)
     return max(1, c)
 
 
@@ -479,7 +490,7 @@ def grouped_wgrad(X, G, offsets, D=None, alpha: float = 1.0, beta: float = 0.0, 
     N = G.shape[1]
     if offsets.dim() != 1 or offsets.shape[0] < 1:
         raise ValueError("offsets must be a vector of groups + 1 row numbers")
-    groups = offsets.shape[0] - 1
+    groups = _extent(offsets.shape[0] - 1, "offsets")
     off = _vector(offsets, "offsets", torch.int32, dev, groups + 1)
     if D is not None and D.shape[0] != groups:
         raise ValueError("D has %d groups, offsets %d" % (D.shape[0], groups))
@@ -590,7 +601,7 @@ def q4_quantize(W, block: int = 128, zeros: bool = True, stream=None):
     if W.dim() == 3 and W.shape[0] > 1 and W.numel() and W.stride(0) != N * ldw:
         raise ValueError("W's groups must follow one another")
     blocks = -(-K // block)
-    rows = N * (lead[0] if lead else 1)
+    rows = _extent(N * (lead[0] if lead else 1), "W as one matrix")
     Q = S = Z = None
 
     def body(s):
@@ -629,6 +640,7 @@ def q4_matvec(X, Q, scales, zeros=None, block: int = 128, Y=None, offsets=None, 
         raise ValueError("Q holds %d weights a row, X %d values" % (2 * bytes_, K))
     per_block = (*lead, N, -(-K // block))
     pq = _packed(Q, "Q", torch.uint8, dev, Q.shape)
+    _extent(N if N > groups else groups, "Q")
     ps = _packed(scales, "scales", X.dtype, dev, per_block)
     pz = _packed(zeros, "zeros", torch.uint8, dev, per_block) if zeros is not None else 0
     off = _vector(offsets, "offsets", torch.int32, dev, groups + 1) if offsets is not None else 0

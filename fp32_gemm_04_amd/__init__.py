@@ -535,6 +535,8 @@ def linear_cross_entropy(X, W, targets, stream=None):
         nonlocal loss, lse
         loss, lse = (X.new_empty(rows, dtype=torch.float32) for _ in range(2))
         n = _lib.sgemm_xent_workspace(t, rows, vocab, K, 0)
+        if n < 0:
+            return n
         ws = X.new_empty(n, dtype=torch.uint8)
         return _lib.sgemm_xent(t, rows, vocab, K, X.data_ptr(), ldx, W.data_ptr(), ldw, tg,
                                loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), n, s)
@@ -563,6 +565,8 @@ def linear_cross_entropy_backward(dloss, X, W, targets, lse, dX=None, dW=None, n
         if need_dW and dW is None:
             dW = X.new_empty(vocab, K)
         n = _lib.sgemm_xent_workspace(t, rows, vocab, K, 1)
+        if n < 0:
+            return n
         ws = X.new_empty(n, dtype=torch.uint8)
         return _lib.sgemm_xent_backward(t, rows, vocab, K, X.data_ptr(), ldx, W.data_ptr(), ldw, tg,
                                         pl, pd, dX.data_ptr() if need_dX else 0, lddx,

@@ -52,3 +52,19 @@ CALLS = {
 def test_sizes_past_an_int_are_refused(call):
     with FakeTensorMode(), pytest.raises(ValueError, match="extent or stride of [0-9]{10}"):
         CALLS[call]()
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_sizes_that_the_library_refuses_name_the_parameter(monkeypatch, backward):
+    """Sizes that an int holds and the library does not take: its status comes back, from the
+    workspace's size already."""
+    monkeypatch.setattr(sg, "_current_device", lambda: 0)
+    monkeypatch.setattr(sg, "_current_stream", lambda index: 0)
+    with FakeTensorMode(), pytest.raises(sg.SgemmError, match="parameter 3") as e:
+        X, W, t = fake(1, 0), fake(2 ** 31 - 1, 0), targets(1)
+        if backward:
+            row = fake(1, dtype=torch.float32)
+            sg.linear_cross_entropy_backward(row, X, W, t, row)
+        else:
+            sg.linear_cross_entropy(X, W, t)
+    assert e.value.status == -3

@@ -9,8 +9,9 @@
  * kernels on `stream` and return, and allocate, free, copy and synchronise
  * nothing, so they may be captured into a HIP graph.  Outputs must not
  * overlap inputs.  Argument errors are returned as -p (p counts the first
- * parameter as 1) before any HIP call; a positive value is the hipError_t of a
- * failed HIP call.  The calls are re-entrant: they share no state but a
+ * parameter as 1) before any HIP call, but for a workspace that is too small: the
+ * size that it needs depends on the current device, which is asked for its compute
+ * units first.  A positive value is the hipError_t of a failed HIP call.  The calls are re-entrant: they share no state but a
  * per-device cache of the compute-unit count, and workspaces are the
  * caller's, one per call in flight (also one per captured graph that may run
  * beside another).

@@ -190,8 +190,8 @@ int sgemm_q4_matvec(int type, int groups, int rows, int N, int K, int block, con
  * sgemm_q4_quantize -- the nearest weights of that form to W (N x K of `type`,
  * values below 2^127 in magnitude): per block, with Z: scale (max(w, 0) - min(w, 0)) / 15 and the
  * zero that makes the smallest weight 0; without (Z NULL): scale max|w| / 7
- * around 8.  The scale is rounded to `type` first and q to the nearest integer
- * (ties to even) of w / scale + zero, clamped to 0 .. 15.  A block whose scale
+ * around 8.  The scale is rounded to `type` first; q is the nearest integer to w / scale
+ * (ties to even), plus the zero, clamped to 0 .. 15.  A block whose scale
  * rounds to zero reads back as zeros.
  * Returns -1 type, -2 N < 0, -3 K < 0 or odd, -4 block, -5 W, -6 ldw, -7 Q, -8 S.
  */

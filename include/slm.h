@@ -157,8 +157,9 @@ int64_t sgemm_xent_workspace(int type, int rows, int vocab, int K, int backward)
  * sgemm_q4_matvec -- rows times weights held in 4 bits: for each group e, on
  * its rows r,
  *     Y[r][n] <- sum_k X[r][k] * (q_e[n][k] - z_e[n][b]) * s_e[n][b],  b = k / block
- * One pass over the weights serves up to 64 rows of a group together, so this is
- * meant for single tokens and short batches; any number of rows is computed.
+ * One pass over the weights serves up to 64 bf16 or 24 fp32 rows together (with
+ * offsets, no more than twice a group's mean), so this is meant for single tokens and
+ * short batches; any number of rows is computed, in passes of so many.
  *
  *   type      enum sgemm_type of X, S and Y
  *   groups    sets of weights (1 when offsets is NULL), at most 65535

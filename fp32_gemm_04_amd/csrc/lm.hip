@@ -336,11 +336,13 @@ XentPlan xent_plan(int type, bool fast, int rows, int vocab, int K, int cus)
     p.piece = round_up(ceil_div(vocab, p.pieces), 256);
     p.pieces = ceil_div(vocab, p.piece);
     p.ld = p.piece + 64;
-    // Few rows: a row's gradient is mostly one derivative's (its target's), whose rounding
-    // to bf16 would shift the whole row by up to 2^-8.  So what the rounding leaves over is
-    // kept as further rows; with many rows the roundings average out (T 384: 0.0022 off
-    // against 0.0017 of an fp32 sum rounded once; one row: 0.0034), and here the time is
-    // that of reading W and writing dW, whatever the rows.
+    // A row's gradient is mostly one derivative's (its target's), whose rounding to bf16
+    // shifts the whole row by up to 2^-8 (one row: 0.0034 off, against 0.0017 of an fp32 sum
+    // rounded once).  With few rows, where the time is that of reading W and writing dW, what
+    // the rounding leaves over is kept as further rows.  With many it would double the
+    // products' work, so each derivative is rounded, as a stored gradient of the type would
+    // be (T 384: 0.0022 off), also where all round the same way, as with one dloss in all
+    // rows.
     p.low_rows = type != SGEMM_TYPE_BF16 || rows > 128 ? 0
                  : rows <= 8                           ? 8
                  : rows <= 16                          ? 16

@@ -129,9 +129,10 @@ int sgemm_xent(int type, int rows, int vocab, int K, const void *X, int ldx, con
  *     dX[t][k] = sum_v d[t][v] W[v][k]      dW[v][k] = sum_t d[t][v] X[t][k]
  * The logits are computed again, a piece of the vocabulary at a time; d is
  * held in `type` for one piece (bf16 rounds each d once, by at most 2^-8 of
- * itself, as a stored gradient of that type would; with up to 128 rows, where the
- * roundings would not average out, what they leave over is kept beside it), and
- * both products sum in fp32 over all pieces.  A row that does not count adds 0 *
+ * itself, as a stored gradient of that type would; with up to 128 rows what that leaves
+ * over is kept beside it, so that d has 16 bits), and both products sum in fp32 over
+ * all pieces.  These roundings need not average out: with the same dloss in every
+ * row, the derivatives at the targets, all close to -dloss, round the same way.  A row that does not count adds 0 *
  * X[t][k] to dW: X must be finite there.
  *
  *   lse       as sgemm_xent gave it

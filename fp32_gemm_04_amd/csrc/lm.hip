@@ -9,27 +9,12 @@
 #include <cstdint>
 
 #include "../../include/slm.h"
+#include "lm_host.hpp"
 #include "lm_kernels.hpp"
 
 namespace sgemm {
 namespace lm {
-namespace {
 
-// Without a device, sizes are those of a whole MI355X (the call then fails).
-constexpr int kNoDeviceUnits = 256;
-
-// Largest extent taken: tile edges past the end of a matrix stay within int.
-constexpr int kMostExtent = INT_MAX - 1024;
-
-// Most workgroups of 256 a launch takes along x: below 2^32 work items.
-constexpr int kMostBlocks = (1 << 24) - 1;
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
-int elem_size(int type) { return type == SGEMM_TYPE_BF16 ? 2 : 4; }
-bool aligned(const void *p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-// Compute units of the current device (cached; 0 on failure, with the error in *rc).
 int compute_units(int *rc)
 {
     static std::atomic<int> cache[64];
@@ -47,6 +32,13 @@ int compute_units(int *rc)
     *rc = e == hipSuccess ? (int)hipErrorInvalidDevice : (int)e;
     return 0;
 }
+
+namespace {
+
+// Without a device, sizes are those of a whole MI355X (the call then fails).
+constexpr int kNoDeviceUnits = 256;
+
+int elem_size(int type) { return type == SGEMM_TYPE_BF16 ? 2 : 4; }
 
 // An operand the direct loads take: rows at 4-byte addresses, and tile offsets below 2^31.
 bool fast_operand(const void *p, int64_t ld, int64_t group_stride, int size)

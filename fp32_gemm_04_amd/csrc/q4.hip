@@ -3,41 +3,24 @@
 // here allocates, frees, copies or synchronises.
 #include <hip/hip_runtime.h>
 
-#include <atomic>
-#include <climits>
 #include <cstdint>
 
 #include "../../include/slm.h"
+#include "lm_host.hpp"
 #include "q4.hpp"
 
 namespace sgemm {
 namespace q4 {
 namespace {
 
-// Largest extents taken: a workgroup's offsets stay within 32 bits.
-constexpr int kMostExtent = INT_MAX - 1024, kMostK = 1 << 27;
+using lm::aligned;
+using lm::ceil_div;
+using lm::compute_units;
+using lm::kMostBlocks;
+using lm::kMostExtent;
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-bool aligned(const void *p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-// Compute units of the current device (cached; 0 on failure, with the error in *rc).
-int compute_units(int *rc)
-{
-    static std::atomic<int> cache[64];
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e == hipSuccess && dev >= 0 && dev < 64) {
-        int n = cache[dev].load(std::memory_order_relaxed);
-        if (n > 0) return n;
-        e = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev);
-        if (e == hipSuccess && n > 0) {
-            cache[dev].store(n, std::memory_order_relaxed);
-            return n;
-        }
-    }
-    *rc = e == hipSuccess ? (int)hipErrorInvalidDevice : (int)e;
-    return 0;
-}
+// A workgroup's offsets stay within 32 bits.
+constexpr int kMostK = 1 << 27;
 
 struct Form {
     int rt, nt;
@@ -181,7 +164,6 @@ extern "C" int sgemm_q4_quantize(int type, int N, int K, int block, const void *
     if ((work && !S) || !aligned(S, size)) return -8;
     if (!work) return 0;
     const int nblk = (int)ceil_div(K, block);
-    constexpr int64_t kMostBlocks = (1 << 24) - 1;  // of 256: below 2^32 work items
     const int64_t blocks = ceil_div((int64_t)N * nblk, 16);
     const dim3 grid((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks));
     if (type == SGEMM_TYPE_BF16)

@@ -11,6 +11,7 @@
 #include "../../include/slm.h"
 #include "lm_host.hpp"
 #include "lm_kernels.hpp"
+#include "lm_rule.hpp"
 
 namespace sgemm {
 namespace lm {
@@ -67,53 +68,6 @@ int launch(const TileKernel &k, TileArgs &a, int64_t blocks, int slices, hipStre
     return (int)hipGetLastError();
 }
 
-// What a tile costs: outputs times contraction over `rate`, the rate its kernel reaches
-// on a compute unit relative to the largest tile's, `lead` being the contraction's worth
-// of time that filling the ring and writing the tile take when nothing else runs on the
-// unit (the 256 tile leaves no room for a second workgroup).  Measured, bf16: T 8192, H 2048, V
-// 131072 with gradients 15.9 ms with the 256 tile, 16.9 with 128 x 192; T 384, H 1024, V
-// 50021 369 and 277 us; 16 experts' backward pass of 16384 rows 381 and 349 us (128 x
-// 128: 403, 64 x 128: 477).  fp32: T 1023, H 1000, V 49999 3.22 ms with the 128 tile,
-// 3.35 with 64 x 64; 24 experts' backward pass of 1500 rows 93 and 63 us; the loss of 37
-// rows (H 1024, V 32000) 45.9 us with 64 x 64 and 39.6 with 48 x 128, of 140 rows 114 and 90.
-struct TileCost {
-    int bm, bn;
-    double rate;
-    int lead;
-};
-const TileCost kBf16Tiles[NUM_TILES] = {
-    {16, 64, 0.2, 64}, {32, 128, 0.45, 64}, {0, 0, 0, 0}, {64, 128, 0.65, 64}, {128, 128, 0.8, 64}, {128, 192, 0.88, 64},
-    {256, 256, 1.0, 256}};
-const TileCost kF32Tiles[NUM_TILES] = {
-    {16, 64, 0.5, 64}, {32, 64, 0.75, 64}, {48, 128, 0.9, 64}, {64, 64, 0.87, 64}, {128, 128, 1.0, 64}, {0, 0, 0, 0}, {0, 0, 0, 0}};
-
-// The tile that finishes first when every compute unit takes the same number of tiles
-// (a last one that has the unit to itself counts half where two fit beside each other):
-// products of N columns and contraction K, whose rows split into row_tiles(bm) tiles in
-// all.
-template <typename RowTiles>
-int choose_tile(int type, int form, bool fast, RowTiles row_tiles, int64_t N, int64_t K, int cus)
-{
-    const TileCost *t = type == SGEMM_TYPE_BF16 ? kBf16Tiles : kF32Tiles;
-    int best = S16;
-    double least = 0;
-    for (int i = 0; i < (fast ? (int)NUM_TILES : T128 + 1); ++i) {
-        if (t[i].bm == 0 || (i == M48 && (form == F_SUM || form == F_DW))) continue;
-        const int64_t tiles = row_tiles(t[i].bm) * ceil_div(N, t[i].bn);
-        const bool pairs = t[i].lead == 64 && tiles > cus;
-        const double rounds = pairs ? 0.5 * ceil_div(2 * tiles, cus) : (double)ceil_div(tiles, cus);
-        const double cost = rounds * t[i].bm * t[i].bn * (K + t[i].lead) / t[i].rate;
-        if (i == 0 || cost < least) best = i, least = cost;
-    }
-    return best;
-}
-
-// For one product of M x N outputs.
-int plain_tile(int type, int form, bool fast, int64_t M, int64_t N, int64_t K, int cus)
-{
-    return choose_tile(type, form, fast, [&](int bm) { return ceil_div(M, bm); }, N, K, cus);
-}
-
 }  // namespace
 }  // namespace lm
 }  // namespace sgemm
@@ -152,12 +106,7 @@ extern "C" int sgemm_grouped(int type, int trans, int groups, int rows, int N, i
     const int kk = reads ? K : 0;
     const bool fast = kk == 0 || (fast_operand(X, ldx, 0, size) &&
                                   fast_operand(W, ldw, stride_w, size));
-    // A group's last tile is half full on average.
-    const auto row_tiles = [&](int bm) {
-        const int64_t t = rows / bm + used / 2;
-        return t > used ? t : (int64_t)used;
-    };
-    const int tile = choose_tile(type, F_ROWS_N, fast, row_tiles, N, kk, cus);
+    const int tile = rows_tile(size, fast, used, rows, N, kk, cus);
     const TileKernel k = kernel_for(type, trans ? F_ROWS_T : F_ROWS_N, tile, fast);
     // Every group's last tile may be part full.
     const int64_t most = (rows + (int64_t)used * (k.bm - 1)) / k.bm;
@@ -210,8 +159,7 @@ extern "C" int sgemm_grouped_wgrad(int type, int groups, int rows, int M, int N,
     const int kk = reads ? rows : 0;  // 0: every group is empty
     const bool fast = kk == 0 || (fast_operand(X, ldx, 0, size) &&
                                   fast_operand(G, ldg, 0, size));
-    const auto row_tiles = [&](int bm) { return ceil_div(M, bm) * groups; };
-    const int tile = choose_tile(type, F_SUM, fast, row_tiles, N, kk / groups, cus);
+    const int tile = sum_tile(size, fast, groups, kk, M, N, cus);
     const TileKernel k = kernel_for(type, F_SUM, tile, fast);
     const int64_t blocks = ceil_div(M, k.bm) * ceil_div(N, k.bn) * groups;
     TileArgs a = {};
@@ -304,73 +252,6 @@ __global__ void __launch_bounds__(256) xent_sum_kernel(int rows, int low_rows, i
     }
 }
 
-// How the backward pass is cut: `piece` columns of the vocabulary at a time, and
-// the sum over a piece that gives dX in `slices` (few rows and hidden values
-// leave compute units idle otherwise).
-struct XentPlan {
-    int64_t piece, pieces, ld;  // ld: leading dimension of the piece's derivatives
-    int slices, dx_tile;
-    int low_rows, d_rows;       // rows to the rounding's remainders (0: not kept); rows in all
-    bool sums;                  // dX goes through fp32 sums in the workspace
-    int64_t d_bytes, bytes;
-};
-
-XentPlan xent_plan(int type, bool fast, int rows, int vocab, int K, int cus)
-{
-    XentPlan p;
-    const int size = elem_size(type);
-    // A piece's derivatives take up to 256 MiB (the last-level cache's size), but a
-    // piece is never narrower than 2048 columns.
-    int64_t most = ((int64_t)256 << 20) / ((int64_t)rows * size) / 256 * 256;
-    if (most < 2048) most = 2048;
-    if (most > (1 << 20) - 256) most = (1 << 20) - 256;  // fast_operand's limit for its rows
-    p.pieces = ceil_div(vocab, most);
-    p.piece = round_up(ceil_div(vocab, p.pieces), 256);
-    p.pieces = ceil_div(vocab, p.piece);
-    p.ld = p.piece + 64;
-    // A row's gradient is mostly one derivative's (its target's), whose rounding to bf16
-    // shifts the whole row by up to 2^-8 (one row: 0.0034 off, against 0.0017 of an fp32 sum
-    // rounded once).  With few rows, where the time is that of reading W and writing dW, what
-    // the rounding leaves over is kept as further rows.  With many it would double the
-    // products' work, so each derivative is rounded, as a stored gradient of the type would
-    // be (T 384: 0.0022 off), also where all round the same way, as with one dloss in all
-    // rows.
-    p.low_rows = type != SGEMM_TYPE_BF16 || rows > 128 ? 0
-                 : rows <= 8                           ? 8
-                 : rows <= 16                          ? 16
-                 : rows <= 32                          ? 32
-                                                       : (int)round_up(rows, 64);
-    p.d_rows = p.low_rows ? 2 * p.low_rows : rows;
-    p.d_bytes = round_up((int64_t)p.d_rows * p.ld * size, 256);
-    // dX may have few tiles and a long sum: where its tiles would not fill the compute
-    // units, the tile is chosen as if the sum were cut as finely as it may be (1024
-    // columns a slice), and cut until each unit has two.
-    const int64_t most_slices = p.piece / 1024 < 1 ? 1 : p.piece / 1024 > 64 ? 64 : p.piece / 1024;
-    p.dx_tile = plain_tile(type, F_PART, fast, p.d_rows, K, p.piece, cus);
-    p.slices = 1;
-    if (ceil_div(p.d_rows, 128) * ceil_div(K, 128) < cus) {
-        p.dx_tile = choose_tile(
-            type, F_PART, fast, [&](int bm) { return ceil_div(p.d_rows, bm) * most_slices; }, K,
-            p.piece / most_slices, cus);
-        const TileCost &t = (type == SGEMM_TYPE_BF16 ? kBf16Tiles : kF32Tiles)[p.dx_tile];
-        const int64_t s = 2 * cus / (ceil_div(p.d_rows, t.bm) * ceil_div(K, t.bn));
-        p.slices = (int)(s < 1 ? 1 : s > most_slices ? most_slices : s);
-    }
-    p.sums = p.low_rows > 0 || p.slices > 1 || (p.pieces > 1 && type != SGEMM_TYPE_F32);
-    p.bytes = p.d_bytes + (p.sums ? (int64_t)p.slices * p.d_rows * K * 4 : 0);
-    return p;
-}
-
-// Each row's value at its target, and its statistics over the columns of each tile, of
-// the narrower of the tiles that run with and without direct loads.
-int64_t stats_bytes(int type, int rows, int vocab, int K, int cus)
-{
-    const TileCost *t = type == SGEMM_TYPE_BF16 ? kBf16Tiles : kF32Tiles;
-    const int a = t[plain_tile(type, F_STATS, true, rows, vocab, K, cus)].bn;
-    const int b = t[plain_tile(type, F_STATS, false, rows, vocab, K, cus)].bn;
-    return round_up((int64_t)rows * 4, 256) + (int64_t)rows * ceil_div(vocab, a < b ? a : b) * 8;
-}
-
 int check_xent(int type, int rows, int vocab, int K, const void *X, int ldx, const void *W, int ldw,
                const int64_t *targets)
 {
@@ -404,10 +285,11 @@ extern "C" int64_t sgemm_xent_workspace(int type, int rows, int vocab, int K, in
     int rc = 0;
     int cus = compute_units(&rc);
     if (cus == 0) cus = kNoDeviceUnits;
-    if (!backward) return stats_bytes(type, rows, vocab, K, cus);
+    const int size = elem_size(type);
+    if (!backward) return stats_bytes(size, rows, vocab, K, cus);
     // Whichever operands the call gets.
-    const int64_t a = xent_plan(type, true, rows, vocab, K, cus).bytes;
-    const int64_t b = xent_plan(type, false, rows, vocab, K, cus).bytes;
+    const int64_t a = xent_plan(size, true, rows, vocab, K, cus).bytes;
+    const int64_t b = xent_plan(size, false, rows, vocab, K, cus).bytes;
     return a > b ? a : b;
 }
 
@@ -422,12 +304,12 @@ extern "C" int sgemm_xent(int type, int rows, int vocab, int K, const void *X, i
     if (rows == 0) return 0;
     int rc = 0;
     const int cus = compute_units(&rc);
-    if (ws_bytes < stats_bytes(type, rows, vocab, K, cus ? cus : kNoDeviceUnits)) return -13;
-    if (cus == 0) return rc;
     const int size = elem_size(type);
+    if (ws_bytes < stats_bytes(size, rows, vocab, K, cus ? cus : kNoDeviceUnits)) return -13;
+    if (cus == 0) return rc;
     const bool fast = K == 0 || (fast_operand(X, ldx, 0, size) &&
                                  fast_operand(W, ldw, 0, size));
-    const int tile = plain_tile(type, F_STATS, fast, rows, vocab, K, cus);
+    const int tile = plain_tile(size, F_STATS, fast, rows, vocab, K, cus);
     const TileKernel k = kernel_for(type, F_STATS, tile, fast);
     float *value = static_cast<float *>(ws);
     float *parts = value + round_up((int64_t)rows * 4, 256) / 4;
@@ -472,7 +354,7 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
         return launch(k, a, ceil_div(vocab, k.bm) * ceil_div(K, k.bn), 1, stream);
     }
     const bool fast_x = fast_operand(X, ldx, 0, size), fast_w = fast_operand(W, ldw, 0, size);
-    const XentPlan p = xent_plan(type, fast_w, rows, vocab, K, cus ? cus : kNoDeviceUnits);
+    const XentPlan p = xent_plan(size, fast_w, rows, vocab, K, cus ? cus : kNoDeviceUnits);
     if (ws_bytes < p.bytes) return -17;
     if (cus == 0) return rc;
     float *sums = reinterpret_cast<float *>(static_cast<char *>(ws) + p.d_bytes);
@@ -485,8 +367,7 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
         {
             const bool fast = fast_x && fast_w;
             const int stored = p.low_rows ? p.low_rows : rows;
-            int tile = plain_tile(type, F_GRAD, fast, stored, n, K, cus);
-            if (p.low_rows && tile == T256) tile = T192;  // the 256 tile keeps no remainders
+            const int tile = grad_tile(size, fast, p, rows, n, K, cus);
             const TileKernel k = kernel_for(type, F_GRAD, tile, fast);
             a = TileArgs{};
             a.A = X, a.B = Wc, a.C = ws;
@@ -501,7 +382,7 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
         }
         if (dW) {
             const bool fast = fast_x;
-            const int tile = plain_tile(type, F_DW, fast, n, K, p.d_rows, cus);
+            const int tile = plain_tile(size, F_DW, fast, n, K, p.d_rows, cus);
             const TileKernel k = kernel_for(type, F_DW, tile, fast);
             a = TileArgs{};
             a.A = ws, a.B = X, a.C = static_cast<char *>(dW) + col0 * lddw * size;
@@ -521,8 +402,8 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
             a.lda = p.ld, a.ldb = ldw;
             a.M = p.d_rows, a.N = K, a.K = n;
             a.a_cols = n8, a.b_cols = K, a.b_rows = n;
-            const bool direct = !p.sums && p.pieces == 1;
-            const TileKernel k = kernel_for(type, direct ? F_DX : F_PART, p.dx_tile, fast);
+            const bool direct = p.dx_form == F_DX;
+            const TileKernel k = kernel_for(type, p.dx_form, p.dx_tile, fast);
             if (direct) {
                 a.C = dX, a.ldc = lddx, a.alpha = 1.f;
                 a.vec_c = vector_rows(dX, lddx, 0, size);

@@ -2,24 +2,11 @@
 // host code (lm.hip) and the translation units that instantiate them.
 #pragma once
 
+#include "lm_rule.hpp"
 #include "lm_tile.hpp"
 
 namespace sgemm {
 namespace lm {
-
-enum Tile { S16, M32, M48, M64, T128, T192, T256, NUM_TILES };
-// The operand layouts and epilogues of the products.
-enum Form {
-    F_ROWS_T,   // grouped rows, weights N x K
-    F_ROWS_N,   // grouped rows, weights K x N
-    F_SUM,      // grouped contraction
-    F_STATS,    // logits to row statistics
-    F_GRAD,     // logits to their derivatives
-    F_PART,     // d W, fp32 sums
-    F_DX,       // d W, rounded to the type
-    F_DW,       // d^T X
-    NUM_FORMS
-};
 
 struct TileKernel {
     TileFn fn;

@@ -36,6 +36,7 @@
 #pragma once
 
 #include "lm_tile.hpp"
+#include "q4_rule.hpp"
 
 namespace sgemm {
 namespace q4 {
@@ -43,9 +44,6 @@ namespace q4 {
 using lm::bf16;
 using lm::bf16x8;
 using lm::u32x4;
-
-constexpr int kWaves = 8;
-constexpr int kThreads = kWaves * 64;
 
 struct Q4Args {
     const void *X;
@@ -129,11 +127,6 @@ __device__ __forceinline__ float block_sum(float v)
     return v;
 }
 
-// Chunks of weights a wave keeps in flight: 4 KB, which with 16 waves on a compute
-// unit covers the latency of memory at its full rate.
-constexpr int ring_depth(int nt) { return nt == 1 ? 4 : 2; }
-constexpr int ring_bytes(int nt) { return kWaves * ring_depth(nt) * nt * 1024; }
-
 // A scale and 16 + its zero as LDS holds them: bf16 scales as two bf16 values in a word
 // (16 + z is exact), fp32 ones as two floats.
 template <typename T> struct Entry {
@@ -152,14 +145,9 @@ template <> struct Entry<float> {
     __device__ float scale() const { return s; }
     __device__ float zero() const { return z; }
 };
-
-// Bytes of LDS after the ring.
-template <typename T>
-inline int slab_bytes(int slab, int block, int cols, int pass)
-{
-    return slab / block * ((cols + 1) * (int)sizeof(Entry<T>) + pass * 4) +
-           Parts<T>::value * pass * (slab * 2 + 16) + 16;
-}
+static_assert(sizeof(Entry<bf16>) == entry_bytes(2) && sizeof(Entry<float>) == entry_bytes(4) &&
+                  Parts<bf16>::value == parts_of(2) && Parts<float>::value == parts_of(4),
+              "what the rule counts with");
 
 // Every wave's LDS writes are done; global loads stay in flight.
 __device__ __forceinline__ void lds_barrier()

@@ -448,9 +448,10 @@ def grouped_gemm(X, W, offsets, Y=None, trans: bool = False, alpha: float = 1.0,
 
     X: (rows, K); W: (groups, K, N), or (groups, N, K) with ``trans``; offsets:
     groups + 1 int32 on the device, increasing; Y: (rows, N), allocated as
-    zeros when None.  float32 or bfloat16, rows may be padded.  Rows outside
-    every group keep what Y holds.  The gradient of X is
-    ``grouped_gemm(dY, W, offsets, trans=not trans)``.  Returns Y.
+    zeros when None (a pass over Y of its own).  float32 or bfloat16, rows may be
+    padded.  Rows outside every group keep what Y holds.  Autograd does not see the
+    product: its gradients are ``grouped_gemm(dY, W, offsets, trans=not trans)`` and
+    ``grouped_wgrad``.  Returns Y.
     """
     t = _type_of(X, "X")
     dev = X.device
@@ -526,7 +527,8 @@ def linear_cross_entropy(X, W, targets, stream=None):
 
     X: (rows, K); W: (vocab, K), float32 or bfloat16; targets: int64, one per
     row; a target outside [0, vocab) marks a row that does not count (loss 0).
-    loss and lse are float32.
+    loss and lse are float32.  Autograd does not see them: the gradients are
+    ``linear_cross_entropy_backward``'s.
     """
     t, dev, ldx, ldw, rows, K, vocab, tg = _xent_operands(X, W, targets)
     loss = lse = None

@@ -23,7 +23,7 @@ FLAGS = [
 # the ILP machine scheduler: with the default one the accumulators of the
 # two unrolled slabs are renamed and copied back every iteration (measured
 # on the 160x160 kernel: 10 extra 64-bit moves per loop trip).  The other
-# kernels keep the default, under which they do not spill.
+# kernels keep the default.
 SOURCES = {
     "sgemm.hip": [],
     "mfma_dl.hip": ["-Xarch_device", "-mllvm=--misched=gcn-max-ilp"],

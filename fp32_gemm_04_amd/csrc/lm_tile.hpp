@@ -306,7 +306,8 @@ __device__ __forceinline__ int64_t scan_tiles(const int *offsets, int groups, in
 // Why this form: slabs of 128 bytes, since 64 with twice the buffers doubled the barriers
 // and were slower; operands half a slab ahead, so that reads of LDS hide behind products
 // of one wave per SIMD; no workgroup stays for a second tile (no gain, and the 256 tile
-// spilled).
+// spilled).  Two forms of the 256 tile spill outside their loops: row statistics 32
+// registers (written with them: 302 MB instead of 34 at T 8192, V 131072), partial sums 8.
 template <typename T, int BM, int BN, int WM, int WN, int NBUF, int BL, int WPE, Layout LA,
           Layout LB, Ragged RG, Epilogue EP, bool FAST>
 __global__ void __launch_bounds__(WM *WN * 64) __attribute__((amdgpu_waves_per_eu(WPE)))

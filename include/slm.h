@@ -103,7 +103,9 @@ int sgemm_grouped_wgrad(int type, int groups, int rows, int M, int N, float alph
  *     lse[t]  = log(sum_v exp(z[t][v]))
  *     loss[t] = lse[t] - z[t][targets[t]]
  * without keeping the logits: tiles of them are reduced to a maximum and a sum
- * of exponentials per row.
+ * of exponentials per row.  Finite logits have to lie below 2^126 in magnitude.  The
+ * loss is never below 0, and its roundings are relative to the target's distance
+ * from the row's largest logit, not to lse.
  *
  *   rows, vocab, K   >= 0 (rows tokens, K hidden values; vocab >= 1 if rows > 0)
  *   X, ldx    rows x K of `type`;  W, ldw: vocab x K of `type`
@@ -135,7 +137,8 @@ int sgemm_xent(int type, int rows, int vocab, int K, const void *X, int ldx, con
  * row, the derivatives at the targets, all close to -dloss, round the same way.  A row that does not count adds 0 *
  * X[t][k] to dW: X must be finite there.
  *
- *   lse       as sgemm_xent gave it
+ *   lse       as sgemm_xent gave it (its rounding, 2^-24 of lse, is one of
+ *             every exp(z - lse))
  *   dloss     rows floats, the gradient of each row's loss
  *   dX, lddx  rows x K of `type`, or NULL: not computed
  *   dW, lddw  vocab x K of `type`, or NULL: not computed

@@ -287,6 +287,7 @@ extern "C" int64_t sgemm_xent_workspace(int type, int rows, int vocab, int K, in
     if (cus == 0) cus = kNoDeviceUnits;
     const int size = elem_size(type);
     if (!backward) return stats_bytes(size, rows, vocab, K, cus);
+    if (K == 0) return 0;  // the gradients have no elements
     // Whichever operands the call gets.
     const int64_t a = xent_plan(size, true, rows, vocab, K, cus).bytes;
     const int64_t b = xent_plan(size, false, rows, vocab, K, cus).bytes;
@@ -341,7 +342,7 @@ extern "C" int sgemm_xent_backward(int type, int rows, int vocab, int K, const v
     if (lddx < (K > 1 ? K : 1)) return -13;
     if (!aligned(dW, size)) return -14;
     if (lddw < (K > 1 ? K : 1)) return -15;
-    if ((rows > 0 && !ws) || !aligned(ws, 16)) return -16;
+    if ((rows > 0 && K > 0 && !ws) || !aligned(ws, 16)) return -16;
     if (K == 0 || vocab == 0 || (!dX && !dW) || (rows == 0 && !dW)) return 0;
     int rc = 0;
     const int cus = compute_units(&rc);

@@ -102,6 +102,7 @@ struct XentPlan {
     int64_t d_bytes, bytes;
 };
 
+// Every extent at least 1.
 inline XentPlan xent_plan(int size, bool fast, int rows, int vocab, int K, int cus)
 {
     XentPlan p;

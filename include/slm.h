@@ -183,7 +183,8 @@ int64_t sgemm_xent_workspace(int type, int rows, int vocab, int K, int backward)
  * -7 X, -8 ldx, -9 Q, -10 S, -12 Y, -13 ldy, -14 offsets not 4-byte aligned.
  *
  * Accuracy: fp32 rows keep their 24 bits (they are multiplied as three exact
- * bf16 parts); with w the dequantised weights, sums are within about
+ * bf16 parts; of values below 2^-110 in magnitude what lies under 2^-133 is lost);
+ * with w the dequantised weights, sums are within about
  * 4 K 2^-24 sum_b |s| sum_k (16 + q) |x| of the exact value.  A row that holds an
  * infinity, a NaN, or a value beyond 2^118 in magnitude may come out as NaN.
  */

@@ -115,3 +115,18 @@ def test_exact(dtype, case):
 def test_exact_with_all_bits_of_fp32(case):
     say("q4 bits", case)
     run(case, F32, True, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("block", [32, 128])
+@pytest.mark.parametrize("power", [-100, -126, -133, -137])
+def test_small_values_of_fp32(block, power):
+    """Down to bits of 2^-133 everything is kept, below it what the last part holds under that:
+    at most 2^-133 a value, times up to 31."""
+    say("q4 small", block, power)
+    K = 520
+    X, Q, S, Z = (t.cuda() for t in operands((0, 7, 41, K, block), True))
+    X *= 2.0 ** power
+    Y = sg.q4_matvec(X, Q, S, Z, block=block).double()
+    lost = 0 if power >= -133 else 4 * 31 * 2.0 ** -133
+    assert ((Y - product(X, Q, S, Z, K, block)).abs() <= lost).all()

@@ -48,7 +48,10 @@ EXPORTS = ("sgemm_f32", "sgemm_f32_variant", "sgemm_plan", "sgemm_tune", "sgemm_
            "sconv2d_num_stem_kernels",
            # include/slm.h
            "sgemm_grouped", "sgemm_grouped_wgrad", "sgemm_xent", "sgemm_xent_backward",
-           "sgemm_xent_workspace", "sgemm_q4_matvec", "sgemm_q4_quantize")
+           "sgemm_xent_workspace", "sgemm_q4_matvec", "sgemm_q4_quantize",
+           "sgemm_expert_sort", "sgemm_expert_sort_workspace", "sgemm_expert_gather",
+           "sgemm_expert_combine", "sgemm_expert_combine_backward", "sgemm_q8_quantize",
+           "sgemm_q8_gemm", "sgemm_q8_matvec")
 
 if not os.path.exists(LIBRARY):
     raise ImportError("libsgemm.so is not built; run __graft_entry__.build() "
@@ -105,11 +108,20 @@ for _name, _args in {
         "sgemm_xent_backward": [_i] * 4 + [_p, _i, _p, _i] + [_p] * 4 + [_i, _p, _i, _p, _i64, _p],
         "sgemm_q4_matvec": [_i] * 6 + [_p, _i, _p, _p, _p, _p, _i, _p, _p],
         "sgemm_q4_quantize": [_i] * 4 + [_p, _i, _p, _p, _p, _p],
+        "sgemm_expert_sort": [_i] * 2 + [_p] * 5 + [_i64, _p],
+        "sgemm_expert_gather": [_i] * 4 + [_p, _i, _p, _p, _i, _p, _i, _i, _p],
+        "sgemm_expert_combine": [_i] * 5 + [_p, _i, _p, _p, _f, _p, _i, _p],
+        "sgemm_expert_combine_backward": [_i] * 5 + [_p, _i, _p, _i, _p, _p, _p, _i, _i, _p, _p],
+        "sgemm_q8_quantize": [_i] * 3 + [_p, _i, _i, _p, _i, _p, _i, _p, _p],
+        "sgemm_q8_gemm": [_i] * 5 + [_p, _i, _p, _p, _i, _i64, _p, _p, _i, _p, _p],
+        "sgemm_q8_matvec": [_i] * 5 + [_p, _i, _p, _i, _i64, _p, _p, _i, _p, _p],
 }.items():
     getattr(_lib, _name).restype = ctypes.c_int
     getattr(_lib, _name).argtypes = _args
 _lib.sgemm_xent_workspace.restype = ctypes.c_int64
 _lib.sgemm_xent_workspace.argtypes = [ctypes.c_int] * 5
+_lib.sgemm_expert_sort_workspace.restype = ctypes.c_int64
+_lib.sgemm_expert_sort_workspace.argtypes = [ctypes.c_int] * 2
 
 
 class SgemmError(RuntimeError):
@@ -355,6 +367,56 @@ def sgemm_q4_matvec(type, groups, rows, N, K, block, X, ldx, Q, S, Z, Y, ldy, of
 def sgemm_q4_quantize(type, N, K, block, W, ldw, Q, S, Z, stream=0) -> int:
     """C ABI ``sgemm_q4_quantize``.  Returns the status."""
     return _lib.sgemm_q4_quantize(type, N, K, block, W, ldw, Q, S, Z, stream)
+
+
+def sgemm_expert_sort(slots, groups, experts, offsets, order, place, ws, ws_bytes, stream=0) -> int:
+    """C ABI ``sgemm_expert_sort``.  Returns the status."""
+    return _lib.sgemm_expert_sort(slots, groups, experts, offsets, order, place, ws, ws_bytes, stream)
+
+
+def sgemm_expert_sort_workspace(slots, groups) -> int:
+    """C ABI ``sgemm_expert_sort_workspace``: bytes, or a negative status."""
+    return _lib.sgemm_expert_sort_workspace(slots, groups)
+
+
+def sgemm_expert_gather(type, tokens, k, H, X, ldx, place, weights, rows, R, ldr, fill,
+                        stream=0) -> int:
+    """C ABI ``sgemm_expert_gather``.  Returns the status."""
+    return _lib.sgemm_expert_gather(type, tokens, k, H, X, ldx, place, weights, rows, R, ldr, fill,
+                                    stream)
+
+
+def sgemm_expert_combine(type, tokens, k, H, rows, R, ldr, place, weights, beta, out, ldo,
+                         stream=0) -> int:
+    """C ABI ``sgemm_expert_combine``.  Returns the status."""
+    return _lib.sgemm_expert_combine(type, tokens, k, H, rows, R, ldr, place, weights, beta, out,
+                                     ldo, stream)
+
+
+def sgemm_expert_combine_backward(type, tokens, k, H, rows, dout, lddo, R, ldr, place, weights, dR,
+                                  lddr, fill, dweights, stream=0) -> int:
+    """C ABI ``sgemm_expert_combine_backward``.  Returns the status."""
+    return _lib.sgemm_expert_combine_backward(type, tokens, k, H, rows, dout, lddo, R, ldr, place,
+                                              weights, dR, lddr, fill, dweights, stream)
+
+
+def sgemm_q8_quantize(type, rows, K, X, ldx, k, place, out_rows, Q, ldq, scales, stream=0) -> int:
+    """C ABI ``sgemm_q8_quantize``.  Returns the status."""
+    return _lib.sgemm_q8_quantize(type, rows, K, X, ldx, k, place, out_rows, Q, ldq, scales, stream)
+
+
+def sgemm_q8_gemm(type, groups, rows, N, K, X, ldx, x_scales, W, ldw, stride_w, w_scales, Y, ldy,
+                  offsets, stream=0) -> int:
+    """C ABI ``sgemm_q8_gemm``.  Returns the status."""
+    return _lib.sgemm_q8_gemm(type, groups, rows, N, K, X, ldx, x_scales, W, ldw, stride_w, w_scales,
+                              Y, ldy, offsets, stream)
+
+
+def sgemm_q8_matvec(type, groups, rows, N, K, X, ldx, W, ldw, stride_w, w_scales, Y, ldy, offsets,
+                    stream=0) -> int:
+    """C ABI ``sgemm_q8_matvec``.  Returns the status."""
+    return _lib.sgemm_q8_matvec(type, groups, rows, N, K, X, ldx, W, ldw, stride_w, w_scales, Y, ldy,
+                                offsets, stream)
 
 
 _TYPES = {torch.float32: SGEMM_TYPE_F32, torch.bfloat16: SGEMM_TYPE_BF16}
@@ -659,4 +721,245 @@ def q4_matvec(X, Q, scales, zeros=None, block: int = 128, Y=None, offsets=None, 
         return _lib.sgemm_q4_matvec(t, groups, rows, N, K, block, X.data_ptr(), ldx, pq, ps, pz,
                                     Y.data_ptr(), ldy, off, s)
     _run("sgemm_q4_matvec", dev, stream, (X, Q, scales, zeros, Y, offsets), body)
+    return Y
+
+
+def expert_sort(experts, groups: int, stream=None):
+    """(offsets, order, place): rows for each token's choices of expert, sorted by expert
+    and, within one, by token (``sgemm_expert_sort``).
+
+    experts: (tokens, k) int64, packed; a choice outside [0, groups) is dropped (padding,
+    or another device's expert); groups at most 4096.  offsets: groups + 1 int32, as the
+    grouped products take them; order: int32, the slot t * k + j of each row, those
+    dropped last; place: (tokens, k) int32, each choice's row r, or -2 - r where it is dropped
+    and r is one of the rows behind the last expert's.
+    """
+    if experts.dtype is not torch.int64 or experts.dim() != 2:
+        raise TypeError("experts must be a 2-D int64 tensor, not %d-D %s"
+                        % (experts.dim(), experts.dtype))
+    dev = experts.device
+    if not experts.is_cuda or not experts.is_contiguous():
+        raise ValueError("experts must be packed on a GPU")
+    slots = _extent(experts.numel(), "experts")
+    _extent(groups, "groups")
+    offsets = order = place = None
+
+    def body(s):
+        nonlocal offsets, order, place
+        n = _lib.sgemm_expert_sort_workspace(slots, groups)
+        if n < 0:
+            return n
+        offsets = experts.new_empty(groups + 1, dtype=torch.int32)
+        order = experts.new_empty(slots, dtype=torch.int32)
+        place = experts.new_empty(experts.shape, dtype=torch.int32)
+        ws = experts.new_empty(n, dtype=torch.uint8)
+        return _lib.sgemm_expert_sort(slots, groups, experts.data_ptr(), offsets.data_ptr(),
+                                      order.data_ptr(), place.data_ptr(), ws.data_ptr(), n, s)
+    _run("sgemm_expert_sort", dev, stream, (experts,), body)
+    return offsets, order, place
+
+
+def _slots(place, weights, device, tokens, name):
+    """(k, place's pointer, weights' pointer): one row and one weight for each choice."""
+    if place.dim() != 2 or place.shape[0] != tokens:
+        raise ValueError("place must be (%d, k) for the rows of %s" % (tokens, name))
+    _extent(place.numel(), "place")
+    pp = _packed(place, "place", torch.int32, device, place.shape)
+    pw = _packed(weights, "weights", torch.float32, device, place.shape) if weights is not None else 0
+    return place.shape[1], pp, pw
+
+
+def expert_gather(X, place, weights=None, out=None, stream=None):
+    """out[place[t, j]] <- weights[t, j] * X[t]: tokens to their rows sorted by expert
+    (``sgemm_expert_gather``).
+
+    X: (tokens, H), float32 or bfloat16; place as ``expert_sort`` gives it; weights: (tokens,
+    k) float32, or None: 1.  out: (rows, H), whose rows without a choice are left as they were;
+    when None it has tokens * k rows, those of dropped choices zero (for a place of another origin,
+    which may name no choice for a row at all, give ``out``).
+    Autograd does not see the copy: the gradient by X is ``expert_combine(dout, place,
+    weights)``, that by the weights ``expert_combine_backward(X, dout, place,
+    need_dR=False)[1]``.  Returns out.
+    """
+    t = _type_of(X, "X")
+    dev = X.device
+    ldx = _operand(X, "X", X.dtype, dev)
+    tokens, H = X.shape
+    k, pp, pw = _slots(place, weights, dev, tokens, "X")
+    fill = out is None
+    ldo = max(1, H) if fill else _operand(out, "out", X.dtype, dev, 2, None, H)
+
+    def body(s):
+        nonlocal out
+        if out is None:
+            out = X.new_empty(tokens * k, H)
+        return _lib.sgemm_expert_gather(t, tokens, k, H, X.data_ptr(), ldx, pp, pw, out.shape[0],
+                                        out.data_ptr(), ldo, fill, s)
+    _run("sgemm_expert_gather", dev, stream, (X, place, weights, out), body)
+    return out
+
+
+def expert_combine(R, place, weights=None, out=None, beta: float = 0.0, stream=None):
+    """out[t] <- beta * out[t] + sum over j of weights[t, j] * R[place[t, j]]: rows sorted by
+    expert back to their tokens (``sgemm_expert_combine``).
+
+    R: (rows, H), float32 or bfloat16; place and weights as in ``expert_gather``; out: (tokens,
+    H), allocated when None.  A dropped choice adds nothing, whatever its weight.  Autograd
+    does not see the sum: its gradients are ``expert_combine_backward``'s.  Returns out.
+    """
+    t = _type_of(R, "R")
+    dev = R.device
+    ldr = _operand(R, "R", R.dtype, dev)
+    rows, H = R.shape
+    tokens = place.shape[0] if place.dim() else 0
+    k, pp, pw = _slots(place, weights, dev, tokens, "out")
+    ldo = _operand(out, "out", R.dtype, dev, 2, tokens, H) if out is not None else max(1, H)
+
+    def body(s):
+        nonlocal out
+        if out is None:
+            out = (R.new_empty if beta == 0.0 else R.new_zeros)(tokens, H)
+        return _lib.sgemm_expert_combine(t, tokens, k, H, rows, R.data_ptr(), ldr, pp, pw, beta,
+                                         out.data_ptr(), ldo, s)
+    _run("sgemm_expert_combine", dev, stream, (R, place, weights, out), body)
+    return out
+
+
+def expert_combine_backward(dout, R, place, weights=None, dR=None, need_dR: bool = True,
+                            need_dweights: bool = True, stream=None):
+    """(dR, dweights): gradients of sum(dout * out) of ``expert_combine`` by its rows and
+    weights (``sgemm_expert_combine_backward``).
+
+    dout: (tokens, H); R: (rows, H) as the forward pass had it.  dR: (rows, H), whose rows
+    without a choice are left as they were; when None it is allocated, and rows of dropped
+    choices are zero (for a place that ``expert_sort`` did not give, give ``dR``).
+    dweights: (tokens, k) float32, 0 for a dropped choice.  One that is not needed is not
+    computed and comes back as None.
+    """
+    t = _type_of(dout, "dout")
+    dev = dout.device
+    lddo = _operand(dout, "dout", dout.dtype, dev)
+    tokens, H = dout.shape
+    ldr = _operand(R, "R", dout.dtype, dev, 2, None, H)
+    rows = R.shape[0]
+    k, pp, pw = _slots(place, weights, dev, tokens, "dout")
+    dR = dR if need_dR else None
+    fill = dR is None
+    lddr = max(1, H) if fill else _operand(dR, "dR", dout.dtype, dev, 2, rows, H)
+    dw = None
+
+    def body(s):
+        nonlocal dR, dw
+        if need_dR and dR is None:
+            dR = (R.new_empty if rows <= tokens * k else R.new_zeros)(rows, H)
+        if need_dweights:
+            dw = dout.new_empty(place.shape, dtype=torch.float32)
+        return _lib.sgemm_expert_combine_backward(
+            t, tokens, k, H, rows, dout.data_ptr(), lddo, R.data_ptr(), ldr, pp, pw,
+            dR.data_ptr() if need_dR else 0, lddr, fill, dw.data_ptr() if need_dweights else 0, s)
+    _run("sgemm_expert_combine_backward", dev, stream, (dout, R, place, weights, dR), body)
+    return dR, dw
+
+
+def q8_quantize(X, place=None, stream=None):
+    """(Q, scales): each row of X in 8 bits with a scale of its own, the largest magnitude
+    over 127 (``sgemm_q8_quantize``).  A row is Q[r] * scales[r].
+
+    X: (rows, K) or (groups, rows, K) (weights of all experts, packed groups), float32 or
+    bfloat16.  Q: int8 of the same shape, rows padded to a multiple of 16 bytes; scales: float32,
+    one for each row.  With ``place`` ((rows, k) int32, as ``expert_sort`` gives it; X 2-D) row
+    t goes to the k rows place[t] of (rows * k, K), sorted by expert; those of dropped choices are
+    zero.  A row with an infinity or a NaN gets the scale NaN.
+    """
+    t = _type_of(X, "X")
+    dev, lead = X.device, tuple(X.shape[:-2])
+    if X.dim() not in (2, 3) or (place is not None and X.dim() != 2):
+        raise TypeError("X must be 2-D, or 3-D without place")
+    ldx = _operand(X, "X", X.dtype, dev, X.dim())
+    rows, K = X.shape[-2:]
+    if lead and lead[0] > 1 and X.numel() and X.stride(0) != rows * ldx:
+        raise ValueError("X's groups must follow one another")
+    k, pp, _ = _slots(place, None, dev, rows, "X") if place is not None else (0, 0, 0)
+    n = _extent(rows * (lead[0] if lead else 1), "X as one matrix")
+    out = n * k if place is not None else n
+    ldq = _extent(-(-K // 16) * 16 if K else 1, "Q")
+    Q = scales = None
+
+    def body(s):
+        nonlocal Q, scales
+        Q = X.new_empty(lead + (out if place is not None else rows, ldq), dtype=torch.int8)[..., :K]
+        scales = X.new_empty(lead + (out if place is not None else rows,), dtype=torch.float32)
+        return _lib.sgemm_q8_quantize(t, n, K, X.data_ptr(), ldx, k, pp, out, Q.data_ptr(), ldq,
+                                      scales.data_ptr(), s)
+    _run("sgemm_q8_quantize", dev, stream, (X, place), body)
+    return Q, scales
+
+
+def _q8_weights(Q, scales, offsets, device, K):
+    """(groups, N, leading dimension, offsets' pointer, scales' pointer) of 8-bit weights."""
+    if Q.dim() != (2 if offsets is None else 3):
+        raise ValueError("Q must be (N, K), or (groups, N, K) with offsets")
+    groups, N = Q.shape[0] if Q.dim() == 3 else 1, Q.shape[-2]
+    ldw = _operand(Q, "Q", torch.int8, device, Q.dim(), N, K)
+    ps = _packed(scales, "scales", torch.float32, device, Q.shape[:-1])
+    off = _vector(offsets, "offsets", torch.int32, device, groups + 1) if offsets is not None else 0
+    return groups, N, ldw, off, ps
+
+
+def q8_gemm(X, x_scales, Q, scales, offsets=None, Y=None, dtype=torch.bfloat16, stream=None):
+    """Y[r, n] <- (X[r] . Q[n]) * x_scales[r] * scales[n], the sums exact integers
+    (``sgemm_q8_gemm``).
+
+    X: (rows, K) int8 and x_scales: (rows,) as ``q8_quantize`` gives them; Q: (N, K) int8 and
+    scales: (N,), or with ``offsets`` (groups + 1 int32, rows sorted by group) (groups, N, K) and
+    (groups, N).  K at most 131071.  Y: (rows, N), float32 or bfloat16; allocated as ``dtype`` when
+    None (as zeros with offsets).  Rows outside every group keep what Y holds.  Operands whose rows start
+    at multiples of 4 bytes are read fastest.  Returns Y.
+    """
+    dev = X.device
+    ldx = _operand(X, "X", torch.int8, dev)
+    rows, K = X.shape
+    sx = _vector(x_scales, "x_scales", torch.float32, dev, rows)
+    groups, N, ldw, off, ps = _q8_weights(Q, scales, offsets, dev, K)
+    if Y is not None:
+        dtype = Y.dtype
+    t = _TYPES.get(dtype)
+    if t is None:
+        raise TypeError("Y must be float32 or bfloat16, not %s" % dtype)
+    ldy = _operand(Y, "Y", dtype, dev, 2, rows, N) if Y is not None else max(1, N)
+
+    def body(s):
+        nonlocal Y
+        if Y is None:
+            Y = (X.new_empty if offsets is None else X.new_zeros)((rows, N), dtype=dtype)
+        return _lib.sgemm_q8_gemm(t, groups, rows, N, K, X.data_ptr(), ldx, sx, Q.data_ptr(), ldw,
+                                  _groups_of(Q) if offsets is not None else 0, ps, Y.data_ptr(), ldy,
+                                  off, s)
+    _run("sgemm_q8_gemm", dev, stream, (X, x_scales, Q, scales, Y, offsets), body)
+    return Y
+
+
+def q8_matvec(X, Q, scales, Y=None, offsets=None, stream=None):
+    """Y <- ``q8_gemm(*q8_quantize(X), Q, scales)`` in one launch, for a few rows of X
+    (``sgemm_q8_matvec``), bit for bit.
+
+    X: (rows, K), float32 or bfloat16, K at most 106496; Q and scales as in ``q8_gemm``; Y:
+    (rows, N) of X's type, allocated when None (as zeros with ``offsets``).  One pass over the weights serves
+    up to 16 rows.  Returns Y.
+    """
+    t = _type_of(X, "X")
+    dev = X.device
+    ldx = _operand(X, "X", X.dtype, dev)
+    rows, K = X.shape
+    groups, N, ldw, off, ps = _q8_weights(Q, scales, offsets, dev, K)
+    ldy = _operand(Y, "Y", X.dtype, dev, 2, rows, N) if Y is not None else max(1, N)
+
+    def body(s):
+        nonlocal Y
+        if Y is None:
+            Y = (X.new_empty if offsets is None else X.new_zeros)(rows, N)
+        return _lib.sgemm_q8_matvec(t, groups, rows, N, K, X.data_ptr(), ldx, Q.data_ptr(), ldw,
+                                    _groups_of(Q) if offsets is not None else 0, ps, Y.data_ptr(),
+                                    ldy, off, s)
+    _run("sgemm_q8_matvec", dev, stream, (X, Q, scales, Y, offsets), body)
     return Y

@@ -31,6 +31,9 @@ SOURCES = {
     "lm.hip": [],
     "lm_bf16.hip": [],
     "lm_f32.hip": [],
+    "lm_i8.hip": [],
+    "lm_route.hip": [],
+    "lm_q8.hip": [],
     "q4.hip": [],
 }
 

@@ -17,6 +17,8 @@ struct TileKernel {
 // where A's rows are contiguous in memory, since they make no whole 128-byte LDS rows).
 TileKernel bf16_kernel(int form, int tile, bool fast);
 TileKernel f32_kernel(int form, int tile, bool fast);
+// 8-bit operands, both contiguous along the contraction; results scaled to bf16 or fp32.
+TileKernel i8_kernel(bool bf16_out, bool grouped, int tile, bool fast);
 
 template <typename T, int BM, int BN, int WM, int WN, int NBUF, int BL, int WPE, bool FAST>
 TileKernel tile_entry(int form)

@@ -1,0 +1,374 @@
+// Rows in 8-bit integers, and products of a few such rows with 8-bit weights (include/slm.h).
+//
+// Quantisation.  scale = m / 127 with m the row's largest magnitude; q is x / scale
+// rounded to the nearest integer, ties to even, of the exact quotient: rint(x * (1 / scale)) is
+// at most one off, the remainder x - q scale is exact in one fma (it is a multiple of
+// the smaller operand's last bit, below 2 scale), and comparing twice its size
+// with scale says whether, and to which side, q moves.
+#pragma once
+
+#include "lm_tile.hpp"
+
+namespace sgemm {
+namespace lm {
+
+// What a row's values are divided by, scaled by a power of two so that its reciprocal is
+// finite and normal where the scale is tiny.
+struct Quantum {
+    float scale;    // as stored
+    float by;       // power of two
+    float step, inverse;
+    // m: the largest magnitude's bits, in which an infinity or a NaN lies above every number.
+    __device__ __forceinline__ explicit Quantum(uint32_t m)
+    {
+        scale = __builtin_bit_cast(float, m) / 127.f;
+        by = scale < 0x1p-60f ? 0x1p80f : 1.f;
+        step = scale * by;
+        inverse = step > 0.f ? 1.f / step : 0.f;
+        if (m >= 0x7f800000u) {
+            scale = __builtin_nanf("");
+            by = inverse = step = 0.f;
+        }
+    }
+    __device__ __forceinline__ int of(float x) const
+    {
+        if (!(inverse > 0.f)) return 0;
+        const float v = x * by;
+        float q = rintf(v * inverse);
+        const float left = fmaf(-q, step, v), twice = 2.f * fabsf(left);
+        // On a tie the even neighbour stays.
+        if (twice > step || (twice == step && ((int)q & 1))) q += left > 0.f ? 1.f : -1.f;
+        const int i = (int)q;
+        return i > 127 ? 127 : i < -127 ? -127 : i;
+    }
+};
+
+__device__ __forceinline__ uint32_t magnitude(float x)
+{
+    return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const uint32_t u = __shfl_xor(v, d);
+        v = u > v ? u : v;
+    }
+    return v;
+}
+
+// Sixteen values of a row from k on as fp32, zeros from K on.
+template <typename T>
+__device__ __forceinline__ void load16(const T *row, int k, int K, float (&v)[16])
+{
+    if (k + 16 <= K) {
+        T x[16];
+        __builtin_memcpy(x, row + k, sizeof(x));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = (float)x[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = k + i < K ? (float)row[k + i] : 0.f;
+    }
+}
+
+__device__ __forceinline__ uint32_t max16(const float (&v)[16], uint32_t m)
+{
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = magnitude(v[i]) > m ? magnitude(v[i]) : m;
+    return m;
+}
+
+__device__ __forceinline__ u32x4 quantize16(const float (&v)[16], const Quantum &s)
+{
+    u32x4 q;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        uint32_t u = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u |= ((uint32_t)s.of(v[4 * w + i]) & 0xffu) << (8 * i);
+        q[w] = u;
+    }
+    return q;
+}
+
+struct QuantArgs {
+    const void *X;
+    int8_t *Q;
+    float *scales;
+    const int *place;  // or null: row r to row r
+    int64_t ldx, ldq;
+    int rows, K, k, out_rows;
+};
+
+// WAVES waves share a row of X; each lane keeps its first 16 values, and reads what follows again.
+template <typename T, int WAVES>
+__global__ void __launch_bounds__(256) q8_quantize_kernel(QuantArgs a)
+{
+    constexpr int ROWS = 4 / WAVES;
+    __shared__ uint32_t part[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.rows; r0 += (int64_t)gridDim.x * ROWS) {
+        const int64_t r = r0 + wave / WAVES;
+        const bool here = r < a.rows;
+        const T *row = static_cast<const T *>(a.X) + r * a.ldx;
+        const int k0 = ((wave % WAVES) * 64 + lane) * 16, step = WAVES * 64 * 16;
+        float first[16], v[16];
+        uint32_t m = 0;
+        if (here) {
+            load16(row, k0, a.K, first);
+            m = max16(first, m);
+            for (int k = k0 + step; k < a.K; k += step) {
+                load16(row, k, a.K, v);
+                m = max16(v, m);
+            }
+        }
+        m = wave_max(m);
+        if constexpr (WAVES > 1) {
+            if (lane == 0) part[wave] = m;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) {
+                const uint32_t u = part[wave / WAVES * WAVES + w];
+                m = u > m ? u : m;
+            }
+            __syncthreads();
+        }
+        if (!here) continue;
+        const Quantum s(m);
+        const int copies = a.place ? a.k : 1;
+        for (int k = k0; k < a.K || k == k0; k += step) {
+            if (k != k0) load16(row, k, a.K, v);
+            const u32x4 q = k < a.K ? quantize16(k == k0 ? first : v, s) : u32x4{0, 0, 0, 0};
+            for (int j = 0; j < copies; ++j) {
+                int64_t to = r;
+                bool unused = false;
+                if (a.place) {
+                    const int p = a.place[r * a.k + j];
+                    unused = p <= -2;
+                    to = unused ? -2 - p : p;
+                    if (to < 0 || to >= a.out_rows) continue;
+                }
+                const u32x4 out = unused ? u32x4{0, 0, 0, 0} : q;
+                int8_t *d = a.Q + to * a.ldq + k;
+                if (k + 16 <= a.K) {
+                    __builtin_memcpy(d, &out, 16);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (k + i < a.K) d[i] = (int8_t)(out[i / 4] >> (8 * (i % 4)));
+                }
+                if (k0 == 0 && k == 0) a.scales[to] = unused ? 0.f : s.scale;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------- a few rows
+
+// Y[r][n] for a few rows: every weight is used once a row, so the time is that of reading the
+// weights.  A workgroup of eight waves quantises its rows into LDS once, then takes tiles of 16
+// columns; the waves split the contraction, slab by slab of 128 bytes, and their integer sums
+// meet in LDS.  Weights travel through a ring of LDS of each wave's own by direct loads,
+// which ask for whole 128-byte rows; fetched straight into the lanes that the matrix
+// instruction wants them in, neighbouring lanes would ask for different rows.  The ring runs on
+// from tile to tile, and is filled before the rows are quantised.
+struct VecArgs {
+    const void *X;
+    const int8_t *W;
+    const float *w_scales;
+    void *Y;
+    const int *offsets;  // or null: one group of all rows
+    int64_t ldx, ldw, stride_w, ldy;
+    int rows, N, K;
+    int pass;            // rows in LDS at once, at most 16
+    int slabs;           // of 128 bytes
+};
+typedef void (*VecFn)(VecArgs);
+
+constexpr int kVecWaves = 8;
+constexpr int kVecSlab = 16 * 128;
+constexpr int kVecTiles = 32;  // tiles whose column scales are fetched at once
+// Bytes of LDS: the rows, the rings, two tiles' sums, two sets of column scales, and the rows'
+// maxima and scales.
+inline int vec_lds(int pass, int slabs, int depth)
+{
+    return pass * slabs * 128 + kVecWaves * depth * kVecSlab + 2 * kVecWaves * 1024 +
+           2 * kVecTiles * 64 + 16 * kVecWaves * 4 + 64;
+}
+
+template <typename T, int DEPTH, bool FAST>
+__global__ void __launch_bounds__(kVecWaves * 64) q8_vec_kernel(VecArgs a)
+{
+    extern __shared__ __attribute__((aligned(1024))) char vec_shared[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    char *ring = vec_shared + wave * (DEPTH * kVecSlab);
+    int *sums = reinterpret_cast<int *>(vec_shared + kVecWaves * DEPTH * kVecSlab);
+    float *columns = reinterpret_cast<float *>(sums + 2 * kVecWaves * 256);
+    uint32_t *maxima = reinterpret_cast<uint32_t *>(columns + 2 * kVecTiles * 16);
+    float *scales = reinterpret_cast<float *>(maxima + 16 * kVecWaves);
+    char *rows_lds = reinterpret_cast<char *>(scales + 16);
+
+    const int group = blockIdx.y;
+    int begin = 0, end = a.rows;
+    if (a.offsets) group_rows(a.offsets, group, a.rows, begin, end);
+    begin = __builtin_amdgcn_readfirstlane(begin);
+    end = __builtin_amdgcn_readfirstlane(end);
+    const int tiles_n = (a.N + 15) / 16;
+    const int8_t *W = a.W + group * a.stride_w;
+    const float *ws = a.w_scales + (int64_t)group * a.N;
+    // This wave's slabs of a tile, and this workgroup's tiles.
+    const int ns = wave < a.slabs ? (a.slabs - wave + kVecWaves - 1) / kVecWaves : 0;
+    const int tiles = (int)blockIdx.x < tiles_n ? (tiles_n - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+
+    for (int first = begin; first < end; first += a.pass) {
+        const int R = end - first < a.pass ? end - first : a.pass;
+        // ---- the ring: the next slab to fetch, and where to
+        int f_tile = blockIdx.x, f_slab = 0, f_buf = 0;
+        const int frow = lane >> 3, fchunk = (lane & 7) ^ ((frow >> 1) & 7);
+        const int frow2 = frow + 8, fchunk2 = (lane & 7) ^ ((frow2 >> 1) & 7);
+        const uint32_t voff = (uint32_t)frow * (uint32_t)a.ldw + fchunk * 16u;
+        const uint32_t voff2 = (uint32_t)frow2 * (uint32_t)a.ldw + fchunk2 * 16u;
+        u32x4 hold[2];
+        auto fetch = [&]() {
+            const int k = (wave + kVecWaves * f_slab) * 128;
+            const bool more = f_slab < ns && f_tile < tiles_n;
+            const int64_t n0 = (int64_t)f_tile * 16;
+            const char *p = reinterpret_cast<const char *>(W) + n0 * a.ldw + k;
+            const int64_t left = more ? (a.N - 1 - n0) * a.ldw + a.K - k : 0;
+            if constexpr (FAST) {
+                u32x4 rs = descriptor(p, left);
+                uint32_t at = (uint32_t)(uintptr_t)(lds_char *)ring + f_buf * kVecSlab;
+                // Wait states between a vector unit's write of these and their use.
+                asm volatile("s_nop 4" : "+s"(rs), "+s"(at));
+                load_slab16(rs, voff, at);
+                load_slab16(rs, voff2, at + 1024);
+                f_buf = f_buf + 1 == DEPTH ? 0 : f_buf + 1;
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = h ? frow2 : frow, c = (h ? fchunk2 : fchunk) * 16;
+                    const char *q = p + row * a.ldw + c;
+                    const int room = more && n0 + row < a.N ? a.K - k - c : 0;
+                    hold[h] = u32x4{0, 0, 0, 0};
+                    if (room >= 16) {
+                        __builtin_memcpy(&hold[h], q, 16);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (i < room) hold[h][i / 4] |= (uint32_t)(uint8_t)q[i] << (8 * (i % 4));
+                    }
+                }
+            }
+            if (++f_slab >= ns) f_slab = 0, f_tile += gridDim.x;
+        };
+        if (ns > 0) {
+            if constexpr (FAST) {
+#pragma unroll
+                for (int d = 0; d < DEPTH; ++d) fetch();
+            } else {
+                fetch();
+            }
+        }
+        // ---- the rows, in the slabs' order: chunk c of row r of a slab at place c ^ (r / 2)
+        {
+            int per = 1;  // waves of a row
+            while (per < kVecWaves && per * 2 * R <= kVecWaves) per *= 2;
+            const int stride = kVecWaves / per, part = wave % per;
+            float v[16];
+            for (int r = wave / per; r < R; r += stride) {
+                const T *row = static_cast<const T *>(a.X) + (int64_t)(first + r) * a.ldx;
+                uint32_t m = 0;
+                for (int c = part * 64 + lane; c < a.slabs * 8; c += per * 64) {
+                    load16(row, c * 16, a.K, v);
+                    m = max16(v, m);
+                }
+                m = wave_max(m);
+                if (lane == 0) maxima[r * kVecWaves + part] = m;
+            }
+            __syncthreads();
+            for (int r = wave / per; r < R; r += stride) {
+                const T *row = static_cast<const T *>(a.X) + (int64_t)(first + r) * a.ldx;
+                uint32_t m = 0;
+                for (int p = 0; p < per; ++p) {
+                    const uint32_t u = maxima[r * kVecWaves + p];
+                    m = u > m ? u : m;
+                }
+                const Quantum s(m);
+                if (part == 0 && lane == 0) scales[r] = s.scale;
+                for (int c = part * 64 + lane; c < a.slabs * 8; c += per * 64) {
+                    load16(row, c * 16, a.K, v);
+                    const u32x4 q = quantize16(v, s);
+                    *reinterpret_cast<u32x4 *>(rows_lds + ((c >> 3) * R + r) * 128 +
+                                               (((c & 7) ^ ((r >> 1) & 7)) << 4)) = q;
+                }
+            }
+            __syncthreads();
+        }
+        // ---- tiles
+        const int l16 = lane & 15, g = lane >> 4;
+        const int xr = l16 < R ? l16 : R - 1;  // rows past the last repeat it, and are not stored
+        int buf = 0;
+        for (int i = 0; i < tiles; ++i) {
+            const int n0 = (blockIdx.x + i * gridDim.x) * 16;
+            if (i % kVecTiles == 0) {
+                // A thread for each column of the next tiles: a wait for them, which is one for
+                // the ring's loads too, is rare.  Read after the tile's barrier.
+                const int64_t n = (blockIdx.x + (int64_t)(i + (threadIdx.x >> 4)) * gridDim.x) * 16 +
+                                  (threadIdx.x & 15);
+                columns[(i / kVecTiles & 1) * (kVecTiles * 16) + threadIdx.x] = n < a.N ? ws[n] : 0.f;
+            }
+            i32x4 acc = {0, 0, 0, 0};
+            for (int t = 0; t < ns; ++t) {
+                if constexpr (FAST) {
+                    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(2 * (DEPTH - 1)) : "memory");
+                } else {
+                    *reinterpret_cast<u32x4 *>(ring + lane * 16) = hold[0];
+                    *reinterpret_cast<u32x4 *>(ring + 1024 + lane * 16) = hold[1];
+                    fetch();
+                    __builtin_amdgcn_wave_barrier();
+                }
+                const char *slab = ring + buf * kVecSlab;
+                const char *x = rows_lds + ((wave + kVecWaves * t) * R + xr) * 128;
+                i32x4 wf[2], xf[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    wf[k] = *reinterpret_cast<const i32x4 *>(
+                        slab + l16 * 128 + (((4 * k + g) ^ ((l16 >> 1) & 7)) << 4));
+                    xf[k] = *reinterpret_cast<const i32x4 *>(x + (((4 * k + g) ^ ((xr >> 1) & 7)) << 4));
+                }
+                if constexpr (FAST) {
+                    // Read before the buffer is filled again.
+                    asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(wf[0]), "+v"(wf[1]) : : "memory");
+                    fetch();
+                    buf = buf + 1 == DEPTH ? 0 : buf + 1;
+                } else {
+                    __builtin_amdgcn_wave_barrier();
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[k], xf[k], acc, 0, 0, 0);
+            }
+            // Two sets of sums in turn, so that one barrier a tile is enough.
+            int *tile = sums + (i & 1) * (kVecWaves * 256);
+            *reinterpret_cast<i32x4 *>(tile + wave * 256 + l16 * 16 + 4 * g) = acc;
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            const int row = threadIdx.x >> 4, n = n0 + (threadIdx.x & 15);
+            if (row < R && n < a.N) {
+                const float w = columns[i % (2 * kVecTiles) * 16 + (threadIdx.x & 15)];
+                int sum = 0;
+#pragma unroll
+                for (int v = 0; v < kVecWaves; ++v) sum += tile[v * 256 + threadIdx.x];
+                static_cast<T *>(a.Y)[(int64_t)(first + row) * a.ldy + n] =
+                    (T)((float)sum * scales[row] * w);
+            }
+        }
+        if constexpr (FAST) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();  // the rows and the rings may be written again
+    }
+}
+
+}  // namespace lm
+}  // namespace sgemm

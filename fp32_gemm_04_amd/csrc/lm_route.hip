@@ -1,0 +1,194 @@
+// libsgemm rows sorted by expert: argument checks, launch shapes and launches, behind the C
+// ABI declared in include/slm.h.  Nothing here allocates, frees, copies or synchronises.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/slm.h"
+#include "lm_host.hpp"
+#include "lm_route.hpp"
+
+namespace sgemm {
+namespace lm {
+namespace {
+
+constexpr int kMostGroups = 4096;
+constexpr int kMostSegments = 256;
+
+// How a sort is cut: the slots of one chunk are counted and placed by one workgroup; more go
+// in two launches over segments.
+struct SortPlan {
+    int waves, segment, segments;
+    int64_t bytes;
+};
+
+SortPlan sort_plan(int slots, int groups)
+{
+    SortPlan p;
+    // 16 waves' counters fit 32 KB up to 1024 experts.
+    p.waves = groups <= 1024 ? 16 : 4;
+    const int chunk = sort_chunk(p.waves);
+    const int64_t chunks = slots > 0 ? ceil_div(slots, chunk) : 1;
+    p.segments = (int)(chunks < kMostSegments ? chunks : kMostSegments);
+    // Whole chunks each; the last segments may be empty.
+    p.segment = (int)(ceil_div(chunks, p.segments) * chunk);
+    p.bytes = p.segments > 1 ? (int64_t)p.segments * (groups + 1) * 4 : 0;
+    return p;
+}
+
+// The shape of a launch over tokens' rows: threads along a row, and workgroups.
+int cols_log2(int pieces)
+{
+    int n = 0;
+    while (n < 8 && (1 << n) < pieces) ++n;
+    return n;
+}
+
+dim3 copy_grid(int tokens, int pieces, int log2)
+{
+    const int64_t work = ceil_div(tokens, 256 >> log2) * ceil_div(pieces, 1 << log2);
+    return dim3((unsigned)(work < kMostBlocks ? work : kMostBlocks));
+}
+
+// The checks that the copies share, of sizes; `type` is parameter 1, tokens 2, k 3, H 4.
+int check_sizes(int type, int tokens, int k, int H)
+{
+    if (type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16) return -1;
+    if (tokens < 0 || tokens > kMostExtent) return -2;
+    if (k < 0 || (tokens > 0 && k > kMostExtent / tokens)) return -3;
+    if (H < 0 || H > kMostExtent) return -4;
+    return 0;
+}
+
+}  // namespace
+}  // namespace lm
+}  // namespace sgemm
+
+using namespace sgemm::lm;
+
+extern "C" int64_t sgemm_expert_sort_workspace(int slots, int groups)
+{
+    if (slots < 0 || slots > kMostExtent) return -1;
+    if (groups < 0 || groups > kMostGroups) return -2;
+    return sort_plan(slots, groups).bytes;
+}
+
+extern "C" int sgemm_expert_sort(int slots, int groups, const int64_t *experts, int *offsets,
+                                 int *order, int *place, void *ws, int64_t ws_bytes,
+                                 hipStream_t stream)
+{
+    if (slots < 0 || slots > kMostExtent) return -1;
+    if (groups < 0 || groups > kMostGroups) return -2;
+    if ((slots > 0 && !experts) || !aligned(experts, 8)) return -3;
+    if (!offsets || !aligned(offsets, 4)) return -4;
+    if (!aligned(order, 4)) return -5;
+    if ((slots > 0 && !place) || !aligned(place, 4)) return -6;
+    const SortPlan p = sort_plan(slots, groups);
+    if ((p.bytes > 0 && !ws) || !aligned(ws, 4)) return -7;
+    if (ws_bytes < p.bytes) return -8;
+    SortArgs a = {};
+    a.experts = experts, a.offsets = offsets, a.order = order, a.place = place;
+    a.counts = p.segments > 1 ? static_cast<int *>(ws) : nullptr;
+    a.slots = slots, a.groups = groups;
+    a.segment = p.segment, a.segments = p.segments;
+    const int n = groups + 1;
+    if (a.counts) {
+        sort_count_kernel<<<dim3(p.segments), dim3(p.waves * 64), n * 4, stream>>>(a);
+        if (int rc = (int)hipGetLastError()) return rc;
+    }
+    const int lds = n * 4 + (p.waves * n * 2 > n * 4 ? p.waves * n * 2 : n * 4);
+    sort_place_kernel<<<dim3(p.segments), dim3(p.waves * 64), lds, stream>>>(a);
+    return (int)hipGetLastError();
+}
+
+extern "C" int sgemm_expert_gather(int type, int tokens, int k, int H, const void *X, int ldx,
+                                   const int *place, const float *weights, int rows, void *R,
+                                   int ldr, int fill, hipStream_t stream)
+{
+    if (int rc = check_sizes(type, tokens, k, H)) return rc;
+    const int size = type == SGEMM_TYPE_BF16 ? 2 : 4, least = H > 1 ? H : 1;
+    const bool work = tokens > 0 && k > 0 && H > 0 && rows > 0;
+    if ((work && !X) || !aligned(X, size)) return -5;
+    if (ldx < least) return -6;
+    if ((work && !place) || !aligned(place, 4)) return -7;
+    if (!aligned(weights, 4)) return -8;
+    if (rows < 0 || rows > kMostExtent) return -9;
+    if ((work && !R) || !aligned(R, size)) return -10;
+    if (ldr < least) return -11;
+    if (fill != 0 && fill != 1) return -12;
+    if (!work) return 0;
+    RouteArgs a = {};
+    a.X = X, a.out = R, a.place = place, a.weights = weights;
+    a.ldx = ldx, a.ldo = ldr;
+    a.tokens = tokens, a.k = k, a.H = H, a.rows = rows, a.fill = fill;
+    const int pieces = (int)ceil_div(H, 16 / size);
+    a.cols_log2 = cols_log2(pieces);
+    auto fn = type == SGEMM_TYPE_BF16
+                  ? (weights ? gather_kernel<bf16, true> : gather_kernel<bf16, false>)
+                  : (weights ? gather_kernel<float, true> : gather_kernel<float, false>);
+    fn<<<copy_grid(tokens, pieces, a.cols_log2), dim3(256), 0, stream>>>(a);
+    return (int)hipGetLastError();
+}
+
+extern "C" int sgemm_expert_combine(int type, int tokens, int k, int H, int rows, const void *R,
+                                    int ldr, const int *place, const float *weights, float beta,
+                                    void *out, int ldo, hipStream_t stream)
+{
+    if (int rc = check_sizes(type, tokens, k, H)) return rc;
+    if (rows < 0 || rows > kMostExtent) return -5;
+    const int size = type == SGEMM_TYPE_BF16 ? 2 : 4, least = H > 1 ? H : 1;
+    const bool work = tokens > 0 && H > 0, reads = work && k > 0 && rows > 0;
+    if ((reads && !R) || !aligned(R, size)) return -6;
+    if (ldr < least) return -7;
+    if ((reads && !place) || !aligned(place, 4)) return -8;
+    if (!aligned(weights, 4)) return -9;
+    if ((work && !out) || !aligned(out, size)) return -11;
+    if (ldo < least) return -12;
+    if (!work) return 0;
+    RouteArgs a = {};
+    a.R = R, a.out = out, a.place = place, a.weights = weights;
+    a.ldr = ldr, a.ldo = ldo, a.beta = beta;
+    a.tokens = tokens, a.k = reads ? k : 0, a.H = H, a.rows = rows;
+    const int pieces = (int)ceil_div(H, 16 / size);
+    a.cols_log2 = cols_log2(pieces);
+    auto fn = type == SGEMM_TYPE_BF16 ? combine_kernel<bf16> : combine_kernel<float>;
+    fn<<<copy_grid(tokens, pieces, a.cols_log2), dim3(256), 0, stream>>>(a);
+    return (int)hipGetLastError();
+}
+
+extern "C" int sgemm_expert_combine_backward(int type, int tokens, int k, int H, int rows,
+                                             const void *dout, int lddo, const void *R, int ldr,
+                                             const int *place, const float *weights, void *dR,
+                                             int lddr, int fill, float *dweights, hipStream_t stream)
+{
+    if (int rc = check_sizes(type, tokens, k, H)) return rc;
+    if (rows < 0 || rows > kMostExtent) return -5;
+    const int size = type == SGEMM_TYPE_BF16 ? 2 : 4, least = H > 1 ? H : 1;
+    const bool slots = tokens > 0 && k > 0;
+    const bool work = slots && H > 0 && rows > 0 && (dR || dweights);
+    if ((work && !dout) || !aligned(dout, size)) return -6;
+    if (lddo < least) return -7;
+    if ((work && dweights && !R) || !aligned(R, size)) return -8;
+    if (ldr < least) return -9;
+    if ((work && !place) || !aligned(place, 4)) return -10;
+    if (!aligned(weights, 4)) return -11;
+    if (!aligned(dR, size)) return -12;
+    if (lddr < least) return -13;
+    if (fill != 0 && fill != 1) return -14;
+    if (!aligned(dweights, 4)) return -15;
+    // Without columns or rows the dot products are empty: zeros are still written.
+    if (!slots || (!dR && !dweights) || (!work && !dweights)) return 0;
+    RouteArgs a = {};
+    a.X = dout, a.R = R, a.out = work ? dR : nullptr, a.place = place, a.weights = weights;
+    a.dweights = dweights;
+    a.ldx = lddo, a.ldr = ldr, a.ldo = lddr;
+    a.tokens = tokens, a.k = k, a.H = H, a.rows = work ? rows : 0, a.fill = fill;
+    // Four waves a token where tokens alone would not fill the chip.
+    const bool few = tokens < 4096;
+    auto fn = type == SGEMM_TYPE_BF16
+                  ? (few ? combine_backward_kernel<bf16, 4> : combine_backward_kernel<bf16, 1>)
+                  : (few ? combine_backward_kernel<float, 4> : combine_backward_kernel<float, 1>);
+    const int64_t blocks = few ? tokens : ceil_div(tokens, 4);
+    fn<<<dim3((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks)), dim3(256), 0, stream>>>(a);
+    return (int)hipGetLastError();
+}

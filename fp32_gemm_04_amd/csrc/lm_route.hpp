@@ -1,0 +1,391 @@
+// Tokens on their way to experts and back (include/slm.h): a stable counting sort of the
+// experts' numbers, and copies between tokens' rows and experts' rows.
+//
+// Everything is addressed from the token's side by place, the row of each of its k choices:
+// the way in reads a token once and writes k rows, the way back reads k rows and writes a
+// token once, so neither direction needs atomics, and sums have one order.
+#pragma once
+
+#include <type_traits>
+
+#include "lm_tile.hpp"
+
+namespace sgemm {
+namespace lm {
+
+// ------------------------------------------------------------------- sorting
+
+struct SortArgs {
+    const int64_t *experts;
+    int *offsets, *order, *place;
+    int *counts;    // of each segment and expert, or null: counted by every workgroup itself
+    int slots, groups;
+    int segment;    // slots of a workgroup, a multiple of a chunk
+    int segments;
+};
+
+constexpr int kSortItems = 4;  // slots of a lane, in registers, per chunk
+inline __host__ __device__ int sort_chunk(int waves) { return waves * 64 * kSortItems; }
+
+// The place of an expert's number among the counters: those outside come last.
+__device__ __forceinline__ int sort_key(const int64_t *experts, int slot, int groups)
+{
+    const int64_t e = experts[slot];
+    return e >= 0 && e < groups ? (int)e : groups;
+}
+
+// Counts of each segment's slots by expert, for the sort of many slots.
+__global__ void __launch_bounds__(1024) sort_count_kernel(SortArgs a)
+{
+    extern __shared__ int hist[];
+    const int n = a.groups + 1;
+    for (int e = threadIdx.x; e < n; e += blockDim.x) hist[e] = 0;
+    __syncthreads();
+    const int64_t s0 = (int64_t)blockIdx.x * a.segment;
+    const int64_t s1 = s0 + a.segment < a.slots ? s0 + a.segment : a.slots;
+#pragma unroll 4
+    for (int64_t s = s0 + threadIdx.x; s < s1; s += blockDim.x)
+        atomicAdd(&hist[sort_key(a.experts, (int)s, a.groups)], 1);
+    __syncthreads();
+    for (int e = threadIdx.x; e < n; e += blockDim.x)
+        a.counts[(int64_t)blockIdx.x * n + e] = hist[e];
+}
+
+// One segment's slots to their rows.  A slot's row is the number of slots with a lower
+// expert, of earlier segments' with its own, and of earlier ones in its segment.  The last is
+// found 64 slots at a time: the lanes with one expert are the and, over the bits of its
+// number, of the ballots of that bit (or their complements); the first of them advances
+// the wave's counter of the expert.  Integer counts: any order of the atomics gives the same.
+__global__ void __launch_bounds__(1024) sort_place_kernel(SortArgs a)
+{
+    extern __shared__ int shared[];
+    __shared__ int wave_sum[16];
+    const int n = a.groups + 1, waves = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int *base = shared;                                        // n: next row of each expert
+    int *total = shared + n;                                   // n, until the counters take its place
+    uint16_t *cnt = reinterpret_cast<uint16_t *>(shared + n);  // waves x n
+    for (int e = threadIdx.x; e < 2 * n; e += blockDim.x) shared[e] = 0;
+    __syncthreads();
+    const int64_t s0 = (int64_t)blockIdx.x * a.segment;
+    const int64_t s1 = s0 + a.segment < a.slots ? s0 + a.segment : a.slots;
+    if (a.counts) {
+        const int all = a.segments * n;
+        for (int i = threadIdx.x; i < all; i += blockDim.x) {
+            const int c = a.counts[i], segment = i / n, e = i - segment * n;
+            if (c == 0) continue;
+            atomicAdd(&total[e], c);
+            if (segment < (int)blockIdx.x) atomicAdd(&base[e], c);
+        }
+    } else {
+#pragma unroll 4
+        for (int s = threadIdx.x; s < a.slots; s += blockDim.x) {
+            const int e = sort_key(a.experts, s, a.groups);
+            atomicAdd(&total[e], 1);
+            if (s < s0) atomicAdd(&base[e], 1);
+        }
+    }
+    __syncthreads();
+    // Rows before each expert: every thread sums `per` neighbouring experts.
+    const int per = (n + blockDim.x - 1) / blockDim.x, e0 = threadIdx.x * per;
+    int mine = 0;
+    for (int e = e0; e < e0 + per && e < n; ++e) mine += total[e];
+    int before = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int v = __shfl_up(before, d);
+        if (lane >= d) before += v;
+    }
+    if (lane == 63) wave_sum[wave] = before;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) before += wave_sum[w];
+    before -= mine;
+    for (int e = e0; e < e0 + per && e < n; ++e) {
+        if (blockIdx.x == 0) a.offsets[e] = before;
+        base[e] += before;
+        before += total[e];
+    }
+    const int bits = 32 - __builtin_clz(n);  // n itself marks lanes without a slot
+    for (int64_t c0 = s0; c0 < s1; c0 += sort_chunk(waves)) {
+        __syncthreads();  // base is complete, total and the last chunk's counters are read
+        for (int e = threadIdx.x; e < waves * n; e += blockDim.x) cnt[e] = 0;
+        __syncthreads();
+        uint16_t *own = cnt + wave * n;
+        int key[kSortItems], rank[kSortItems];
+        const int64_t w0 = c0 + wave * (64 * kSortItems) + lane;
+#pragma unroll
+        for (int i = 0; i < kSortItems; ++i)
+            key[i] = w0 + i * 64 < s1 ? sort_key(a.experts, (int)(w0 + i * 64), a.groups) : n;
+#pragma unroll
+        for (int i = 0; i < kSortItems; ++i) {
+            uint64_t same = ~0ull;
+            for (int b = 0; b < bits; ++b) {
+                const uint64_t set = __ballot(key[i] >> b & 1);
+                same &= key[i] >> b & 1 ? set : ~set;
+            }
+            const int lower = __popcll(same & ((1ull << lane) - 1));
+            rank[i] = 0;
+            if (key[i] < n) {
+                rank[i] = *(volatile uint16_t *)(own + key[i]) + lower;
+            }
+            __builtin_amdgcn_wave_barrier();  // a wave's reads and writes of LDS stay in order
+            if (key[i] < n && lower == 0)
+                *(volatile uint16_t *)(own + key[i]) = (uint16_t)(rank[i] + __popcll(same));
+            __builtin_amdgcn_wave_barrier();
+        }
+        __syncthreads();
+        // Counters to rows before each wave's, relative to the expert's next row.
+        for (int e = threadIdx.x; e < n; e += blockDim.x) {
+            int sum = 0;
+            for (int w = 0; w < waves; ++w) {
+                const int v = cnt[w * n + e];
+                cnt[w * n + e] = (uint16_t)sum;
+                sum += v;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSortItems; ++i) {
+            if (key[i] >= n) continue;
+            const int slot = (int)(w0 + i * 64);
+            const int row = base[key[i]] + own[key[i]] + rank[i];
+            a.place[slot] = key[i] < a.groups ? row : -2 - row;
+            if (a.order) a.order[row] = slot;
+        }
+        if (c0 + sort_chunk(waves) >= s1) break;
+        // The next chunk's rows follow: each expert's last wave knows how many there were.
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSortItems; ++i)
+            if (key[i] < n) atomicAdd(&base[key[i]], 1);
+    }
+}
+
+// ------------------------------------------------------------------- copies
+
+struct RouteArgs {
+    const void *X;         // tokens' rows (gather: X; backward: dout)
+    const void *R;         // experts' rows that are read
+    void *out;             // gather, backward: experts' rows; combine: tokens' rows
+    const int *place;
+    const float *weights;  // or null: 1
+    float *dweights;       // or null
+    int64_t ldx, ldr, ldo;
+    int tokens, k, H, rows;
+    int fill;
+    float beta;
+    int cols_log2;         // threads of a workgroup along a row (of 256)
+};
+
+// Sixteen bytes of a row; addresses need the element's alignment only.
+template <typename T> struct Piece {
+    static constexpr int E = 16 / sizeof(T);
+    T v[E];
+    __device__ __forceinline__ void load(const T *p, int left)
+    {
+        if (left >= E) {
+            __builtin_memcpy(v, p, 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) v[i] = i < left ? p[i] : (T)0.f;
+        }
+    }
+    __device__ __forceinline__ void store(T *p, int left) const
+    {
+        if (left >= E) {
+            __builtin_memcpy(p, v, 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (i < left) p[i] = v[i];
+        }
+    }
+};
+
+// The row that a place names: -1 for none; `unused` where the row is a dropped slot's.
+__device__ __forceinline__ int row_of(int place, int rows, bool &unused)
+{
+    unused = place <= -2;
+    const int r = unused ? -2 - place : place;
+    return r >= 0 && r < rows ? r : -1;
+}
+
+// R[place] <- w X[t], a thread per 16 bytes of a token.
+template <typename T, bool WEIGHTED>
+__global__ void __launch_bounds__(256) gather_kernel(RouteArgs a)
+{
+    constexpr int E = Piece<T>::E;
+    const int cols = 1 << a.cols_log2, per = 256 >> a.cols_log2;
+    const int col = threadIdx.x & (cols - 1), sub = threadIdx.x >> a.cols_log2;
+    const int pieces = (a.H + E - 1) / E, parts = (pieces + cols - 1) / cols;
+    const int64_t work = (int64_t)((a.tokens + per - 1) / per) * parts;
+    for (int64_t b = blockIdx.x; b < work; b += gridDim.x) {
+        const int64_t t = b / parts * per + sub;
+        const int h = ((int)(b % parts) * cols + col) * E;
+        if (t >= a.tokens || h >= a.H) continue;
+        const int left = a.H - h;
+        Piece<T> x;
+        x.load(static_cast<const T *>(a.X) + t * a.ldx + h, left);
+        const int *place = a.place + t * a.k;
+        T *out = static_cast<T *>(a.out) + h;
+        for (int j0 = 0; j0 < a.k; j0 += 4) {
+            int r[4];
+            float w[4];
+            bool unused[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                r[j] = row_of(j0 + j < a.k ? place[j0 + j] : -1, a.rows, unused[j]);
+                if (unused[j] && !a.fill) r[j] = -1;
+                if constexpr (WEIGHTED)
+                    w[j] = r[j] >= 0 && !unused[j] ? a.weights[t * a.k + j0 + j] : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (r[j] < 0) continue;
+                Piece<T> y = x;
+                if constexpr (WEIGHTED) {
+#pragma unroll
+                    for (int i = 0; i < E; ++i) y.v[i] = (T)(w[j] * (float)x.v[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < E; ++i) y.v[i] = unused[j] ? (T)0.f : y.v[i];
+                y.store(out + r[j] * a.ldo, left);
+            }
+        }
+    }
+}
+
+// out[t] <- beta out[t] + sum_j w R[place], a thread per 16 bytes of a token.
+template <typename T>
+__global__ void __launch_bounds__(256) combine_kernel(RouteArgs a)
+{
+    constexpr int E = Piece<T>::E;
+    const int cols = 1 << a.cols_log2, per = 256 >> a.cols_log2;
+    const int col = threadIdx.x & (cols - 1), sub = threadIdx.x >> a.cols_log2;
+    const int pieces = (a.H + E - 1) / E, parts = (pieces + cols - 1) / cols;
+    const int64_t work = (int64_t)((a.tokens + per - 1) / per) * parts;
+    for (int64_t b = blockIdx.x; b < work; b += gridDim.x) {
+        const int64_t t = b / parts * per + sub;
+        const int h = ((int)(b % parts) * cols + col) * E;
+        if (t >= a.tokens || h >= a.H) continue;
+        const int left = a.H - h;
+        const T *R = static_cast<const T *>(a.R) + h;
+        const int *place = a.place + t * a.k;
+        float sum[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) sum[i] = 0.f;
+        for (int j0 = 0; j0 < a.k; j0 += 4) {
+            Piece<T> x[4];
+            float w[4];
+            int r[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                r[j] = j0 + j < a.k ? place[j0 + j] : -1;
+                if (r[j] >= a.rows) r[j] = -1;
+                w[j] = 1.f;
+                if (r[j] < 0) continue;
+                if (a.weights) w[j] = a.weights[t * a.k + j0 + j];
+                x[j].load(R + r[j] * a.ldr, left);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (r[j] >= 0)
+#pragma unroll
+                    for (int i = 0; i < E; ++i) sum[i] = fmaf(w[j], (float)x[j].v[i], sum[i]);
+        }
+        T *out = static_cast<T *>(a.out) + t * a.ldo + h;
+        Piece<T> y;
+        if (a.beta != 0.f) {
+            y.load(out, left);
+#pragma unroll
+            for (int i = 0; i < E; ++i) sum[i] = fmaf(a.beta, (float)y.v[i], sum[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) y.v[i] = (T)sum[i];
+        y.store(out, left);
+    }
+}
+
+// dR[place] <- w dout[t] and dw = <dout[t], R[place]>: WAVES waves share a token, eight of its
+// rows at a time.
+template <typename T, int WAVES>
+__global__ void __launch_bounds__(256) combine_backward_kernel(RouteArgs a)
+{
+    constexpr int E = Piece<T>::E, KT = 8, TOKENS = 4 / WAVES;
+    __shared__ float parts[4][KT];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int64_t t0 = (int64_t)blockIdx.x * TOKENS; t0 < a.tokens; t0 += (int64_t)gridDim.x * TOKENS) {
+        const int64_t t = t0 + wave / WAVES;
+        const bool here = t < a.tokens;
+        for (int j0 = 0; j0 < a.k; j0 += KT) {
+            float dot[KT], w[KT];
+            int r[KT];
+            bool unused[KT];
+#pragma unroll
+            for (int j = 0; j < KT; ++j) {
+                dot[j] = 0.f, r[j] = -1, w[j] = 1.f, unused[j] = false;
+                if (here && a.rows > 0 && j0 + j < a.k) {
+                    r[j] = row_of(a.place[t * a.k + j0 + j], a.rows, unused[j]);
+                    if (r[j] >= 0 && !unused[j] && a.weights) w[j] = a.weights[t * a.k + j0 + j];
+                }
+            }
+            const int step = WAVES * 64 * E;
+            for (int h = ((wave % WAVES) * 64 + lane) * E; here && a.rows > 0 && h < a.H;
+                 h += step) {
+                const int left = a.H - h;
+                Piece<T> d, x[KT];
+                d.load(static_cast<const T *>(a.X) + t * a.ldx + h, left);
+                if (a.dweights) {
+#pragma unroll
+                    for (int j = 0; j < KT; ++j)
+                        if (r[j] >= 0 && !unused[j])
+                            x[j].load(static_cast<const T *>(a.R) + r[j] * a.ldr + h, left);
+#pragma unroll
+                    for (int j = 0; j < KT; ++j)
+                        if (r[j] >= 0 && !unused[j])
+#pragma unroll
+                            for (int i = 0; i < E; ++i)
+                                dot[j] = fmaf((float)d.v[i], (float)x[j].v[i], dot[j]);
+                }
+                if (a.out) {
+                    T *out = static_cast<T *>(a.out) + h;
+#pragma unroll
+                    for (int j = 0; j < KT; ++j) {
+                        if (r[j] < 0 || (unused[j] && !a.fill)) continue;
+                        Piece<T> y;
+#pragma unroll
+                        for (int i = 0; i < E; ++i)
+                            y.v[i] = unused[j] ? (T)0.f : (T)(w[j] * (float)d.v[i]);
+                        y.store(out + r[j] * a.ldo, left);
+                    }
+                }
+            }
+            if (!a.dweights) continue;
+#pragma unroll
+            for (int j = 0; j < KT; ++j)
+#pragma unroll
+                for (int d = 1; d < 64; d *= 2) dot[j] += __shfl_xor(dot[j], d);
+            if constexpr (WAVES > 1) {
+                if (lane == 0)
+#pragma unroll
+                    for (int j = 0; j < KT; ++j) parts[wave][j] = dot[j];
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < KT; ++j) {
+                    dot[j] = 0.f;
+#pragma unroll
+                    for (int w = 0; w < WAVES; ++w)
+                        dot[j] += parts[wave / WAVES * WAVES + w][j];
+                }
+                __syncthreads();
+            }
+            if (here && wave % WAVES == 0 && lane == 0)
+#pragma unroll
+                for (int j = 0; j < KT; ++j)
+                    if (j0 + j < a.k) a.dweights[t * a.k + j0 + j] = dot[j];
+        }
+    }
+}
+
+}  // namespace lm
+}  // namespace sgemm

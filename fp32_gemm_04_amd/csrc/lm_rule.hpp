@@ -43,8 +43,16 @@ constexpr TileCost kBf16Tiles[NUM_TILES] = {
 constexpr TileCost kF32Tiles[NUM_TILES] = {
     {16, 64, 0.5, 64}, {32, 64, 0.75, 64}, {48, 128, 0.9, 64}, {64, 64, 0.87, 64}, {128, 128, 1.0, 64}, {0, 0, 0, 0}, {0, 0, 0, 0}};
 
+// 8-bit integers: the contraction counts in pairs of bytes, so that a slab is 64 as with bf16.
+constexpr TileCost kI8Tiles[NUM_TILES] = {
+    {16, 64, 0.2, 64}, {32, 128, 0.45, 64}, {0, 0, 0, 0}, {64, 128, 0.65, 64}, {128, 128, 0.8, 64}, {128, 192, 0.88, 64},
+    {256, 256, 1.0, 256}};
+
 // By the size of an element.
-inline const TileCost *tile_costs(int size) { return size == 2 ? kBf16Tiles : kF32Tiles; }
+inline const TileCost *tile_costs(int size)
+{
+    return size == 1 ? kI8Tiles : size == 2 ? kBf16Tiles : kF32Tiles;
+}
 
 // The tile that finishes first when every compute unit takes the same number of tiles
 // (a last one that has the unit to itself counts half where two fit beside each other):

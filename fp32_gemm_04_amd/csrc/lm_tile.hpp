@@ -1,10 +1,10 @@
 // Tile kernels of the language-model products (include/slm.h): fp32 or bf16
-// operands, fp32 accumulation, three operand layouts, ragged rows or a ragged
-// contraction, and the epilogues the products need.
+// operands with fp32 accumulation, or 8-bit integers with 32-bit sums; three operand
+// layouts, ragged rows or a ragged contraction, and the epilogues the products need.
 //
 // One workgroup computes a BM x BN tile of C = A B^T, where A has BM rows and
 // B has BN rows (the columns of C), both walked along the contraction in
-// slabs of 128 bytes (BK = 64 bf16 or 32 fp32).  An operand comes in one of
+// slabs of 128 bytes (BK = 128 integers, 64 bf16 or 32 fp32).  An operand comes in one of
 // two layouts in memory:
 //   KC  the contraction index is contiguous: a slab row is 128 bytes of it;
 //   MC  the row index is contiguous: the slab is BK rows of BM (or BN) values.
@@ -39,7 +39,9 @@
 // four fp32 16x16x4 steps s = 0..3 take k = 4 g + s; with BL = 32 and g = lane / 32, two
 // bf16 32x32x16 cover the same half slab.  The larger block
 // halves the instructions a wave issues, which the largest tile needs: its
-// accumulators leave one wave per SIMD.  B is the instruction's first operand, so
+// accumulators leave one wave per SIMD.  8-bit integers take 16 bytes of k where bf16 takes
+// eight values, so their slabs, addresses and reads of LDS are those of bf16 KC operands.
+// B is the instruction's first operand, so
 // a lane holds groups of four consecutive columns of one row of C:
 //   row lane % BL, columns 4 g .. 4 g + 3 (BL = 32: and 8, 16, 24 further on).
 #pragma once
@@ -56,6 +58,8 @@ typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
@@ -65,8 +69,9 @@ enum Layout { KC, MC };
 enum Ragged { PLAIN, ROWS, SUM };
 // STORE: C <- alpha acc + beta C.  STATS: row maxima and sums of exponentials of
 // the tile, and the value at the row's target.  GRAD: the loss's derivative by
-// each value.  PART: fp32 C <- acc (+ C), for sums joined later.
-enum Epilogue { STORE, STATS, GRAD, PART };
+// each value.  PART: fp32 C <- acc (+ C), for sums joined later.  SCALE: C <- acc times
+// its row's and its column's scale.
+enum Epilogue { STORE, STATS, GRAD, PART, SCALE };
 
 struct TileArgs {
     const void *A, *B;
@@ -97,6 +102,8 @@ struct TileArgs {
     // below a slab's rows or a multiple of them (0: never).
     int store_rows, low_rows;
     int wrap;
+    // SCALE: of each row of A, and of each row of B (N of one group after another's).
+    const float *scale_a, *scale_b;
 };
 
 typedef void (*TileFn)(TileArgs);
@@ -109,6 +116,10 @@ template <> struct Elem<bf16> {
 template <> struct Elem<float> {
     static constexpr int BK = 32, EPC = 4;
     typedef f32x4 Frag;
+};
+template <> struct Elem<int8_t> {
+    static constexpr int BK = 128, EPC = 16;
+    typedef i32x4 Frag;
 };
 
 // Lane l's 16 bytes at base + voff go to LDS [lds + 16 l, + 16); zeros where
@@ -246,13 +257,15 @@ struct Slab {
 };
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-template <int BL> struct AccOf { typedef f32x4 Type; };
-template <> struct AccOf<32> { typedef f32x16 Type; };
+template <typename T, int BL> struct AccOf { typedef f32x4 Type; };
+template <typename T> struct AccOf<T, 32> { typedef f32x16 Type; };
+template <> struct AccOf<int8_t, 16> { typedef i32x4 Type; };
+template <> struct AccOf<int8_t, 32> { typedef i32x16 Type; };
 
 template <typename T, int BL>
-__device__ __forceinline__ typename AccOf<BL>::Type mfma_step(const typename Elem<T>::Frag &b,
-                                                              const typename Elem<T>::Frag &a,
-                                                              typename AccOf<BL>::Type c)
+__device__ __forceinline__ typename AccOf<T, BL>::Type mfma_step(const typename Elem<T>::Frag &b,
+                                                                 const typename Elem<T>::Frag &a,
+                                                                 typename AccOf<T, BL>::Type c)
 {
     if constexpr (std::is_same<T, float>::value) {
         static_assert(BL == 16, "fp32 tiles have blocks of 16");
@@ -260,6 +273,11 @@ __device__ __forceinline__ typename AccOf<BL>::Type mfma_step(const typename Ele
         for (int s = 0; s < 4; ++s)
             c = __builtin_amdgcn_mfma_f32_16x16x4f32(b[s], a[s], c, 0, 0, 0);
         return c;
+    } else if constexpr (std::is_same<T, int8_t>::value) {
+        if constexpr (BL == 16)
+            return __builtin_amdgcn_mfma_i32_16x16x64_i8(b, a, c, 0, 0, 0);
+        else
+            return __builtin_amdgcn_mfma_i32_32x32x32_i8(b, a, c, 0, 0, 0);
     } else if constexpr (BL == 16) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
     } else {
@@ -309,7 +327,7 @@ __device__ __forceinline__ int64_t scan_tiles(const int *offsets, int groups, in
 // spilled).  Two forms of the 256 tile spill outside their loops: row statistics 32
 // registers (written with them: 302 MB instead of 34 at T 8192, V 131072), partial sums 8.
 template <typename T, int BM, int BN, int WM, int WN, int NBUF, int BL, int WPE, Layout LA,
-          Layout LB, Ragged RG, Epilogue EP, bool FAST>
+          Layout LB, Ragged RG, Epilogue EP, bool FAST, typename TC = T>
 __global__ void __launch_bounds__(WM *WN * 64) __attribute__((amdgpu_waves_per_eu(WPE)))
 tile_kernel(TileArgs g)
 {
@@ -422,13 +440,13 @@ tile_kernel(TileArgs g)
     const int64_t step_b = LB == KC ? 128 : (int64_t)BK * g.ldb * SZ;
     const int slabs = (K + BK - 1) / BK;
 
-    typename AccOf<BL>::Type acc[FM][FN];
+    typename AccOf<T, BL>::Type acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-            for (int q = 0; q < BL * BL / 64; ++q) acc[i][j][q] = 0.f;
+            for (int q = 0; q < BL * BL / 64; ++q) acc[i][j][q] = 0;
 
     const int wr = wave / WN, wc = wave % WN;
     // Operand read r of half slab h: step by step, the wave's B blocks, then its A blocks.
@@ -652,12 +670,12 @@ tile_kernel(TileArgs g)
     // Group u of the wave's FN * GR: its first column, and its values in row block i.
     auto column = [&](int u) { return nw + BL * (u / GR) + 8 * (u % GR); };
     auto value = [&](int i, int u, int q) { return acc[i][u / GR][4 * (u % GR) + q]; };
-    typedef T Vec __attribute__((ext_vector_type(4)));
+    typedef TC Vec __attribute__((ext_vector_type(4)));
     // bf16 blocks of 32: two neighbouring groups of a row lie in a lane pair (l, l + 32) as
     // columns 0-3, 8-11 and 4-7, 12-15; exchanged, each lane stores eight in a row, half as
     // many and twice as wide stores.
-    constexpr bool PAIRED = BL == 32 && SZ == 2;
-    auto store_pair = [&](T *crow, int u, auto first, auto second) {
+    constexpr bool PAIRED = BL == 32 && sizeof(TC) == 2;
+    auto store_pair = [&](TC *crow, int u, auto first, auto second) {
         typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
         if constexpr (sizeof(first) == sizeof(u32x2)) {
             const u32x2 x = __builtin_bit_cast(u32x2, first), y = __builtin_bit_cast(u32x2, second);
@@ -729,6 +747,49 @@ tile_kernel(TileArgs g)
             store(std::true_type{}, std::false_type{});
         else
             store(std::false_type{}, std::false_type{});
+    } else if constexpr (EP == SCALE) {
+        // Sums below 2^31 become fp32 (half a step of 2^-24 relative), then two products and
+        // one rounding to TC.
+        TC *C = static_cast<TC *>(g.C);
+        const float *sb = g.scale_b + (int64_t)group * g.N;
+        auto store = [&](auto inside) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                const int m = mw + BL * i;
+                if (m >= row_end) continue;
+                TC *crow = C + (int64_t)(row0 + m) * g.ldc;
+                const float sa = g.scale_a[row0 + m];
+                Vec before;
+#pragma unroll
+                for (int u = 0; u < FN * GR; ++u) {
+                    const int n = column(u);
+                    float s[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        s[q] = decltype(inside)::value || n + q < g.N ? sb[n + q] : 0.f;
+                    Vec out;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) out[q] = (TC)((float)value(i, u, q) * sa * s[q]);
+                    if constexpr (PAIRED && decltype(inside)::value) {
+                        if (u % 2 == 0)
+                            before = out;
+                        else
+                            store_pair(crow, u - 1, before, out);
+                    } else if (decltype(inside)::value || (g.vec_c && n + 4 <= g.N)) {
+                        *reinterpret_cast<Vec *>(crow + n) = out;
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (n + q < g.N) crow[n + q] = out[q];
+                    }
+                }
+            }
+        };
+        if (whole)
+            store(std::true_type{});
+        else
+            store(std::false_type{});
     } else if constexpr (EP == PART) {
         float *C = static_cast<float *>(g.C) + blockIdx.z * g.slice_stride;
 #pragma unroll

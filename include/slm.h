@@ -1,7 +1,8 @@
 /*
  * libsgemm -- matrix products of language models for AMD Instinct MI355X
- * (gfx950), C ABI: products grouped by expert, the softmax cross entropy of an
- * output layer, and products with weights held in 4 bits.
+ * (gfx950), C ABI: products grouped by expert and the rows they take, the softmax cross
+ * entropy of an output layer, products with weights held in 4 bits and products in 8-bit
+ * integers.
  *
  * The conventions are those of include/sgemm.h: row-major matrices, element
  * (r, c) of a matrix with leading dimension ld at index r*ld + c; device
@@ -203,6 +204,161 @@ int sgemm_q4_matvec(int type, int groups, int rows, int N, int K, int block, con
  */
 int sgemm_q4_quantize(int type, int N, int K, int block, const void *W, int ldw, uint8_t *Q,
                       void *S, uint8_t *Z, hipStream_t stream);
+
+/*
+ * Rows sorted by expert, and back.  `tokens` tokens choose k experts each; slot
+ * s = t * k + j is token t's choice j.
+ *
+ * sgemm_expert_sort -- the rows that grouped products take: a slot whose expert lies in
+ * [0, groups) gets a row, by expert and, within one, by slot (a stable sort); a slot
+ * whose expert lies outside is dropped, and stands behind them all, again by slot.
+ *
+ *   slots     tokens * k, >= 0
+ *   groups    number of experts, 0 .. 4096
+ *   experts   slots int64
+ *   offsets   groups + 1 ints: expert e has rows offsets[e] .. offsets[e+1] - 1
+ *   order     slots ints: the slot of each row, those dropped last; or NULL
+ *   place     slots ints: each slot's row r; -2 - r where it is dropped (r is then one of
+ *             the rows from offsets[groups] on, which no expert has)
+ *   ws, ws_bytes   workspace, 4-byte aligned, of at least
+ *             sgemm_expert_sort_workspace(slots, groups) bytes (NULL where that is 0)
+ * Returns -1 slots, -2 groups, -3 experts (NULL with slots, or not 8-byte aligned), -4
+ * offsets (NULL or not 4-byte aligned), -5 order, -6 place, -7 ws, -8 ws_bytes too small.
+ */
+int sgemm_expert_sort(int slots, int groups, const int64_t *experts, int *offsets, int *order,
+                      int *place, void *ws, int64_t ws_bytes, hipStream_t stream);
+
+/* Bytes of workspace for sgemm_expert_sort; -1, -2 for invalid sizes. */
+int64_t sgemm_expert_sort_workspace(int slots, int groups);
+
+/*
+ * sgemm_expert_gather -- tokens to their rows: with r = place[t*k + j],
+ *     R[r] <- weights[t*k + j] * X[t]
+ * The products are fp32, rounded once to `type`; without weights rows are copied bit for bit.
+ *
+ *   type      enum sgemm_type of X and R
+ *   tokens, k, H   >= 0; tokens * k at most 2^31 - 1025
+ *   X, ldx    tokens x H, ldx >= max(1, H)
+ *   place     tokens * k ints, as sgemm_expert_sort gives them.  Rows are taken where 0 <=
+ *             r < rows; -1 means no row, and any other value is left out as well.  No
+ *             two places are the same (what a row that is named twice holds is not defined)
+ *   weights   tokens * k floats, or NULL: 1
+ *   rows      rows of R, >= 0
+ *   R, ldr    rows x H, ldr >= max(1, H)
+ *   fill      0: rows without a token are left as they were; 1: the rows r of dropped
+ *             slots (place -2 - r) are set to zero, so that with rows = tokens * k all
+ *             of R is written
+ * The gradient by X is sgemm_expert_combine of the gradient by R; that by the weights is
+ * sgemm_expert_combine_backward's with X as dout and the gradient by R as Y.
+ * Returns -1 type, -2 tokens, -3 k (or tokens * k too large), -4 H, -5 X, -6 ldx, -7
+ * place, -8 weights, -9 rows, -10 R, -11 ldr, -12 fill.
+ */
+int sgemm_expert_gather(int type, int tokens, int k, int H, const void *X, int ldx,
+                        const int *place, const float *weights, int rows, void *R, int ldr,
+                        int fill, hipStream_t stream);
+
+/*
+ * sgemm_expert_combine -- rows back to tokens:
+ *     out[t] <- beta * out[t] + sum_j weights[t*k + j] * R[place[t*k + j]]
+ * summed in fp32 in the order of j, rounded once.  A slot without a row adds nothing and
+ * its weight is not used; a token with none gets beta * out[t].  One row may serve several slots.
+ *
+ *   R, ldr    rows x H of `type`;  place, weights as above
+ *   beta      beta == 0: out is written, not read
+ *   out, ldo  tokens x H, ldo >= max(1, H)
+ * Returns -1 type, -2 tokens, -3 k, -4 H, -5 rows, -6 R, -7 ldr, -8 place, -9 weights,
+ * -11 out, -12 ldo.
+ */
+int sgemm_expert_combine(int type, int tokens, int k, int H, int rows, const void *R, int ldr,
+                         const int *place, const float *weights, float beta, void *out, int ldo,
+                         hipStream_t stream);
+
+/*
+ * sgemm_expert_combine_backward -- gradients of sum_t <dout[t], out[t]>:
+ *     dR[place[s]] <- weights[s] * dout[t]        dweights[s] <- <dout[t], R[place[s]]>
+ * A slot without a row gets dweights 0.  The dot products are fp32 sums, in one order for
+ * given sizes: results repeat bit for bit.
+ *
+ *   dout, lddo   tokens x H of `type`
+ *   R, ldr    as the forward pass had it; not read where dweights is NULL
+ *   weights   tokens * k floats, or NULL: 1
+ *   dR, lddr  rows x H of `type`, or NULL: not computed;  fill as in sgemm_expert_gather
+ *   dweights  tokens * k floats, or NULL: not computed
+ * Returns -1 type, -2 tokens, -3 k, -4 H, -5 rows, -6 dout, -7 lddo, -8 R, -9 ldr, -10
+ * place, -11 weights, -12 dR, -13 lddr, -14 fill, -15 dweights.
+ */
+int sgemm_expert_combine_backward(int type, int tokens, int k, int H, int rows, const void *dout,
+                                  int lddo, const void *R, int ldr, const int *place,
+                                  const float *weights, void *dR, int lddr, int fill,
+                                  float *dweights, hipStream_t stream);
+
+/*
+ * Products in 8-bit integers, with a scale for each row of X (token) and each column of Y
+ * (channel): the value of q is q times its scale.
+ *
+ * sgemm_q8_quantize -- rows to 8 bits: with m the largest magnitude of row r of X,
+ *     scales[r] = m / 127 (fp32)        Q[r][k] = X[r][k] / scales[r]
+ * rounded to the nearest integer, ties to even, of the exact quotient of the stored values.
+ * A row whose scale is zero gets zeros; a row that holds an infinity or a NaN gets
+ * the scale NaN and zeros, so that its products are NaN.  Weights are quantised by the same call (N x K: a
+ * scale for each output channel).
+ *
+ *   type      enum sgemm_type of X
+ *   rows, K   >= 0;  X, ldx: rows x K
+ *   k, place  NULL place (k = 0): row r of X goes to row r of Q, out_rows = rows.  Otherwise
+ *             row t goes to the k rows place[t*k + j], as sgemm_expert_gather sends them
+ *             (rows without a token: left as they were, but those of dropped slots set
+ *             to zero, with the scale 0)
+ *   out_rows  rows of Q and scales
+ *   Q, ldq    out_rows x K bytes, ldq >= max(1, K).  The products read rows at 4-byte
+ *             addresses (Q and ldq multiples of 4) fastest
+ *   scales    out_rows floats
+ * Returns -1 type, -2 rows, -3 K, -4 X, -5 ldx, -6 k (negative, rows * k too large, or not
+ * 0 without place), -7 place, -8 out_rows, -9 Q, -10 ldq, -11 scales.
+ */
+int sgemm_q8_quantize(int type, int rows, int K, const void *X, int ldx, int k, const int *place,
+                      int out_rows, int8_t *Q, int ldq, float *scales, hipStream_t stream);
+
+/*
+ * sgemm_q8_gemm -- for each group e, on its rows r = offsets[e] .. offsets[e+1] - 1,
+ *     Y[r][n] <- (sum_k X[r][k] * W_e[n][k]) * x_scales[r] * w_scales[e][n]
+ * The sums are exact (32-bit integers); they become fp32, are multiplied by the row's scale
+ * and then the column's, and rounded to `type`.
+ *
+ *   type      enum sgemm_type of Y
+ *   groups    sets of weights (1 when offsets is NULL)
+ *   rows, N   >= 0;  K 0 .. 131071, which no sum of products of bytes overflows at
+ *   X, ldx    rows x K bytes;  x_scales: rows floats
+ *   W, ldw, stride_w   N x K bytes a group, ldw >= max(1, K), stride_w >= 0 bytes from one
+ *             group to the next;  w_scales: groups x N floats, packed
+ *   Y, ldy    rows x N, written
+ *   offsets   groups + 1 ints on the device, as in sgemm_grouped (rows outside every group
+ *             are left as they were), or NULL: all rows, one group
+ * X and W at 4-byte addresses with leading dimensions (and stride_w) of multiples of 4 are
+ * loaded straight to LDS; others go through registers, more slowly.
+ * Returns -1 type, -2 groups, -3 rows, -4 N (or more than 2^31 - 1 tiles), -5 K, -6 X, -7
+ * ldx, -8 x_scales, -9 W, -10 ldw, -11 stride_w, -12 w_scales, -13 Y, -14 ldy, -15 offsets
+ * not 4-byte aligned.
+ */
+int sgemm_q8_gemm(int type, int groups, int rows, int N, int K, const int8_t *X, int ldx,
+                  const float *x_scales, const int8_t *W, int ldw, int64_t stride_w,
+                  const float *w_scales, void *Y, int ldy, const int *offsets, hipStream_t stream);
+
+/*
+ * sgemm_q8_matvec -- sgemm_q8_quantize and sgemm_q8_gemm in one launch, for a few rows of X:
+ * every workgroup quantises them for itself.  One pass over the weights serves up to 16 rows
+ * (fewer where K is above 6656: 104 KB of quantised rows), so this is meant for single tokens and
+ * short batches; any number of rows is computed, in passes of so many.  Results
+ * are those of the two calls bit for bit.
+ *
+ *   type      enum sgemm_type of X and Y
+ *   groups    as in sgemm_q8_gemm, at most 65535;  K at most 106496
+ * Returns -1 type, -2 groups, -3 rows, -4 N, -5 K, -6 X, -7 ldx, -8 W, -9 ldw, -10
+ * stride_w, -11 w_scales, -12 Y, -13 ldy, -14 offsets not 4-byte aligned.
+ */
+int sgemm_q8_matvec(int type, int groups, int rows, int N, int K, const void *X, int ldx,
+                    const int8_t *W, int ldw, int64_t stride_w, const float *w_scales, void *Y,
+                    int ldy, const int *offsets, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -123,9 +123,15 @@ extern "C" int sgemm_expert_gather(int type, int tokens, int k, int H, const voi
     a.tokens = tokens, a.k = k, a.H = H, a.rows = rows, a.fill = fill;
     const int pieces = (int)ceil_div(H, 16 / size);
     a.cols_log2 = cols_log2(pieces);
+    const bool uniform = a.cols_log2 >= 6;  // a wave has one token
+    const auto of = [&](auto plain, auto plain_uniform, auto weighted, auto weighted_uniform) {
+        return weights ? (uniform ? weighted_uniform : weighted) : uniform ? plain_uniform : plain;
+    };
     auto fn = type == SGEMM_TYPE_BF16
-                  ? (weights ? gather_kernel<bf16, true> : gather_kernel<bf16, false>)
-                  : (weights ? gather_kernel<float, true> : gather_kernel<float, false>);
+                  ? of(gather_kernel<bf16, false, false>, gather_kernel<bf16, false, true>,
+                       gather_kernel<bf16, true, false>, gather_kernel<bf16, true, true>)
+                  : of(gather_kernel<float, false, false>, gather_kernel<float, false, true>,
+                       gather_kernel<float, true, false>, gather_kernel<float, true, true>);
     fn<<<copy_grid(tokens, pieces, a.cols_log2), dim3(256), 0, stream>>>(a);
     return (int)hipGetLastError();
 }
@@ -151,7 +157,10 @@ extern "C" int sgemm_expert_combine(int type, int tokens, int k, int H, int rows
     a.tokens = tokens, a.k = reads ? k : 0, a.H = H, a.rows = rows;
     const int pieces = (int)ceil_div(H, 16 / size);
     a.cols_log2 = cols_log2(pieces);
-    auto fn = type == SGEMM_TYPE_BF16 ? combine_kernel<bf16> : combine_kernel<float>;
+    const bool uniform = a.cols_log2 >= 6;  // a wave has one token
+    auto fn = type == SGEMM_TYPE_BF16
+                  ? (uniform ? combine_kernel<bf16, true> : combine_kernel<bf16, false>)
+                  : (uniform ? combine_kernel<float, true> : combine_kernel<float, false>);
     fn<<<copy_grid(tokens, pieces, a.cols_log2), dim3(256), 0, stream>>>(a);
     return (int)hipGetLastError();
 }

@@ -177,132 +177,162 @@ struct RouteArgs {
     int cols_log2;         // threads of a workgroup along a row (of 256)
 };
 
-// Sixteen bytes of a row; addresses need the element's alignment only.
+// Sixteen bytes of a row (E values); addresses need the element's alignment only.
 template <typename T> struct Piece {
     static constexpr int E = 16 / sizeof(T);
-    T v[E];
-    __device__ __forceinline__ void load(const T *p, int left)
-    {
-        if (left >= E) {
-            __builtin_memcpy(v, p, 16);
-        } else {
-#pragma unroll
-            for (int i = 0; i < E; ++i) v[i] = i < left ? p[i] : (T)0.f;
-        }
-    }
-    __device__ __forceinline__ void store(T *p, int left) const
-    {
-        if (left >= E) {
-            __builtin_memcpy(p, v, 16);
-        } else {
-#pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (i < left) p[i] = v[i];
-        }
-    }
+    typedef T Vec __attribute__((ext_vector_type(E)));
+    typedef Vec Loose __attribute__((aligned(sizeof(T))));
+    Vec v;
+    __device__ __forceinline__ void load(const T *p) { v = *reinterpret_cast<const Loose *>(p); }
+    __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<Loose *>(p) = v; }
+    __device__ __forceinline__ void zero() { v = (T)0.f; }
+};
+// One value, for what is left of a row after its whole pieces.
+template <typename T> struct Single {
+    static constexpr int E = 1;
+    T v[1];
+    __device__ __forceinline__ void load(const T *p) { v[0] = *p; }
+    __device__ __forceinline__ void store(T *p) const { *p = v[0]; }
+    __device__ __forceinline__ void zero() { v[0] = (T)0.f; }
 };
 
-// The row that a place names: -1 for none; `unused` where the row is a dropped slot's.
-__device__ __forceinline__ int row_of(int place, int rows, bool &unused)
+// p[i], a scalar load where i is the wave's (no output of these kernels overlaps an input).
+template <bool UNIFORM, typename T> __device__ __forceinline__ T read(const T *p, int64_t i)
 {
-    unused = place <= -2;
-    const int r = unused ? -2 - place : place;
-    return r >= 0 && r < rows ? r : -1;
+    if constexpr (UNIFORM)
+        return ((const __attribute__((address_space(4))) T *)(uintptr_t)p)[i];
+    else
+        return p[i];
+}
+
+// Choices of a token that are handled together: their rows are all in flight at once.
+constexpr int kChoices = 8;
+
+// Up to kChoices choices of a token from j0 on: their places and weights.
+template <bool UNIFORM> struct Choices {
+    int p[kChoices];
+    float w[kChoices];
+    uint32_t rows;
+    __device__ __forceinline__ Choices(const RouteArgs &a, int t, int j0, bool weighted) : rows(a.rows)
+    {
+        // (Past the last choice the last is read again: loads without branches.)
+#pragma unroll
+        for (int j = 0; j < kChoices; ++j) {
+            const int64_t slot = (int64_t)t * a.k + (j0 + j < a.k ? j0 + j : a.k - 1);
+            p[j] = read<UNIFORM>(a.place, slot);
+            if (j0 + j >= a.k) p[j] = -1;
+            w[j] = 1.f;
+            if (weighted) w[j] = read<UNIFORM>(a.weights, slot);
+        }
+    }
+    // Choice j has row p[j]; or it is dropped, and row -2 - p[j] is one that no expert has.
+    __device__ __forceinline__ bool held(int j) const { return (uint32_t)p[j] < rows; }
+    __device__ __forceinline__ bool dropped(int j) const { return (uint32_t)(-2 - p[j]) < rows; }
+};
+
+// Which token and column a workgroup's turn b is for.  UNIFORM: a wave has one token, and the
+// compiler is told so: its places and weights then are scalar loads, and its rows' addresses a
+// scalar base each, where vector loads of them would be two more for each of a row.
+template <bool UNIFORM, int E>
+__device__ __forceinline__ bool turn_of(const RouteArgs &a, int64_t b, int parts, int &t, int &h)
+{
+    const int cols = 1 << a.cols_log2, per = 256 >> a.cols_log2;
+    const int col = threadIdx.x & (cols - 1);
+    int sub = threadIdx.x >> a.cols_log2;
+    if constexpr (UNIFORM) sub = __builtin_amdgcn_readfirstlane(sub);
+    const int64_t at = b / parts * per + sub;
+    h = ((int)(b % parts) * cols + col) * E;
+    t = (int)at;
+    return at < a.tokens;
+}
+
+__device__ __forceinline__ int parts_of_row(const RouteArgs &a, int e)
+{
+    return ((a.H + e - 1) / e + (1 << a.cols_log2) - 1) >> a.cols_log2;
+}
+__device__ __forceinline__ int64_t turns(const RouteArgs &a, int parts)
+{
+    const int per = 256 >> a.cols_log2;
+    return ((int64_t)a.tokens + per - 1) / per * parts;
 }
 
 // R[place] <- w X[t], a thread per 16 bytes of a token.
-template <typename T, bool WEIGHTED>
+template <typename T, bool WEIGHTED, bool UNIFORM>
 __global__ void __launch_bounds__(256) gather_kernel(RouteArgs a)
 {
     constexpr int E = Piece<T>::E;
-    const int cols = 1 << a.cols_log2, per = 256 >> a.cols_log2;
-    const int col = threadIdx.x & (cols - 1), sub = threadIdx.x >> a.cols_log2;
-    const int pieces = (a.H + E - 1) / E, parts = (pieces + cols - 1) / cols;
-    const int64_t work = (int64_t)((a.tokens + per - 1) / per) * parts;
+    const int parts = parts_of_row(a, E);
+    const int64_t work = turns(a, parts);
     for (int64_t b = blockIdx.x; b < work; b += gridDim.x) {
-        const int64_t t = b / parts * per + sub;
-        const int h = ((int)(b % parts) * cols + col) * E;
-        if (t >= a.tokens || h >= a.H) continue;
-        const int left = a.H - h;
-        Piece<T> x;
-        x.load(static_cast<const T *>(a.X) + t * a.ldx + h, left);
-        const int *place = a.place + t * a.k;
-        T *out = static_cast<T *>(a.out) + h;
-        for (int j0 = 0; j0 < a.k; j0 += 4) {
-            int r[4];
-            float w[4];
-            bool unused[4];
+        int t, h;
+        if (!turn_of<UNIFORM, E>(a, b, parts, t, h) || h >= a.H) continue;
+        const auto copy = [&](auto x, int at) {
+            x.load(static_cast<const T *>(a.X) + t * a.ldx + at);
+            for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+                const Choices<UNIFORM> c(a, t, j0, WEIGHTED);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                r[j] = row_of(j0 + j < a.k ? place[j0 + j] : -1, a.rows, unused[j]);
-                if (unused[j] && !a.fill) r[j] = -1;
-                if constexpr (WEIGHTED)
-                    w[j] = r[j] >= 0 && !unused[j] ? a.weights[t * a.k + j0 + j] : 0.f;
-            }
+                for (int j = 0; j < kChoices; ++j) {
+                    auto y = x;
+                    if (c.held(j)) {
+                        if constexpr (WEIGHTED) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (r[j] < 0) continue;
-                Piece<T> y = x;
-                if constexpr (WEIGHTED) {
-#pragma unroll
-                    for (int i = 0; i < E; ++i) y.v[i] = (T)(w[j] * (float)x.v[i]);
+                            for (int i = 0; i < x.E; ++i) y.v[i] = (T)(c.w[j] * (float)x.v[i]);
+                        }
+                        y.store(static_cast<T *>(a.out) + c.p[j] * a.ldo + at);
+                    } else if (a.fill && c.dropped(j)) {
+                        y.zero();
+                        y.store(static_cast<T *>(a.out) + (-2 - c.p[j]) * a.ldo + at);
+                    }
                 }
-#pragma unroll
-                for (int i = 0; i < E; ++i) y.v[i] = unused[j] ? (T)0.f : y.v[i];
-                y.store(out + r[j] * a.ldo, left);
             }
-        }
+        };
+        if (h + E <= a.H)
+            copy(Piece<T>(), h);
+        else
+            for (; h < a.H; ++h) copy(Single<T>(), h);
     }
 }
 
 // out[t] <- beta out[t] + sum_j w R[place], a thread per 16 bytes of a token.
-template <typename T>
+template <typename T, bool UNIFORM>
 __global__ void __launch_bounds__(256) combine_kernel(RouteArgs a)
 {
     constexpr int E = Piece<T>::E;
-    const int cols = 1 << a.cols_log2, per = 256 >> a.cols_log2;
-    const int col = threadIdx.x & (cols - 1), sub = threadIdx.x >> a.cols_log2;
-    const int pieces = (a.H + E - 1) / E, parts = (pieces + cols - 1) / cols;
-    const int64_t work = (int64_t)((a.tokens + per - 1) / per) * parts;
+    const int parts = parts_of_row(a, E);
+    const int64_t work = turns(a, parts);
     for (int64_t b = blockIdx.x; b < work; b += gridDim.x) {
-        const int64_t t = b / parts * per + sub;
-        const int h = ((int)(b % parts) * cols + col) * E;
-        if (t >= a.tokens || h >= a.H) continue;
-        const int left = a.H - h;
-        const T *R = static_cast<const T *>(a.R) + h;
-        const int *place = a.place + t * a.k;
-        float sum[E];
+        int t, h;
+        if (!turn_of<UNIFORM, E>(a, b, parts, t, h) || h >= a.H) continue;
+        const auto sum_up = [&](auto y, int at) {
+            float sum[y.E];
 #pragma unroll
-        for (int i = 0; i < E; ++i) sum[i] = 0.f;
-        for (int j0 = 0; j0 < a.k; j0 += 4) {
-            Piece<T> x[4];
-            float w[4];
-            int r[4];
+            for (int i = 0; i < y.E; ++i) sum[i] = 0.f;
+            for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+                const Choices<UNIFORM> c(a, t, j0, a.weights != nullptr);
+                decltype(y) x[kChoices];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                r[j] = j0 + j < a.k ? place[j0 + j] : -1;
-                if (r[j] >= a.rows) r[j] = -1;
-                w[j] = 1.f;
-                if (r[j] < 0) continue;
-                if (a.weights) w[j] = a.weights[t * a.k + j0 + j];
-                x[j].load(R + r[j] * a.ldr, left);
+                for (int j = 0; j < kChoices; ++j)
+                    if (c.held(j)) x[j].load(static_cast<const T *>(a.R) + c.p[j] * a.ldr + at);
+#pragma unroll
+                for (int j = 0; j < kChoices; ++j)
+                    if (c.held(j))
+#pragma unroll
+                        for (int i = 0; i < y.E; ++i) sum[i] = fmaf(c.w[j], (float)x[j].v[i], sum[i]);
+            }
+            T *out = static_cast<T *>(a.out) + t * a.ldo + at;
+            if (a.beta != 0.f) {
+                y.load(out);
+#pragma unroll
+                for (int i = 0; i < y.E; ++i) sum[i] = fmaf(a.beta, (float)y.v[i], sum[i]);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (r[j] >= 0)
-#pragma unroll
-                    for (int i = 0; i < E; ++i) sum[i] = fmaf(w[j], (float)x[j].v[i], sum[i]);
-        }
-        T *out = static_cast<T *>(a.out) + t * a.ldo + h;
-        Piece<T> y;
-        if (a.beta != 0.f) {
-            y.load(out, left);
-#pragma unroll
-            for (int i = 0; i < E; ++i) sum[i] = fmaf(a.beta, (float)y.v[i], sum[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < E; ++i) y.v[i] = (T)sum[i];
-        y.store(out, left);
+            for (int i = 0; i < y.E; ++i) y.v[i] = (T)sum[i];
+            y.store(out);
+        };
+        if (h + E <= a.H)
+            sum_up(Piece<T>(), h);
+        else
+            for (; h < a.H; ++h) sum_up(Single<T>(), h);
     }
 }
 
@@ -311,78 +341,79 @@ __global__ void __launch_bounds__(256) combine_kernel(RouteArgs a)
 template <typename T, int WAVES>
 __global__ void __launch_bounds__(256) combine_backward_kernel(RouteArgs a)
 {
-    constexpr int E = Piece<T>::E, KT = 8, TOKENS = 4 / WAVES;
-    __shared__ float parts[4][KT];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    constexpr int E = Piece<T>::E, TOKENS = 4 / WAVES;
+    __shared__ float parts[4][kChoices];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     for (int64_t t0 = (int64_t)blockIdx.x * TOKENS; t0 < a.tokens; t0 += (int64_t)gridDim.x * TOKENS) {
-        const int64_t t = t0 + wave / WAVES;
-        const bool here = t < a.tokens;
-        for (int j0 = 0; j0 < a.k; j0 += KT) {
-            float dot[KT], w[KT];
-            int r[KT];
-            bool unused[KT];
+        const bool here = t0 + wave / WAVES < a.tokens;
+        const int t = (int)(here ? t0 + wave / WAVES : a.tokens - 1);
+        for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+            float dot[kChoices];
 #pragma unroll
-            for (int j = 0; j < KT; ++j) {
-                dot[j] = 0.f, r[j] = -1, w[j] = 1.f, unused[j] = false;
-                if (here && a.rows > 0 && j0 + j < a.k) {
-                    r[j] = row_of(a.place[t * a.k + j0 + j], a.rows, unused[j]);
-                    if (r[j] >= 0 && !unused[j] && a.weights) w[j] = a.weights[t * a.k + j0 + j];
-                }
-            }
-            const int step = WAVES * 64 * E;
-            for (int h = ((wave % WAVES) * 64 + lane) * E; here && a.rows > 0 && h < a.H;
-                 h += step) {
-                const int left = a.H - h;
-                Piece<T> d, x[KT];
-                d.load(static_cast<const T *>(a.X) + t * a.ldx + h, left);
-                if (a.dweights) {
+            for (int j = 0; j < kChoices; ++j) dot[j] = 0.f;
+            if (here && a.rows > 0) {
+                const Choices<true> c(a, t, j0, a.weights != nullptr);
+                const auto both = [&](auto d, int at) {
+                    decltype(d) x[kChoices];
+                    if (a.dweights) {
 #pragma unroll
-                    for (int j = 0; j < KT; ++j)
-                        if (r[j] >= 0 && !unused[j])
-                            x[j].load(static_cast<const T *>(a.R) + r[j] * a.ldr + h, left);
-#pragma unroll
-                    for (int j = 0; j < KT; ++j)
-                        if (r[j] >= 0 && !unused[j])
-#pragma unroll
-                            for (int i = 0; i < E; ++i)
-                                dot[j] = fmaf((float)d.v[i], (float)x[j].v[i], dot[j]);
-                }
-                if (a.out) {
-                    T *out = static_cast<T *>(a.out) + h;
-#pragma unroll
-                    for (int j = 0; j < KT; ++j) {
-                        if (r[j] < 0 || (unused[j] && !a.fill)) continue;
-                        Piece<T> y;
-#pragma unroll
-                        for (int i = 0; i < E; ++i)
-                            y.v[i] = unused[j] ? (T)0.f : (T)(w[j] * (float)d.v[i]);
-                        y.store(out + r[j] * a.ldo, left);
+                        for (int j = 0; j < kChoices; ++j)
+                            if (c.held(j)) x[j].load(static_cast<const T *>(a.R) + c.p[j] * a.ldr + at);
                     }
+                    d.load(static_cast<const T *>(a.X) + t * a.ldx + at);
+                    if (a.out) {
+#pragma unroll
+                        for (int j = 0; j < kChoices; ++j) {
+                            auto y = d;
+                            if (c.held(j)) {
+#pragma unroll
+                                for (int i = 0; i < d.E; ++i) y.v[i] = (T)(c.w[j] * (float)d.v[i]);
+                                y.store(static_cast<T *>(a.out) + c.p[j] * a.ldo + at);
+                            } else if (a.fill && c.dropped(j)) {
+                                y.zero();
+                                y.store(static_cast<T *>(a.out) + (-2 - c.p[j]) * a.ldo + at);
+                            }
+                        }
+                    }
+                    if (a.dweights) {
+#pragma unroll
+                        for (int j = 0; j < kChoices; ++j)
+                            if (c.held(j))
+#pragma unroll
+                                for (int i = 0; i < d.E; ++i)
+                                    dot[j] = fmaf((float)d.v[i], (float)x[j].v[i], dot[j]);
+                    }
+                };
+                for (int h = ((wave % WAVES) * 64 + lane) * E; h < a.H; h += WAVES * 64 * E) {
+                    if (h + E <= a.H)
+                        both(Piece<T>(), h);
+                    else
+                        for (int at = h; at < a.H; ++at) both(Single<T>(), at);
                 }
             }
             if (!a.dweights) continue;
 #pragma unroll
-            for (int j = 0; j < KT; ++j)
+            for (int j = 0; j < kChoices; ++j)
 #pragma unroll
                 for (int d = 1; d < 64; d *= 2) dot[j] += __shfl_xor(dot[j], d);
             if constexpr (WAVES > 1) {
                 if (lane == 0)
 #pragma unroll
-                    for (int j = 0; j < KT; ++j) parts[wave][j] = dot[j];
+                    for (int j = 0; j < kChoices; ++j) parts[wave][j] = dot[j];
                 __syncthreads();
 #pragma unroll
-                for (int j = 0; j < KT; ++j) {
+                for (int j = 0; j < kChoices; ++j) {
                     dot[j] = 0.f;
 #pragma unroll
-                    for (int w = 0; w < WAVES; ++w)
-                        dot[j] += parts[wave / WAVES * WAVES + w][j];
+                    for (int w = 0; w < WAVES; ++w) dot[j] += parts[wave / WAVES * WAVES + w][j];
                 }
                 __syncthreads();
             }
             if (here && wave % WAVES == 0 && lane == 0)
 #pragma unroll
-                for (int j = 0; j < KT; ++j)
-                    if (j0 + j < a.k) a.dweights[t * a.k + j0 + j] = dot[j];
+                for (int j = 0; j < kChoices; ++j)
+                    if (j0 + j < a.k) a.dweights[(int64_t)t * a.k + j0 + j] = dot[j];
         }
     }
 }

@@ -50,6 +50,13 @@ dim3 copy_grid(int tokens, int pieces, int log2)
     return dim3((unsigned)(work < kMostBlocks ? work : kMostBlocks));
 }
 
+template <typename T, int KT> auto backward_of(int waves)
+{
+    return waves == 1   ? combine_backward_kernel<T, 1, KT>
+           : waves == 2 ? combine_backward_kernel<T, 2, KT>
+                        : combine_backward_kernel<T, 4, KT>;
+}
+
 // The checks that the copies share, of sizes; `type` is parameter 1, tokens 2, k 3, H 4.
 int check_sizes(int type, int tokens, int k, int H)
 {
@@ -192,12 +199,16 @@ extern "C" int sgemm_expert_combine_backward(int type, int tokens, int k, int H,
     a.dweights = dweights;
     a.ldx = lddo, a.ldr = ldr, a.ldo = lddr;
     a.tokens = tokens, a.k = k, a.H = H, a.rows = work ? rows : 0, a.fill = fill;
-    // Four waves a token where tokens alone would not fill the chip.
-    const bool few = tokens < 4096;
+    // As many waves a token as its row has 16-byte pieces for, and four or eight choices at a time.
+    // us with 1, 2 and 4 waves: 32768 x 8 choices, 64 pieces 122, 132, 180; 128 pieces 232, 232, 242; 16384
+    // x 4, 256 pieces 139, 135, 122; 8192 x 2, 512 pieces 81, 73, 72.  With 4 and 8 choices: 16384 x 4
+    // 122 and 125, 8192 x 6 rows of 896 pieces 313 and 312, 4099 x 3 of 251 fp32 pieces 29.6 and 33.0.
+    const int64_t pieces = ceil_div(H, 16 / size);
+    const int waves = pieces <= 64 ? 1 : pieces <= 128 ? 2 : 4;
     auto fn = type == SGEMM_TYPE_BF16
-                  ? (few ? combine_backward_kernel<bf16, 4> : combine_backward_kernel<bf16, 1>)
-                  : (few ? combine_backward_kernel<float, 4> : combine_backward_kernel<float, 1>);
-    const int64_t blocks = few ? tokens : ceil_div(tokens, 4);
+                  ? (k <= 4 ? backward_of<bf16, 4>(waves) : backward_of<bf16, 8>(waves))
+                  : (k <= 4 ? backward_of<float, 4>(waves) : backward_of<float, 8>(waves));
+    const int64_t blocks = ceil_div(tokens, 4 / waves);
     fn<<<dim3((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks)), dim3(256), 0, stream>>>(a);
     return (int)hipGetLastError();
 }

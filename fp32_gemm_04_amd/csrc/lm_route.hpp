@@ -208,16 +208,16 @@ template <bool UNIFORM, typename T> __device__ __forceinline__ T read(const T *p
 // Choices of a token that are handled together: their rows are all in flight at once.
 constexpr int kChoices = 8;
 
-// Up to kChoices choices of a token from j0 on: their places and weights.
-template <bool UNIFORM> struct Choices {
-    int p[kChoices];
-    float w[kChoices];
+// Up to N choices of a token from j0 on: their places and weights.
+template <bool UNIFORM, int N> struct Choices {
+    int p[N];
+    float w[N];
     uint32_t rows;
     __device__ __forceinline__ Choices(const RouteArgs &a, int t, int j0, bool weighted) : rows(a.rows)
     {
         // (Past the last choice the last is read again: loads without branches.)
 #pragma unroll
-        for (int j = 0; j < kChoices; ++j) {
+        for (int j = 0; j < N; ++j) {
             const int64_t slot = (int64_t)t * a.k + (j0 + j < a.k ? j0 + j : a.k - 1);
             p[j] = read<UNIFORM>(a.place, slot);
             if (j0 + j >= a.k) p[j] = -1;
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(256) gather_kernel(RouteArgs a)
         const auto copy = [&](auto x, int at) {
             x.load(static_cast<const T *>(a.X) + t * a.ldx + at);
             for (int j0 = 0; j0 < a.k; j0 += kChoices) {
-                const Choices<UNIFORM> c(a, t, j0, WEIGHTED);
+                const Choices<UNIFORM, kChoices> c(a, t, j0, WEIGHTED);
 #pragma unroll
                 for (int j = 0; j < kChoices; ++j) {
                     auto y = x;
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(256) combine_kernel(RouteArgs a)
 #pragma unroll
             for (int i = 0; i < y.E; ++i) sum[i] = 0.f;
             for (int j0 = 0; j0 < a.k; j0 += kChoices) {
-                const Choices<UNIFORM> c(a, t, j0, a.weights != nullptr);
+                const Choices<UNIFORM, kChoices> c(a, t, j0, a.weights != nullptr);
                 decltype(y) x[kChoices];
 #pragma unroll
                 for (int j = 0; j < kChoices; ++j)
@@ -336,49 +336,57 @@ __global__ void __launch_bounds__(256) combine_kernel(RouteArgs a)
     }
 }
 
-// dR[place] <- w dout[t] and dw = <dout[t], R[place]>: WAVES waves share a token, eight of its
-// rows at a time.
-template <typename T, int WAVES>
+// p, in a way that keeps what is computed from it where it is used: the addresses of eight rows of
+// two operands, taken out of a loop, would not fit the scalar registers.
+__device__ __forceinline__ int here_only(int p)
+{
+    asm("" : "+s"(p));
+    return p;
+}
+
+// dR[place] <- w dout[t] and dw = <dout[t], R[place]>: WAVES waves share a token, KT of its
+// choices at a time.
+template <typename T, int WAVES, int KT>
 __global__ void __launch_bounds__(256) combine_backward_kernel(RouteArgs a)
 {
     constexpr int E = Piece<T>::E, TOKENS = 4 / WAVES;
-    __shared__ float parts[4][kChoices];
+    __shared__ float parts[4][KT];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     for (int64_t t0 = (int64_t)blockIdx.x * TOKENS; t0 < a.tokens; t0 += (int64_t)gridDim.x * TOKENS) {
         const bool here = t0 + wave / WAVES < a.tokens;
         const int t = (int)(here ? t0 + wave / WAVES : a.tokens - 1);
-        for (int j0 = 0; j0 < a.k; j0 += kChoices) {
-            float dot[kChoices];
+        for (int j0 = 0; j0 < a.k; j0 += KT) {
+            float dot[KT];
 #pragma unroll
-            for (int j = 0; j < kChoices; ++j) dot[j] = 0.f;
+            for (int j = 0; j < KT; ++j) dot[j] = 0.f;
             if (here && a.rows > 0) {
-                const Choices<true> c(a, t, j0, a.weights != nullptr);
+                const Choices<true, KT> c(a, t, j0, a.weights != nullptr);
                 const auto both = [&](auto d, int at) {
-                    decltype(d) x[kChoices];
+                    decltype(d) x[KT];
                     if (a.dweights) {
 #pragma unroll
-                        for (int j = 0; j < kChoices; ++j)
-                            if (c.held(j)) x[j].load(static_cast<const T *>(a.R) + c.p[j] * a.ldr + at);
+                        for (int j = 0; j < KT; ++j)
+                            if (c.held(j)) x[j].load(static_cast<const T *>(a.R) + here_only(c.p[j]) * a.ldr + at);
                     }
                     d.load(static_cast<const T *>(a.X) + t * a.ldx + at);
                     if (a.out) {
 #pragma unroll
-                        for (int j = 0; j < kChoices; ++j) {
+                        for (int j = 0; j < KT; ++j) {
                             auto y = d;
                             if (c.held(j)) {
 #pragma unroll
                                 for (int i = 0; i < d.E; ++i) y.v[i] = (T)(c.w[j] * (float)d.v[i]);
-                                y.store(static_cast<T *>(a.out) + c.p[j] * a.ldo + at);
+                                y.store(static_cast<T *>(a.out) + here_only(c.p[j]) * a.ldo + at);
                             } else if (a.fill && c.dropped(j)) {
                                 y.zero();
-                                y.store(static_cast<T *>(a.out) + (-2 - c.p[j]) * a.ldo + at);
+                                y.store(static_cast<T *>(a.out) + here_only(-2 - c.p[j]) * a.ldo + at);
                             }
                         }
                     }
                     if (a.dweights) {
 #pragma unroll
-                        for (int j = 0; j < kChoices; ++j)
+                        for (int j = 0; j < KT; ++j)
                             if (c.held(j))
 #pragma unroll
                                 for (int i = 0; i < d.E; ++i)
@@ -393,27 +401,31 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(RouteArgs a)
                 }
             }
             if (!a.dweights) continue;
+            // While several sums are left a lane exchanges half of them for its neighbour's other
+            // half: lane l ends with the sum of choice l % KT.
 #pragma unroll
-            for (int j = 0; j < kChoices; ++j)
+            for (int n = KT / 2, d = 1; d < 64; n /= 2, d *= 2) {
+                if (n > 0) {
+                    const bool odd = lane & d;
 #pragma unroll
-                for (int d = 1; d < 64; d *= 2) dot[j] += __shfl_xor(dot[j], d);
-            if constexpr (WAVES > 1) {
-                if (lane == 0)
-#pragma unroll
-                    for (int j = 0; j < kChoices; ++j) parts[wave][j] = dot[j];
-                __syncthreads();
-#pragma unroll
-                for (int j = 0; j < kChoices; ++j) {
-                    dot[j] = 0.f;
-#pragma unroll
-                    for (int w = 0; w < WAVES; ++w) dot[j] += parts[wave / WAVES * WAVES + w][j];
+                    for (int j = 0; j < n; ++j) {
+                        const float keep = odd ? dot[2 * j + 1] : dot[2 * j];
+                        dot[j] = keep + __shfl_xor(odd ? dot[2 * j] : dot[2 * j + 1], d);
+                    }
+                } else {
+                    dot[0] += __shfl_xor(dot[0], d);
                 }
+            }
+            if constexpr (WAVES > 1) {
+                if (lane < KT) parts[wave][lane] = dot[0];
+                __syncthreads();
+                dot[0] = 0.f;
+#pragma unroll
+                for (int w = 0; w < WAVES; ++w) dot[0] += parts[wave / WAVES * WAVES + w][lane % KT];
                 __syncthreads();
             }
-            if (here && wave % WAVES == 0 && lane == 0)
-#pragma unroll
-                for (int j = 0; j < kChoices; ++j)
-                    if (j0 + j < a.k) a.dweights[(int64_t)t * a.k + j0 + j] = dot[j];
+            if (here && wave % WAVES == 0 && lane < KT && j0 + lane < a.k)
+                a.dweights[(int64_t)t * a.k + j0 + lane] = dot[0];
         }
     }
 }

@@ -169,9 +169,9 @@ def test_places_outside_the_rows_are_left_out():
     assert Q[0].tolist() == [127] * 8 and scales[0] * 127 == 1.0
 
 
-# Below 4096 tokens four waves share a token; from there on each has one.
+# One, two and four waves a token (by H), four and eight choices at a time (by k).
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("T,k,H", SHAPES + [(4097, 3, 40), (5000, 9, 700)])
+@pytest.mark.parametrize("T,k,H", SHAPES + [(4097, 3, 40), (5000, 9, 700), (40, 5, 900)])
 @pytest.mark.parametrize("pad,shift", [(0, 0), (3, 1)])
 def test_combine_backward(dtype, T, k, H, pad, shift):
     say("combine backward", dtype, T, k, H, pad, shift)

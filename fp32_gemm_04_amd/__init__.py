@@ -752,9 +752,10 @@ def expert_sort(experts, groups: int, stream=None):
         offsets = experts.new_empty(groups + 1, dtype=torch.int32)
         order = experts.new_empty(slots, dtype=torch.int32)
         place = experts.new_empty(experts.shape, dtype=torch.int32)
-        ws = experts.new_empty(n, dtype=torch.uint8)
+        ws = experts.new_empty(n, dtype=torch.uint8) if n else None
         return _lib.sgemm_expert_sort(slots, groups, experts.data_ptr(), offsets.data_ptr(),
-                                      order.data_ptr(), place.data_ptr(), ws.data_ptr(), n, s)
+                                      order.data_ptr(), place.data_ptr(),
+                                      ws.data_ptr() if n else 0, n, s)
     _run("sgemm_expert_sort", dev, stream, (experts,), body)
     return offsets, order, place
 

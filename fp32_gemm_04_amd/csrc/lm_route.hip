@@ -15,24 +15,24 @@ namespace {
 constexpr int kMostGroups = 4096;
 constexpr int kMostSegments = 256;
 
-// How a sort is cut: the slots of one chunk are counted and placed by one workgroup; more go
-// in two launches over segments.
+// How a sort is cut into segments of whole chunks, one a workgroup.  Few slots are counted by
+// every workgroup for itself, in one launch; for more, a launch before counts each segment's.
 struct SortPlan {
-    int waves, segment, segments;
-    int64_t bytes;
+    int waves, segment, segments, pitch;
+    int64_t bytes;  // of counts; 0: one launch
 };
 
 SortPlan sort_plan(int slots, int groups)
 {
     SortPlan p;
-    // 16 waves' counters fit 32 KB up to 1024 experts.
-    p.waves = groups <= 1024 ? 16 : 4;
+    p.waves = groups <= 2048 ? 16 : 8;  // whose counters fit LDS
     const int chunk = sort_chunk(p.waves);
     const int64_t chunks = slots > 0 ? ceil_div(slots, chunk) : 1;
     p.segments = (int)(chunks < kMostSegments ? chunks : kMostSegments);
-    // Whole chunks each; the last segments may be empty.
+    // The last segments may be empty.
     p.segment = (int)(ceil_div(chunks, p.segments) * chunk);
-    p.bytes = p.segments > 1 ? (int64_t)p.segments * (groups + 1) * 4 : 0;
+    p.pitch = (int)round_up(p.segments, 4);
+    p.bytes = slots > 16384 ? (int64_t)p.pitch * (groups + 1) * 4 : 0;
     return p;
 }
 
@@ -91,19 +91,19 @@ extern "C" int sgemm_expert_sort(int slots, int groups, const int64_t *experts, 
     if (!aligned(order, 4)) return -5;
     if ((slots > 0 && !place) || !aligned(place, 4)) return -6;
     const SortPlan p = sort_plan(slots, groups);
-    if ((p.bytes > 0 && !ws) || !aligned(ws, 4)) return -7;
+    if ((p.bytes > 0 && !ws) || !aligned(ws, 16)) return -7;
     if (ws_bytes < p.bytes) return -8;
     SortArgs a = {};
     a.experts = experts, a.offsets = offsets, a.order = order, a.place = place;
-    a.counts = p.segments > 1 ? static_cast<int *>(ws) : nullptr;
+    a.counts = p.bytes > 0 ? static_cast<int *>(ws) : nullptr;
     a.slots = slots, a.groups = groups;
-    a.segment = p.segment, a.segments = p.segments;
+    a.segment = p.segment, a.segments = p.segments, a.pitch = p.pitch;
     const int n = groups + 1;
     if (a.counts) {
         sort_count_kernel<<<dim3(p.segments), dim3(p.waves * 64), n * 4, stream>>>(a);
         if (int rc = (int)hipGetLastError()) return rc;
     }
-    const int lds = n * 4 + (p.waves * n * 2 > n * 4 ? p.waves * n * 2 : n * 4);
+    const int lds = 2 * n * 4 + p.waves * n * 2;
     sort_place_kernel<<<dim3(p.segments), dim3(p.waves * 64), lds, stream>>>(a);
     return (int)hipGetLastError();
 }

@@ -18,17 +18,18 @@ namespace lm {
 struct SortArgs {
     const int64_t *experts;
     int *offsets, *order, *place;
-    int *counts;    // of each segment and expert, or null: counted by every workgroup itself
+    int *counts;    // of each expert and segment, or null: counted by every workgroup itself
     int slots, groups;
     int segment;    // slots of a workgroup, a multiple of a chunk
     int segments;
+    int pitch;      // counts of one expert: segments, rounded up to 4
 };
 
-constexpr int kSortItems = 4;  // slots of a lane, in registers, per chunk
+constexpr int kSortItems = 2;  // slots of a lane, in registers, per chunk
 inline __host__ __device__ int sort_chunk(int waves) { return waves * 64 * kSortItems; }
 
 // The place of an expert's number among the counters: those outside come last.
-__device__ __forceinline__ int sort_key(const int64_t *experts, int slot, int groups)
+__device__ __forceinline__ int sort_key(const int64_t *experts, int64_t slot, int groups)
 {
     const int64_t e = experts[slot];
     return e >= 0 && e < groups ? (int)e : groups;
@@ -45,10 +46,10 @@ __global__ void __launch_bounds__(1024) sort_count_kernel(SortArgs a)
     const int64_t s1 = s0 + a.segment < a.slots ? s0 + a.segment : a.slots;
 #pragma unroll 4
     for (int64_t s = s0 + threadIdx.x; s < s1; s += blockDim.x)
-        atomicAdd(&hist[sort_key(a.experts, (int)s, a.groups)], 1);
+        atomicAdd(&hist[sort_key(a.experts, s, a.groups)], 1);
     __syncthreads();
     for (int e = threadIdx.x; e < n; e += blockDim.x)
-        a.counts[(int64_t)blockIdx.x * n + e] = hist[e];
+        a.counts[(int64_t)e * a.pitch + blockIdx.x] = hist[e];
 }
 
 // One segment's slots to their rows.  A slot's row is the number of slots with a lower
@@ -60,24 +61,48 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(SortArgs a)
 {
     extern __shared__ int shared[];
     __shared__ int wave_sum[16];
-    const int n = a.groups + 1, waves = blockDim.x >> 6;
+    const int n = a.groups + 1, waves = blockDim.x >> 6, chunk = sort_chunk(waves);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int *base = shared;                                        // n: next row of each expert
-    int *total = shared + n;                                   // n, until the counters take its place
-    uint16_t *cnt = reinterpret_cast<uint16_t *>(shared + n);  // waves x n
-    for (int e = threadIdx.x; e < 2 * n; e += blockDim.x) shared[e] = 0;
-    __syncthreads();
+    int *base = shared;                                            // n: next row of each expert
+    int *total = shared + n;                                       // n
+    uint16_t *cnt = reinterpret_cast<uint16_t *>(shared + 2 * n);  // waves x n
+    uint16_t *own = cnt + wave * n;
     const int64_t s0 = (int64_t)blockIdx.x * a.segment;
     const int64_t s1 = s0 + a.segment < a.slots ? s0 + a.segment : a.slots;
+    int key[kSortItems], rank[kSortItems];
+    const auto load = [&](int64_t c0) {
+        const int64_t w0 = c0 + wave * (64 * kSortItems) + lane;
+#pragma unroll
+        for (int i = 0; i < kSortItems; ++i)
+            key[i] = w0 + i * 64 < s1 ? sort_key(a.experts, w0 + i * 64, a.groups) : n;
+    };
+    load(s0);
+    for (int e = threadIdx.x; e < 2 * n; e += blockDim.x) shared[e] = 0;
+    __syncthreads();
+    // All slots by expert, and those of earlier segments.  (One chunk counts itself below.)
+    const bool alone = a.slots <= chunk;
     if (a.counts) {
-        const int all = a.segments * n;
-        for (int i = threadIdx.x; i < all; i += blockDim.x) {
-            const int c = a.counts[i], segment = i / n, e = i - segment * n;
-            if (c == 0) continue;
-            atomicAdd(&total[e], c);
-            if (segment < (int)blockIdx.x) atomicAdd(&base[e], c);
+        // Some threads for each expert, 16 bytes of its counts at a time.
+        const int quads = a.pitch / 4;
+        const int share = (int)blockDim.x / n < 1 ? 1 : (int)blockDim.x / n;
+        const int part = threadIdx.x / n;
+        for (int e = threadIdx.x - part * n; e < n && part < share; e += blockDim.x) {
+            const i32x4 *c = reinterpret_cast<const i32x4 *>(a.counts + (int64_t)e * a.pitch);
+            int all = 0, earlier = 0;
+#pragma unroll 8
+            for (int q = part; q < quads; q += share) {
+                const i32x4 v = c[q];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int s = 4 * q + i;
+                    all += s < a.segments ? v[i] : 0;
+                    earlier += s < (int)blockIdx.x ? v[i] : 0;
+                }
+            }
+            atomicAdd(&total[e], all);
+            atomicAdd(&base[e], earlier);
         }
-    } else {
+    } else if (!alone) {
 #pragma unroll 4
         for (int s = threadIdx.x; s < a.slots; s += blockDim.x) {
             const int e = sort_key(a.experts, s, a.groups);
@@ -85,37 +110,10 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(SortArgs a)
             if (s < s0) atomicAdd(&base[e], 1);
         }
     }
-    __syncthreads();
-    // Rows before each expert: every thread sums `per` neighbouring experts.
-    const int per = (n + blockDim.x - 1) / blockDim.x, e0 = threadIdx.x * per;
-    int mine = 0;
-    for (int e = e0; e < e0 + per && e < n; ++e) mine += total[e];
-    int before = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int v = __shfl_up(before, d);
-        if (lane >= d) before += v;
-    }
-    if (lane == 63) wave_sum[wave] = before;
-    __syncthreads();
-    for (int w = 0; w < wave; ++w) before += wave_sum[w];
-    before -= mine;
-    for (int e = e0; e < e0 + per && e < n; ++e) {
-        if (blockIdx.x == 0) a.offsets[e] = before;
-        base[e] += before;
-        before += total[e];
-    }
     const int bits = 32 - __builtin_clz(n);  // n itself marks lanes without a slot
-    for (int64_t c0 = s0; c0 < s1; c0 += sort_chunk(waves)) {
-        __syncthreads();  // base is complete, total and the last chunk's counters are read
-        for (int e = threadIdx.x; e < waves * n; e += blockDim.x) cnt[e] = 0;
-        __syncthreads();
-        uint16_t *own = cnt + wave * n;
-        int key[kSortItems], rank[kSortItems];
-        const int64_t w0 = c0 + wave * (64 * kSortItems) + lane;
-#pragma unroll
-        for (int i = 0; i < kSortItems; ++i)
-            key[i] = w0 + i * 64 < s1 ? sort_key(a.experts, (int)(w0 + i * 64), a.groups) : n;
+    for (int64_t c0 = s0; c0 < s1 || c0 == s0; c0 += chunk) {
+        for (int e = lane; e < n; e += 64) own[e] = 0;
+        if (c0 > s0) load(c0);
 #pragma unroll
         for (int i = 0; i < kSortItems; ++i) {
             uint64_t same = ~0ull;
@@ -125,16 +123,14 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(SortArgs a)
             }
             const int lower = __popcll(same & ((1ull << lane) - 1));
             rank[i] = 0;
-            if (key[i] < n) {
-                rank[i] = *(volatile uint16_t *)(own + key[i]) + lower;
-            }
             __builtin_amdgcn_wave_barrier();  // a wave's reads and writes of LDS stay in order
+            if (key[i] < n) rank[i] = *(volatile uint16_t *)(own + key[i]) + lower;
+            __builtin_amdgcn_wave_barrier();
             if (key[i] < n && lower == 0)
                 *(volatile uint16_t *)(own + key[i]) = (uint16_t)(rank[i] + __popcll(same));
-            __builtin_amdgcn_wave_barrier();
         }
         __syncthreads();
-        // Counters to rows before each wave's, relative to the expert's next row.
+        // The waves' counts to rows before each wave's; a chunk that is all there is: the totals.
         for (int e = threadIdx.x; e < n; e += blockDim.x) {
             int sum = 0;
             for (int w = 0; w < waves; ++w) {
@@ -142,22 +138,46 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(SortArgs a)
                 cnt[w * n + e] = (uint16_t)sum;
                 sum += v;
             }
+            if (alone) total[e] = sum;
         }
         __syncthreads();
+        if (c0 == s0) {
+            // Rows before each expert: every thread sums `per` neighbouring experts.
+            const int per = (n + blockDim.x - 1) / blockDim.x, e0 = threadIdx.x * per;
+            int mine = 0;
+            for (int e = e0; e < e0 + per && e < n; ++e) mine += total[e];
+            int before = mine;
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const int v = __shfl_up(before, d);
+                if (lane >= d) before += v;
+            }
+            if (lane == 63) wave_sum[wave] = before;
+            __syncthreads();
+            for (int w = 0; w < wave; ++w) before += wave_sum[w];
+            before -= mine;
+            for (int e = e0; e < e0 + per && e < n; ++e) {
+                if (blockIdx.x == 0) a.offsets[e] = before;
+                base[e] += before;
+                before += total[e];
+            }
+            __syncthreads();
+        }
 #pragma unroll
         for (int i = 0; i < kSortItems; ++i) {
             if (key[i] >= n) continue;
-            const int slot = (int)(w0 + i * 64);
+            const int slot = (int)(c0 + wave * (64 * kSortItems) + i * 64 + lane);
             const int row = base[key[i]] + own[key[i]] + rank[i];
             a.place[slot] = key[i] < a.groups ? row : -2 - row;
             if (a.order) a.order[row] = slot;
         }
-        if (c0 + sort_chunk(waves) >= s1) break;
-        // The next chunk's rows follow: each expert's last wave knows how many there were.
+        if (c0 + chunk >= s1) break;
         __syncthreads();
+        // The next chunk's rows follow.
 #pragma unroll
         for (int i = 0; i < kSortItems; ++i)
             if (key[i] < n) atomicAdd(&base[key[i]], 1);
+        __syncthreads();
     }
 }
 

@@ -220,7 +220,7 @@ int sgemm_q4_quantize(int type, int N, int K, int block, const void *W, int ldw,
  *   order     slots ints: the slot of each row, those dropped last; or NULL
  *   place     slots ints: each slot's row r; -2 - r where it is dropped (r is then one of
  *             the rows from offsets[groups] on, which no expert has)
- *   ws, ws_bytes   workspace, 4-byte aligned, of at least
+ *   ws, ws_bytes   workspace, 16-byte aligned, of at least
  *             sgemm_expert_sort_workspace(slots, groups) bytes (NULL where that is 0)
  * Returns -1 slots, -2 groups, -3 experts (NULL with slots, or not 8-byte aligned), -4
  * offsets (NULL or not 4-byte aligned), -5 order, -6 place, -7 ws, -8 ws_bytes too small.

@@ -40,7 +40,7 @@ def call(fn, kw):
     ("sgemm_expert_sort", dict(offsets=0), -4), ("sgemm_expert_sort", dict(offsets=2), -4),
     ("sgemm_expert_sort", dict(order=2), -5), ("sgemm_expert_sort", dict(place=0), -6),
     ("sgemm_expert_sort", dict(place=1), -6), ("sgemm_expert_sort", dict(slots=100000), -7),
-    ("sgemm_expert_sort", dict(ws=2), -7), ("sgemm_expert_sort", dict(slots=100000, ws=4096), -8),
+    ("sgemm_expert_sort", dict(ws=8), -7), ("sgemm_expert_sort", dict(slots=100000, ws=4096), -8),
     ("sgemm_expert_gather", dict(type=2), -1), ("sgemm_expert_gather", dict(tokens=-1), -2),
     ("sgemm_expert_gather", dict(k=-1), -3), ("sgemm_expert_gather", dict(k=MOST // 8 + 1), -3),
     ("sgemm_expert_gather", dict(H=-1), -4), ("sgemm_expert_gather", dict(X=0), -5),
@@ -124,8 +124,8 @@ def test_valid_arguments_reach_the_device(fn):
 def test_sort_workspace():
     size = sg.sgemm_expert_sort_workspace
     assert size(-1, 1) == -1 and size(MOST + 1, 1) == -1 and size(1, -1) == -2 and size(1, 4097) == -2
-    assert size(0, 0) == 0 and size(4096, 64) == 0  # one workgroup's chunk needs none
-    assert size(4097, 64) == 2 * 65 * 4
+    assert size(0, 0) == 0 and size(16384, 64) == 0  # one launch needs none
+    assert size(16385, 64) == 12 * 65 * 4  # nine chunks of 2048, rounded up to four
     assert size(MOST, 4096) == 256 * 4097 * 4  # never more than 256 segments
 
 

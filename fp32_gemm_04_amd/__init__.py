@@ -113,8 +113,8 @@ for _name, _args in {
         "sgemm_expert_combine": [_i] * 5 + [_p, _i, _p, _p, _f, _p, _i, _p],
         "sgemm_expert_combine_backward": [_i] * 5 + [_p, _i, _p, _i, _p, _p, _p, _i, _i, _p, _p],
         "sgemm_q8_quantize": [_i] * 3 + [_p, _i, _i, _p, _i, _p, _i, _p, _p],
-        "sgemm_q8_gemm": [_i] * 5 + [_p, _i, _p, _p, _i, _i64, _p, _p, _i, _p, _p],
-        "sgemm_q8_matvec": [_i] * 5 + [_p, _i, _p, _i, _i64, _p, _p, _i, _p, _p],
+        "sgemm_q8_gemm": [_i] * 5 + [_p, _i, _p, _p, _i, _i64, _p, _p, _i, _p, _i, _p],
+        "sgemm_q8_matvec": [_i] * 5 + [_p, _i, _p, _i, _i64, _p, _p, _i, _p, _i, _p],
 }.items():
     getattr(_lib, _name).restype = ctypes.c_int
     getattr(_lib, _name).argtypes = _args
@@ -406,17 +406,17 @@ def sgemm_q8_quantize(type, rows, K, X, ldx, k, place, out_rows, Q, ldq, scales,
 
 
 def sgemm_q8_gemm(type, groups, rows, N, K, X, ldx, x_scales, W, ldw, stride_w, w_scales, Y, ldy,
-                  offsets, stream=0) -> int:
+                  offsets, fill, stream=0) -> int:
     """C ABI ``sgemm_q8_gemm``.  Returns the status."""
     return _lib.sgemm_q8_gemm(type, groups, rows, N, K, X, ldx, x_scales, W, ldw, stride_w, w_scales,
-                              Y, ldy, offsets, stream)
+                              Y, ldy, offsets, fill, stream)
 
 
 def sgemm_q8_matvec(type, groups, rows, N, K, X, ldx, W, ldw, stride_w, w_scales, Y, ldy, offsets,
-                    stream=0) -> int:
+                    fill, stream=0) -> int:
     """C ABI ``sgemm_q8_matvec``.  Returns the status."""
     return _lib.sgemm_q8_matvec(type, groups, rows, N, K, X, ldx, W, ldw, stride_w, w_scales, Y, ldy,
-                                offsets, stream)
+                                offsets, fill, stream)
 
 
 _TYPES = {torch.float32: SGEMM_TYPE_F32, torch.bfloat16: SGEMM_TYPE_BF16}
@@ -927,40 +927,57 @@ def q8_gemm(X, x_scales, Q, scales, offsets=None, Y=None, dtype=torch.bfloat16, 
     t = _TYPES.get(dtype)
     if t is None:
         raise TypeError("Y must be float32 or bfloat16, not %s" % dtype)
-    ldy = _operand(Y, "Y", dtype, dev, 2, rows, N) if Y is not None else max(1, N)
+    fill = Y is None
+    ldy = max(1, N) if fill else _operand(Y, "Y", dtype, dev, 2, rows, N)
 
     def body(s):
         nonlocal Y
         if Y is None:
-            Y = (X.new_empty if offsets is None else X.new_zeros)((rows, N), dtype=dtype)
+            Y = X.new_empty((rows, N), dtype=dtype)
         return _lib.sgemm_q8_gemm(t, groups, rows, N, K, X.data_ptr(), ldx, sx, Q.data_ptr(), ldw,
                                   _groups_of(Q) if offsets is not None else 0, ps, Y.data_ptr(), ldy,
-                                  off, s)
+                                  off, fill, s)
     _run("sgemm_q8_gemm", dev, stream, (X, x_scales, Q, scales, Y, offsets), body)
     return Y
 
 
-def q8_matvec(X, Q, scales, Y=None, offsets=None, stream=None):
-    """Y <- ``q8_gemm(*q8_quantize(X), Q, scales)`` in one launch, for a few rows of X
-    (``sgemm_q8_matvec``), bit for bit.
+# Values of X up to which every workgroup quantises them for itself.  us, that and two launches:
+# 4 rows, 4096 x 4096 8.8 and 10.1, 8 rows 10.8 and 10.9, 16 rows 14.8 and 12.3, 12 rows, 8192 x
+# 28001 60.5 and 53.0.
+_MOST_MATVEC = 32768
 
-    X: (rows, K), float32 or bfloat16, K at most 106496; Q and scales as in ``q8_gemm``; Y:
-    (rows, N) of X's type, allocated when None (as zeros with ``offsets``).  One pass over the weights serves
-    up to 16 rows.  Returns Y.
+
+def q8_matvec(X, Q, scales, Y=None, offsets=None, stream=None):
+    """Y <- ``q8_gemm(*q8_quantize(X), Q, scales)``, bit for bit, for a few rows of X: with at most
+    32768 values of X in one launch (``sgemm_q8_matvec``), with more in those two.
+
+    X: (rows, K), float32 or bfloat16, K at most 131071; Q and scales as in ``q8_gemm``; Y:
+    (rows, N) of X's type, allocated when None (its rows outside every group zero).  Returns Y.
     """
     t = _type_of(X, "X")
     dev = X.device
     ldx = _operand(X, "X", X.dtype, dev)
     rows, K = X.shape
     groups, N, ldw, off, ps = _q8_weights(Q, scales, offsets, dev, K)
-    ldy = _operand(Y, "Y", X.dtype, dev, 2, rows, N) if Y is not None else max(1, N)
+    if K > 131071:
+        raise SgemmError(-5, "sgemm_q8_matvec")
+    fill = Y is None
+    ldy = max(1, N) if fill else _operand(Y, "Y", X.dtype, dev, 2, rows, N)
 
     def body(s):
         nonlocal Y
         if Y is None:
-            Y = (X.new_empty if offsets is None else X.new_zeros)(rows, N)
+            Y = X.new_empty(rows, N)
+        stride = _groups_of(Q) if offsets is not None else 0
+        if rows * K > _MOST_MATVEC:
+            ldq = -(-K // 16) * 16
+            ws = X.new_empty(rows * (ldq + 4), dtype=torch.uint8)
+            q = ws.data_ptr()
+            return (_lib.sgemm_q8_quantize(t, rows, K, X.data_ptr(), ldx, 0, 0, rows, q, ldq,
+                                           q + rows * ldq, s)
+                    or _lib.sgemm_q8_gemm(t, groups, rows, N, K, q, ldq, q + rows * ldq, Q.data_ptr(),
+                                          ldw, stride, ps, Y.data_ptr(), ldy, off, fill, s))
         return _lib.sgemm_q8_matvec(t, groups, rows, N, K, X.data_ptr(), ldx, Q.data_ptr(), ldw,
-                                    _groups_of(Q) if offsets is not None else 0, ps, Y.data_ptr(),
-                                    ldy, off, s)
+                                    stride, ps, Y.data_ptr(), ldy, off, fill, s)
     _run("sgemm_q8_matvec", dev, stream, (X, Q, scales, Y, offsets), body)
     return Y

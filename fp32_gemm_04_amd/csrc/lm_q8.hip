@@ -26,6 +26,40 @@ bool q8_fast(const void *p, int64_t ld, int64_t group_stride)
     return aligned(p, 4) && ld % 4 == 0 && group_stride % 4 == 0 && ld < ((int64_t)1 << 22);
 }
 
+template <typename T, bool PLACED> auto quantize_of(int waves)
+{
+    return waves == 1   ? q8_quantize_kernel<T, 1, PLACED>
+           : waves == 2 ? q8_quantize_kernel<T, 2, PLACED>
+                        : q8_quantize_kernel<T, 4, PLACED>;
+}
+
+// A product of few rows: X is int8 with scales, or of the results' type.
+int vec_product(VecArgs &a, bool bytes, bool bf16_out, int cus, hipStream_t stream)
+{
+    a.slabs = (int)ceil_div(a.K, 128);
+    a.pass = a.rows < 16 ? a.rows : 16;
+    if (a.slabs > 0 && a.pass > kVecRows / 128 / a.slabs) a.pass = kVecRows / 128 / a.slabs;
+    const bool fast = a.K == 0 || q8_fast(a.W, a.ldw, a.stride_w);
+    const int depth = vec_lds(a.pass, a.slabs, 4) <= 160 * 1024 ? 4 : 2;
+    const int lds = vec_lds(a.pass, a.slabs, depth);
+    const auto fn = [&](auto four, auto two, auto slow) { return !fast ? slow : depth == 4 ? four : two; };
+    const auto of = [&](auto x, auto y) -> VecFn {
+        typedef decltype(x) TX;
+        typedef decltype(y) TY;
+        return fn(q8_vec_kernel<TX, TY, 4, true>, q8_vec_kernel<TX, TY, 2, true>,
+                  q8_vec_kernel<TX, TY, 2, false>);
+    };
+    const VecFn kernel = bytes ? (bf16_out ? of(int8_t(), bf16()) : of(int8_t(), float()))
+                         : bf16_out ? of(bf16(), bf16())
+                                    : of(float(), float());
+    // Two workgroups a unit where LDS has room, each with its share of the tiles.
+    const int64_t tiles = ceil_div(a.N, 16), used = a.groups < 1 ? 1 : a.groups < a.rows ? a.groups : a.rows;
+    const int64_t room = (int64_t)cus * (160 * 1024 / lds < 2 ? 1 : 2) / used;
+    const int64_t blocks = room < 1 ? 1 : room < tiles ? room : tiles;
+    kernel<<<dim3((unsigned)blocks, (unsigned)(a.groups < 1 ? 1 : a.groups)), dim3(kVecWaves * 64), lds, stream>>>(a);
+    return (int)hipGetLastError();
+}
+
 }  // namespace
 }  // namespace lm
 }  // namespace sgemm
@@ -38,7 +72,7 @@ extern "C" int sgemm_q8_quantize(int type, int rows, int K, const void *X, int l
 {
     if (type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16) return -1;
     if (rows < 0 || rows > kMostExtent) return -2;
-    if (K < 0 || K > kMostExtent) return -3;
+    if (K < 0 || K > kMostQ8) return -3;
     const int size = type == SGEMM_TYPE_BF16 ? 2 : 4, least = K > 1 ? K : 1;
     const bool work = rows > 0 && out_rows > 0 && (!place || k > 0);
     if ((work && K > 0 && !X) || !aligned(X, size)) return -4;
@@ -54,26 +88,24 @@ extern "C" int sgemm_q8_quantize(int type, int rows, int K, const void *X, int l
     a.X = X, a.Q = Q, a.scales = scales, a.place = place;
     a.ldx = ldx, a.ldq = ldq;
     a.rows = rows, a.K = K, a.k = k, a.out_rows = out_rows;
-    // As many waves a row as its first values keep busy.
-    const int waves = K <= 1024 ? 1 : K <= 2048 ? 2 : 4;
-    const auto fn = [&](auto one, auto two, auto four) {
-        return waves == 1 ? one : waves == 2 ? two : four;
-    };
+    const int64_t pieces = ceil_div(K, 16 / size);
+    // As few waves a row as hold it in registers, but more where they would not fill the units.
+    int waves = pieces <= 64 * kHeld ? 1 : pieces <= 128 * kHeld ? 2 : 4;
+    // us: 8192 rows of 2048 bf16 11.5 with one, 11.7 with two; 64 rows of 4096 3.6 with four, 7 with two.
+    while (waves < 4 && (int64_t)rows * waves < 4096 && pieces > 64 * waves) waves *= 2;
     const int64_t blocks = ceil_div(rows, 4 / waves);
     const dim3 grid((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks));
-    if (type == SGEMM_TYPE_BF16)
-        fn(q8_quantize_kernel<bf16, 1>, q8_quantize_kernel<bf16, 2>,
-           q8_quantize_kernel<bf16, 4>)<<<grid, dim3(256), 0, stream>>>(a);
-    else
-        fn(q8_quantize_kernel<float, 1>, q8_quantize_kernel<float, 2>,
-           q8_quantize_kernel<float, 4>)<<<grid, dim3(256), 0, stream>>>(a);
+    const auto fn = type == SGEMM_TYPE_BF16
+                        ? (place ? quantize_of<bf16, true>(waves) : quantize_of<bf16, false>(waves))
+                        : (place ? quantize_of<float, true>(waves) : quantize_of<float, false>(waves));
+    fn<<<grid, dim3(256), 0, stream>>>(a);
     return (int)hipGetLastError();
 }
 
 extern "C" int sgemm_q8_gemm(int type, int groups, int rows, int N, int K, const int8_t *X, int ldx,
                              const float *x_scales, const int8_t *W, int ldw, int64_t stride_w,
                              const float *w_scales, void *Y, int ldy, const int *offsets,
-                             hipStream_t stream)
+                             int fill, hipStream_t stream)
 {
     if (type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16) return -1;
     if (groups < 0 || (!offsets && groups != 1)) return -2;
@@ -81,28 +113,39 @@ extern "C" int sgemm_q8_gemm(int type, int groups, int rows, int N, int K, const
     if (N < 0 || N > kMostExtent) return -4;
     if (K < 0 || K > kMostQ8) return -5;
     const int size = type == SGEMM_TYPE_BF16 ? 2 : 4, least = K > 1 ? K : 1;
-    const bool work = groups > 0 && rows > 0 && N > 0, reads = work && K > 0;
+    const bool work = (groups > 0 || fill) && rows > 0 && N > 0, reads = work && groups > 0 && K > 0;
     if (reads && !X) return -6;
     if (ldx < least) return -7;
-    if ((work && !x_scales) || !aligned(x_scales, 4)) return -8;
+    if ((work && groups > 0 && !x_scales) || !aligned(x_scales, 4)) return -8;
     if (reads && !W) return -9;
     if (ldw < least) return -10;
     if (stride_w < 0) return -11;
-    if ((work && !w_scales) || !aligned(w_scales, 4)) return -12;
+    if ((work && groups > 0 && !w_scales) || !aligned(w_scales, 4)) return -12;
     if ((work && !Y) || !aligned(Y, size)) return -13;
     if (ldy < (N > 1 ? N : 1)) return -14;
     if (!aligned(offsets, 4)) return -15;
+    if (fill != 0 && fill != 1) return -16;
     if (!work) return 0;
-    const int used = groups < rows ? groups : rows;  // groups with rows, at most
+    const int used = groups < 1 ? 1 : groups < rows ? groups : rows;  // groups with rows, at most
     if ((rows + (int64_t)used * 15) / 16 * ceil_div(N, 64) > INT_MAX) return -4;
 
     int rc = 0;
     const int cus = compute_units(&rc);
     if (cus == 0) return rc;
-    const bool fast = K == 0 || (q8_fast(X, ldx, 0) && q8_fast(W, ldw, stride_w));
     const bool bf16_out = type == SGEMM_TYPE_BF16;
-    const int tile = offsets ? rows_tile(1, fast, used, rows, N, ceil_div(K, 2), cus)
-                             : plain_tile(1, F_ROWS_T, fast, rows, N, ceil_div(K, 2), cus);
+    // Few rows: every workgroup streams weights.  us, this and the smallest tile: 16 rows, 4096 x
+    // 4096 9.1 and 13.0, 12 rows, 8192 x 28001 48.5 and 51.2, 16 rows, 4096 x 14336 17.9 and 16.1, 24 rows
+    // 4096 x 4096 13.2 and 13.2; 3 rows a group, 64 groups of 2048 x 1408 33.8 and 37.9, 8 rows, 32
+    // groups of 2048 x 1536 34.5 and 26.2.
+    if (K <= kVecRows && groups <= 65535 && rows <= (offsets ? 4 * (int64_t)used : 16)) {
+        VecArgs v = {};
+        v.X = X, v.x_scales = x_scales, v.W = W, v.w_scales = w_scales, v.Y = Y, v.offsets = offsets;
+        v.ldx = ldx, v.ldw = ldw, v.stride_w = stride_w, v.ldy = ldy;
+        v.rows = rows, v.N = N, v.K = K, v.groups = groups, v.fill = offsets && fill;
+        return vec_product(v, true, bf16_out, cus, stream);
+    }
+    const bool fast = K == 0 || (q8_fast(X, ldx, 0) && q8_fast(W, ldw, stride_w));
+    const int tile = byte_rows_tile(fast, offsets ? used : 0, rows, N, K, cus);
     const TileKernel k = i8_kernel(bf16_out, offsets != nullptr, tile, fast);
     TileArgs a = {};
     a.A = X, a.B = W, a.C = Y;
@@ -111,15 +154,12 @@ extern "C" int sgemm_q8_gemm(int type, int groups, int rows, int N, int K, const
     a.M = rows, a.N = N, a.K = K;
     a.a_cols = a.b_cols = K;
     a.scale_a = x_scales, a.scale_b = w_scales;
-    // How wide the stores to Y may be.
-    for (int v = 2; v > 0; --v)
-        if (!a.vec_c && aligned(Y, 4 * v * size) && ldy % (4 * v) == 0) a.vec_c = v;
     int64_t most = ceil_div(rows, k.bm);
     if (offsets) {  // every group's last tile may be part full
         most = (rows + (int64_t)used * (k.bm - 1)) / k.bm;
-        a.groups = groups, a.offsets = offsets, a.most_tiles = (int)most;
+        a.groups = groups, a.offsets = offsets, a.most_tiles = (int)most, a.fill = fill;
     }
-    const int64_t blocks = most * ceil_div(N, k.bn);
+    const int64_t blocks = most > 0 ? most * ceil_div(N, k.bn) : 1;
     if (blocks > kMostBlocks) return (int)hipErrorInvalidConfiguration;
     k.fn<<<dim3((unsigned)blocks), dim3(k.threads), 0, stream>>>(a);
     return (int)hipGetLastError();
@@ -127,7 +167,7 @@ extern "C" int sgemm_q8_gemm(int type, int groups, int rows, int N, int K, const
 
 extern "C" int sgemm_q8_matvec(int type, int groups, int rows, int N, int K, const void *X, int ldx,
                                const int8_t *W, int ldw, int64_t stride_w, const float *w_scales,
-                               void *Y, int ldy, const int *offsets, hipStream_t stream)
+                               void *Y, int ldy, const int *offsets, int fill, hipStream_t stream)
 {
     if (type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16) return -1;
     if (groups < 0 || (!offsets && groups != 1) || groups > 65535) return -2;
@@ -135,16 +175,17 @@ extern "C" int sgemm_q8_matvec(int type, int groups, int rows, int N, int K, con
     if (N < 0 || N > kMostExtent) return -4;
     if (K < 0 || K > kVecRows) return -5;
     const int size = type == SGEMM_TYPE_BF16 ? 2 : 4, least = K > 1 ? K : 1;
-    const bool work = groups > 0 && rows > 0 && N > 0, reads = work && K > 0;
+    const bool work = (groups > 0 || fill) && rows > 0 && N > 0, reads = work && groups > 0 && K > 0;
     if ((reads && !X) || !aligned(X, size)) return -6;
     if (ldx < least) return -7;
     if (reads && !W) return -8;
     if (ldw < least) return -9;
     if (stride_w < 0) return -10;
-    if ((work && !w_scales) || !aligned(w_scales, 4)) return -11;
+    if ((work && groups > 0 && !w_scales) || !aligned(w_scales, 4)) return -11;
     if ((work && !Y) || !aligned(Y, size)) return -12;
     if (ldy < (N > 1 ? N : 1)) return -13;
     if (!aligned(offsets, 4)) return -14;
+    if (fill != 0 && fill != 1) return -15;
     if (!work) return 0;
 
     int rc = 0;
@@ -153,22 +194,6 @@ extern "C" int sgemm_q8_matvec(int type, int groups, int rows, int N, int K, con
     VecArgs a = {};
     a.X = X, a.W = W, a.w_scales = w_scales, a.Y = Y, a.offsets = offsets;
     a.ldx = ldx, a.ldw = ldw, a.stride_w = stride_w, a.ldy = ldy;
-    a.rows = rows, a.N = N, a.K = K;
-    a.slabs = (int)ceil_div(K, 128);
-    a.pass = rows < 16 ? rows : 16;
-    if (a.slabs > 0 && a.pass > kVecRows / 128 / a.slabs) a.pass = kVecRows / 128 / a.slabs;
-    const bool fast = K == 0 || q8_fast(W, ldw, stride_w);
-    const int depth = vec_lds(a.pass, a.slabs, 4) <= 160 * 1024 ? 4 : 2;
-    const int lds = vec_lds(a.pass, a.slabs, depth);
-    const auto fn = [&](auto four, auto two, auto slow) { return !fast ? slow : depth == 4 ? four : two; };
-    const VecFn kernel =
-        type == SGEMM_TYPE_BF16
-            ? fn(q8_vec_kernel<bf16, 4, true>, q8_vec_kernel<bf16, 2, true>, q8_vec_kernel<bf16, 2, false>)
-            : fn(q8_vec_kernel<float, 4, true>, q8_vec_kernel<float, 2, true>, q8_vec_kernel<float, 2, false>);
-    // Two workgroups a unit where LDS has room, each with its share of the tiles.
-    const int64_t tiles = ceil_div(N, 16), used = groups < rows ? groups : rows;
-    const int64_t room = (int64_t)cus * (160 * 1024 / lds < 2 ? 1 : 2) / used;
-    const int64_t blocks = room < 1 ? 1 : room < tiles ? room : tiles;
-    kernel<<<dim3((unsigned)blocks, (unsigned)groups), dim3(kVecWaves * 64), lds, stream>>>(a);
-    return (int)hipGetLastError();
+    a.rows = rows, a.N = N, a.K = K, a.groups = groups, a.fill = offsets && fill;
+    return vec_product(a, false, type == SGEMM_TYPE_BF16, cus, stream);
 }

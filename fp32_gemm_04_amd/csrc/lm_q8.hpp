@@ -1,16 +1,24 @@
 // Rows in 8-bit integers, and products of a few such rows with 8-bit weights (include/slm.h).
 //
 // Quantisation.  scale = m / 127 with m the row's largest magnitude; q is x / scale
-// rounded to the nearest integer, ties to even, of the exact quotient: rint(x * (1 / scale)) is
-// at most one off, the remainder x - q scale is exact in one fma (it is a multiple of
-// the smaller operand's last bit, below 2 scale), and comparing twice its size
-// with scale says whether, and to which side, q moves.
+// rounded to the nearest integer, ties to even, of the exact quotient.  One fma with the
+// reciprocal of scale and 1.5 * 2^23 rounds x / scale to an integer, in the last bits of its
+// result, and a second gives how far from it the quotient was.  The reciprocal's rounding moves
+// the quotient by less than 2^-17 (127 * 2^-24), so only where that distance is within 2^-16 of
+// a half may q be one off (values of a wave: some 3% of the time); there the
+// remainder x - q scale, exact in one fma (a multiple of the smaller operand's last bit, below
+// 2 scale), is compared with half of scale.
 #pragma once
 
 #include "lm_tile.hpp"
 
 namespace sgemm {
 namespace lm {
+
+__device__ __forceinline__ uint32_t magnitude(float x)
+{
+    return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
+}
 
 // What a row's values are divided by, scaled by a power of two so that its reciprocal is
 // finite and normal where the scale is tiny.
@@ -27,70 +35,89 @@ struct Quantum {
         inverse = step > 0.f ? 1.f / step : 0.f;
         if (m >= 0x7f800000u) {
             scale = __builtin_nanf("");
-            by = inverse = step = 0.f;
+            step = inverse = 0.f;
         }
     }
-    __device__ __forceinline__ int of(float x) const
+    // One value, whatever the scale; without branches.
+    __device__ __forceinline__ int exact(float x) const
     {
-        if (!(inverse > 0.f)) return 0;
-        const float v = x * by;
-        float q = rintf(v * inverse);
+        const float v = x * by, q = rintf(v * inverse);
         const float left = fmaf(-q, step, v), twice = 2.f * fabsf(left);
+        int i = inverse > 0.f ? (int)q : 0;
         // On a tie the even neighbour stays.
-        if (twice > step || (twice == step && ((int)q & 1))) q += left > 0.f ? 1.f : -1.f;
-        const int i = (int)q;
-        return i > 127 ? 127 : i < -127 ? -127 : i;
+        const bool move = twice > step || (twice == step && (i & 1));
+        i += move ? (left > 0.f ? 1 : -1) : 0;
+        i = i > 127 ? 127 : i < -127 ? -127 : i;
+        return inverse > 0.f ? i : 0;
+    }
+    // N values (a multiple of 4) as bytes, the first in the lowest.
+    template <int N> __device__ __forceinline__ void bytes(const float (&x)[N], uint32_t (&q)[N / 4]) const
+    {
+        constexpr float kWhole = 12582912.f;  // 1.5 * 2^23
+        float far = 0.f;
+#pragma unroll
+        for (int w = 0; w < N / 4; ++w) {
+            uint32_t u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float v = x[4 * w + i], whole = fmaf(v, inverse, kWhole);
+                far = fmaxf(far, fabsf(fmaf(v, inverse, kWhole - whole)));
+                u[i] = __builtin_bit_cast(uint32_t, whole);
+            }
+            // The low byte of each.
+            q[w] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(u[3], u[2], 0x0c0c0400u),
+                                         __builtin_amdgcn_perm(u[1], u[0], 0x0c0c0400u), 0x05040100u);
+        }
+        if (by != 1.f || !(inverse > 0.f) || far > 0.5f - 0x1p-16f) {
+#pragma unroll
+            for (int w = 0; w < N / 4; ++w) {
+                q[w] = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[w] |= ((uint32_t)exact(x[4 * w + i]) & 0xffu) << (8 * i);
+            }
+        }
     }
 };
 
-__device__ __forceinline__ uint32_t magnitude(float x)
-{
-    return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
-}
-
+// The wave's largest value: within rows of 16 lanes, then from row to row; lane 63 has it.
 __device__ __forceinline__ uint32_t wave_max(uint32_t v)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const uint32_t u = __shfl_xor(v, d);
+    const auto join = [&](auto ctrl, auto rows) {
+        const uint32_t u = __builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value,
+                                                       decltype(rows)::value, 0xf, false);
         v = u > v ? u : v;
-    }
-    return v;
+    };
+    typedef std::integral_constant<int, 0xf> All;
+    join(std::integral_constant<int, 0x111>{}, All{});                               // from the lane below
+    join(std::integral_constant<int, 0x112>{}, All{});                               // two below
+    join(std::integral_constant<int, 0x114>{}, All{});                               // four
+    join(std::integral_constant<int, 0x118>{}, All{});                               // eight
+    join(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xa>{});  // rows 0, 2 to 1, 3
+    join(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});  // row 1 to 2, 3
+    return __builtin_amdgcn_readlane(v, 63);
 }
 
-// Sixteen values of a row from k on as fp32, zeros from K on.
-template <typename T>
-__device__ __forceinline__ void load16(const T *row, int k, int K, float (&v)[16])
+// N values of a row from k on as fp32, zeros from K on.
+template <int N, typename T>
+__device__ __forceinline__ void load_values(const T *row, int k, int K, float (&v)[N])
 {
-    if (k + 16 <= K) {
-        T x[16];
-        __builtin_memcpy(x, row + k, sizeof(x));
+    if (k + N <= K) {
+        typedef T Vec __attribute__((ext_vector_type(N)));
+        typedef Vec Loose __attribute__((aligned(sizeof(T))));
+        const Vec x = *reinterpret_cast<const Loose *>(row + k);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = (float)x[i];
+        for (int i = 0; i < N; ++i) v[i] = (float)x[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = k + i < K ? (float)row[k + i] : 0.f;
+        for (int i = 0; i < N; ++i) v[i] = k + i < K ? (float)row[k + i] : 0.f;
     }
 }
 
-__device__ __forceinline__ uint32_t max16(const float (&v)[16], uint32_t m)
+template <int N> __device__ __forceinline__ uint32_t max_of(const float (&v)[N], uint32_t m)
 {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = magnitude(v[i]) > m ? magnitude(v[i]) : m;
+    for (int i = 0; i < N; ++i) m = magnitude(v[i]) > m ? magnitude(v[i]) : m;
     return m;
-}
-
-__device__ __forceinline__ u32x4 quantize16(const float (&v)[16], const Quantum &s)
-{
-    u32x4 q;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        uint32_t u = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) u |= ((uint32_t)s.of(v[4 * w + i]) & 0xffu) << (8 * i);
-        q[w] = u;
-    }
-    return q;
 }
 
 struct QuantArgs {
@@ -102,29 +129,71 @@ struct QuantArgs {
     int rows, K, k, out_rows;
 };
 
-// WAVES waves share a row of X; each lane keeps its first 16 values, and reads what follows again.
-template <typename T, int WAVES>
+// WAVES waves share a row of X, 16 bytes a lane at a time; each lane keeps its first kHeld pieces,
+// and reads what follows again.  All loads of the kept pieces are in flight at once: none is
+// behind a branch, since a piece that would end past the row is moved back to end with it (its
+// values meet another piece's, and so do the bytes that both write).
+constexpr int kHeld = 4;
+
+template <typename T, int WAVES, bool PLACED>
 __global__ void __launch_bounds__(256) q8_quantize_kernel(QuantArgs a)
 {
-    constexpr int ROWS = 4 / WAVES;
+    constexpr int ROWS = 4 / WAVES, E = 16 / sizeof(T), step = WAVES * 64 * E;
+    typedef T Vec __attribute__((ext_vector_type(E)));
+    typedef Vec Loose __attribute__((aligned(sizeof(T))));
+    // Magnitudes order like their bits, as integers of the value's size.
+    typedef typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type U;
+    typedef U Bits __attribute__((ext_vector_type(E)));
     __shared__ uint32_t part[4];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int k0 = ((wave % WAVES) * 64 + lane) * E;
     for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.rows; r0 += (int64_t)gridDim.x * ROWS) {
         const int64_t r = r0 + wave / WAVES;
         const bool here = r < a.rows;
-        const T *row = static_cast<const T *>(a.X) + r * a.ldx;
-        const int k0 = ((wave % WAVES) * 64 + lane) * 16, step = WAVES * 64 * 16;
-        float first[16], v[16];
-        uint32_t m = 0;
-        if (here) {
-            load16(row, k0, a.K, first);
-            m = max16(first, m);
-            for (int k = k0 + step; k < a.K; k += step) {
-                load16(row, k, a.K, v);
-                m = max16(v, m);
+        const T *row = static_cast<const T *>(a.X) + (here ? r : a.rows - 1) * a.ldx;
+        // f(row of Q, whether it is a dropped choice's) for every row that this one goes to.
+        const auto each_row = [&](auto f) {
+            if constexpr (!PLACED) {
+                f(r, false);
+            } else {
+                for (int j = 0; j < a.k; ++j) {
+                    const int p = read<true>(a.place, r * a.k + j), out = p <= -2 ? -2 - p : p;
+                    if ((uint32_t)out < (uint32_t)a.out_rows) f((int64_t)out, p <= -2);
+                }
             }
+        };
+        const auto put_scale = [&](float scale) {
+            if (wave % WAVES == 0 && lane == 0)
+                each_row([&](int64_t out, bool dropped) { a.scales[out] = dropped ? 0.f : scale; });
+        };
+        if (a.K < E) {  // no whole piece (one wave a row)
+            const float x = lane < a.K ? (float)row[lane] : 0.f;
+            const Quantum s(wave_max(magnitude(x)));
+            if (!here) continue;
+            each_row([&](int64_t out, bool dropped) {
+                if (lane < a.K) a.Q[out * a.ldq + lane] = dropped ? 0 : (int8_t)s.exact(x);
+            });
+            put_scale(s.scale);
+            continue;
         }
-        m = wave_max(m);
+        const auto start = [&](int k) { return k + E <= a.K ? k : a.K - E; };
+        const auto load = [&](int k) { return (Vec) * reinterpret_cast<const Loose *>(row + start(k)); };
+        Bits top = 0;
+        const auto max_in = [&](Vec x) {
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(Bits, x) & (U)((U)~(U)0 >> 1));
+        };
+        // (A row past the last reads the last, and a lane past the row's end its last piece.)
+        Vec held[kHeld];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) held[i] = load(k0 + i * step);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) max_in(held[i]);
+        for (int k = k0 + kHeld * step; k < a.K; k += step) max_in(load(k));
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < E; ++i) m = top[i] > m ? top[i] : m;
+        m = wave_max(m << (32 - 8 * sizeof(T)));
         if constexpr (WAVES > 1) {
             if (lane == 0) part[wave] = m;
             __syncthreads();
@@ -137,38 +206,35 @@ __global__ void __launch_bounds__(256) q8_quantize_kernel(QuantArgs a)
         }
         if (!here) continue;
         const Quantum s(m);
-        const int copies = a.place ? a.k : 1;
-        for (int k = k0; k < a.K || k == k0; k += step) {
-            if (k != k0) load16(row, k, a.K, v);
-            const u32x4 q = k < a.K ? quantize16(k == k0 ? first : v, s) : u32x4{0, 0, 0, 0};
-            for (int j = 0; j < copies; ++j) {
-                int64_t to = r;
-                bool unused = false;
-                if (a.place) {
-                    const int p = a.place[r * a.k + j];
-                    unused = p <= -2;
-                    to = unused ? -2 - p : p;
-                    if (to < 0 || to >= a.out_rows) continue;
-                }
-                const u32x4 out = unused ? u32x4{0, 0, 0, 0} : q;
-                int8_t *d = a.Q + to * a.ldq + k;
-                if (k + 16 <= a.K) {
-                    __builtin_memcpy(d, &out, 16);
-                } else {
+        const auto put = [&](Vec x, int k) {
+            if (k >= a.K) return;
+            float v[E];
+            uint32_t q[E / 4];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (k + i < a.K) d[i] = (int8_t)(out[i / 4] >> (8 * (i % 4)));
-                }
-                if (k0 == 0 && k == 0) a.scales[to] = unused ? 0.f : s.scale;
-            }
+            for (int i = 0; i < E; ++i) v[i] = (float)x[i];
+            s.bytes(v, q);
+            each_row([&](int64_t out, bool dropped) {
+                uint32_t z[E / 4];
+#pragma unroll
+                for (int w = 0; w < E / 4; ++w) z[w] = dropped ? 0 : q[w];
+                __builtin_memcpy(a.Q + out * a.ldq + start(k), z, E);
+            });
+        };
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            __builtin_amdgcn_sched_barrier(0);  // one piece at a time: fewer registers
+            if (i * step < a.K) put(held[i], k0 + i * step);
         }
+        for (int k = k0 + kHeld * step; k < a.K; k += step) put(load(k), k);
+        put_scale(s.scale);
     }
 }
 
 // ------------------------------------------------------------- a few rows
 
 // Y[r][n] for a few rows: every weight is used once a row, so the time is that of reading the
-// weights.  A workgroup of eight waves quantises its rows into LDS once, then takes tiles of 16
+// weights.  A workgroup of eight waves puts its rows into LDS once, quantising them where TX is
+// not int8, then takes tiles of 16
 // columns; the waves split the contraction, slab by slab of 128 bytes, and their integer sums
 // meet in LDS.  Weights travel through a ring of LDS of each wave's own by direct loads,
 // which ask for whole 128-byte rows; fetched straight into the lanes that the matrix
@@ -176,12 +242,14 @@ __global__ void __launch_bounds__(256) q8_quantize_kernel(QuantArgs a)
 // from tile to tile, and is filled before the rows are quantised.
 struct VecArgs {
     const void *X;
+    const float *x_scales;  // of 8-bit rows
     const int8_t *W;
     const float *w_scales;
     void *Y;
     const int *offsets;  // or null: one group of all rows
     int64_t ldx, ldw, stride_w, ldy;
-    int rows, N, K;
+    int rows, N, K, groups;
+    int fill;            // rows outside every group are set to zero
     int pass;            // rows in LDS at once, at most 16
     int slabs;           // of 128 bytes
 };
@@ -198,7 +266,7 @@ inline int vec_lds(int pass, int slabs, int depth)
            2 * kVecTiles * 64 + 16 * kVecWaves * 4 + 64;
 }
 
-template <typename T, int DEPTH, bool FAST>
+template <typename TX, typename TY, int DEPTH, bool FAST>
 __global__ void __launch_bounds__(kVecWaves * 64) q8_vec_kernel(VecArgs a)
 {
     extern __shared__ __attribute__((aligned(1024))) char vec_shared[];
@@ -212,6 +280,9 @@ __global__ void __launch_bounds__(kVecWaves * 64) q8_vec_kernel(VecArgs a)
     char *rows_lds = reinterpret_cast<char *>(scales + 16);
 
     const int group = blockIdx.y;
+    if (a.fill && group == 0)
+        zero_outside(a.offsets, a.groups, a.rows, a.N, static_cast<TY *>(a.Y), a.ldy, blockIdx.x, gridDim.x);
+    if (group >= a.groups) return;
     int begin = 0, end = a.rows;
     if (a.offsets) group_rows(a.offsets, group, a.rows, begin, end);
     begin = __builtin_amdgcn_readfirstlane(begin);
@@ -273,24 +344,42 @@ __global__ void __launch_bounds__(kVecWaves * 64) q8_vec_kernel(VecArgs a)
             }
         }
         // ---- the rows, in the slabs' order: chunk c of row r of a slab at place c ^ (r / 2)
-        {
+        const auto chunk_of = [&](int r, int c) {
+            return reinterpret_cast<u32x4 *>(rows_lds + ((c >> 3) * R + r) * 128 +
+                                             (((c & 7) ^ ((r >> 1) & 7)) << 4));
+        };
+        const TX *X = static_cast<const TX *>(a.X) + (int64_t)first * a.ldx;
+        if constexpr (std::is_same<TX, int8_t>::value) {
+            if (threadIdx.x < R) scales[threadIdx.x] = a.x_scales[first + threadIdx.x];
+            for (int i = threadIdx.x; i < R * a.slabs * 8; i += kVecWaves * 64) {
+                const int r = i / (a.slabs * 8), c = i - r * (a.slabs * 8), left = a.K - c * 16;
+                const int8_t *x = X + r * a.ldx + c * 16;
+                u32x4 q = {0, 0, 0, 0};
+                if (left >= 16) {
+                    __builtin_memcpy(&q, x, 16);
+                } else {
+#pragma unroll
+                    for (int b = 0; b < 16; ++b)
+                        if (b < left) q[b / 4] |= (uint32_t)(uint8_t)x[b] << (8 * (b % 4));
+                }
+                *chunk_of(r, c) = q;
+            }
+        } else {
             int per = 1;  // waves of a row
             while (per < kVecWaves && per * 2 * R <= kVecWaves) per *= 2;
             const int stride = kVecWaves / per, part = wave % per;
             float v[16];
             for (int r = wave / per; r < R; r += stride) {
-                const T *row = static_cast<const T *>(a.X) + (int64_t)(first + r) * a.ldx;
                 uint32_t m = 0;
                 for (int c = part * 64 + lane; c < a.slabs * 8; c += per * 64) {
-                    load16(row, c * 16, a.K, v);
-                    m = max16(v, m);
+                    load_values<16>(X + r * a.ldx, c * 16, a.K, v);
+                    m = max_of(v, m);
                 }
                 m = wave_max(m);
                 if (lane == 0) maxima[r * kVecWaves + part] = m;
             }
             __syncthreads();
             for (int r = wave / per; r < R; r += stride) {
-                const T *row = static_cast<const T *>(a.X) + (int64_t)(first + r) * a.ldx;
                 uint32_t m = 0;
                 for (int p = 0; p < per; ++p) {
                     const uint32_t u = maxima[r * kVecWaves + p];
@@ -299,14 +388,14 @@ __global__ void __launch_bounds__(kVecWaves * 64) q8_vec_kernel(VecArgs a)
                 const Quantum s(m);
                 if (part == 0 && lane == 0) scales[r] = s.scale;
                 for (int c = part * 64 + lane; c < a.slabs * 8; c += per * 64) {
-                    load16(row, c * 16, a.K, v);
-                    const u32x4 q = quantize16(v, s);
-                    *reinterpret_cast<u32x4 *>(rows_lds + ((c >> 3) * R + r) * 128 +
-                                               (((c & 7) ^ ((r >> 1) & 7)) << 4)) = q;
+                    load_values<16>(X + r * a.ldx, c * 16, a.K, v);
+                    uint32_t q[4];
+                    s.bytes(v, q);
+                    *chunk_of(r, c) = u32x4{q[0], q[1], q[2], q[3]};
                 }
             }
-            __syncthreads();
         }
+        __syncthreads();
         // ---- tiles
         const int l16 = lane & 15, g = lane >> 4;
         const int xr = l16 < R ? l16 : R - 1;  // rows past the last repeat it, and are not stored
@@ -361,8 +450,8 @@ __global__ void __launch_bounds__(kVecWaves * 64) q8_vec_kernel(VecArgs a)
                 int sum = 0;
 #pragma unroll
                 for (int v = 0; v < kVecWaves; ++v) sum += tile[v * 256 + threadIdx.x];
-                static_cast<T *>(a.Y)[(int64_t)(first + row) * a.ldy + n] =
-                    (T)((float)sum * scales[row] * w);
+                static_cast<TY *>(a.Y)[(int64_t)(first + row) * a.ldy + n] =
+                    (TY)((float)sum * scales[row] * w);
             }
         }
         if constexpr (FAST) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");

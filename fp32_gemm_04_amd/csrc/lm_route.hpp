@@ -216,15 +216,6 @@ template <typename T> struct Single {
     __device__ __forceinline__ void zero() { v[0] = (T)0.f; }
 };
 
-// p[i], a scalar load where i is the wave's (no output of these kernels overlaps an input).
-template <bool UNIFORM, typename T> __device__ __forceinline__ T read(const T *p, int64_t i)
-{
-    if constexpr (UNIFORM)
-        return ((const __attribute__((address_space(4))) T *)(uintptr_t)p)[i];
-    else
-        return p[i];
-}
-
 // Choices of a token that are handled together: their rows are all in flight at once.
 constexpr int kChoices = 8;
 
@@ -254,16 +245,17 @@ template <bool UNIFORM, int N> struct Choices {
 // compiler is told so: its places and weights then are scalar loads, and its rows' addresses a
 // scalar base each, where vector loads of them would be two more for each of a row.
 template <bool UNIFORM, int E>
-__device__ __forceinline__ bool turn_of(const RouteArgs &a, int64_t b, int parts, int &t, int &h)
+__device__ __forceinline__ bool turn_of(const RouteArgs &a, int64_t b, int parts, int &t, int &h0)
 {
     const int cols = 1 << a.cols_log2, per = 256 >> a.cols_log2;
     const int col = threadIdx.x & (cols - 1);
     int sub = threadIdx.x >> a.cols_log2;
     if constexpr (UNIFORM) sub = __builtin_amdgcn_readfirstlane(sub);
     const int64_t at = b / parts * per + sub;
-    h = ((int)(b % parts) * cols + col) * E;
+    const uint32_t h = ((uint32_t)(b % parts) * cols + col) * E;  // may pass 2^31
     t = (int)at;
-    return at < a.tokens;
+    h0 = (int)h;
+    return at < a.tokens && h < (uint32_t)a.H;
 }
 
 __device__ __forceinline__ int parts_of_row(const RouteArgs &a, int e)
@@ -285,7 +277,7 @@ __global__ void __launch_bounds__(256) gather_kernel(RouteArgs a)
     const int64_t work = turns(a, parts);
     for (int64_t b = blockIdx.x; b < work; b += gridDim.x) {
         int t, h;
-        if (!turn_of<UNIFORM, E>(a, b, parts, t, h) || h >= a.H) continue;
+        if (!turn_of<UNIFORM, E>(a, b, parts, t, h)) continue;
         const auto copy = [&](auto x, int at) {
             x.load(static_cast<const T *>(a.X) + t * a.ldx + at);
             for (int j0 = 0; j0 < a.k; j0 += kChoices) {
@@ -322,7 +314,7 @@ __global__ void __launch_bounds__(256) combine_kernel(RouteArgs a)
     const int64_t work = turns(a, parts);
     for (int64_t b = blockIdx.x; b < work; b += gridDim.x) {
         int t, h;
-        if (!turn_of<UNIFORM, E>(a, b, parts, t, h) || h >= a.H) continue;
+        if (!turn_of<UNIFORM, E>(a, b, parts, t, h)) continue;
         const auto sum_up = [&](auto y, int at) {
             float sum[y.E];
 #pragma unroll
@@ -413,11 +405,12 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(RouteArgs a)
                                     dot[j] = fmaf((float)d.v[i], (float)x[j].v[i], dot[j]);
                     }
                 };
-                for (int h = ((wave % WAVES) * 64 + lane) * E; h < a.H; h += WAVES * 64 * E) {
-                    if (h + E <= a.H)
-                        both(Piece<T>(), h);
+                for (uint32_t h = ((wave % WAVES) * 64 + lane) * E; h < (uint32_t)a.H;
+                     h += WAVES * 64 * E) {
+                    if (h + E <= (uint32_t)a.H)
+                        both(Piece<T>(), (int)h);
                     else
-                        for (int at = h; at < a.H; ++at) both(Single<T>(), at);
+                        for (int at = (int)h; at < a.H; ++at) both(Single<T>(), at);
                 }
             }
             if (!a.dweights) continue;

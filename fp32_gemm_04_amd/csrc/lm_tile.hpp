@@ -104,6 +104,7 @@ struct TileArgs {
     int wrap;
     // SCALE: of each row of A, and of each row of B (N of one group after another's).
     const float *scale_a, *scale_b;
+    int fill;                    // SCALE, ROWS: rows outside every group are set to zero
 };
 
 typedef void (*TileFn)(TileArgs);
@@ -285,6 +286,15 @@ __device__ __forceinline__ typename AccOf<T, BL>::Type mfma_step(const typename 
     }
 }
 
+// p[i], a scalar load where i is the wave's (no output of these kernels overlaps an input).
+template <bool UNIFORM, typename T> __device__ __forceinline__ T read(const T *p, int64_t i)
+{
+    if constexpr (UNIFORM)
+        return ((const __attribute__((address_space(4))) T *)(uintptr_t)p)[i];
+    else
+        return p[i];
+}
+
 __device__ __forceinline__ int clamp_row(int v, int lo, int hi)
 {
     return v < lo ? lo : v > hi ? hi : v;
@@ -295,6 +305,18 @@ __device__ __forceinline__ void group_rows(const int *offsets, int e, int rows, 
 {
     begin = clamp_row(offsets[e], 0, rows);
     end = clamp_row(offsets[e + 1], begin, rows);
+}
+
+// Rows of C outside increasing groups are set to zero, each by one of all workgroups.
+template <typename TC>
+__device__ __forceinline__ void zero_outside(const int *offsets, int groups, int rows, int N, TC *C,
+                                             int64_t ldc, int block, int blocks)
+{
+    const int low = clamp_row(offsets[0], 0, rows), high = clamp_row(offsets[groups], low, rows);
+    for (int64_t i = block; i < (int64_t)low + rows - high; i += blocks) {
+        TC *c = C + (i < low ? i : high + i - low) * ldc;
+        for (int n = threadIdx.x; n < N; n += blockDim.x) c[n] = (TC)0.f;
+    }
 }
 
 // The row tiles of all groups, counted 64 groups at a time by the wave's lanes.
@@ -360,6 +382,10 @@ tile_kernel(TileArgs g)
             all += __shfl((long long)scan_tiles(g.offsets, g.groups, g.M, BM, g0, b, e, n), 63);
         const int total = (int)(all < g.most_tiles ? all : g.most_tiles);
         const int tiles_n = (g.N + BN - 1) / BN;
+        if constexpr (EP == SCALE)
+            if (g.fill)
+                zero_outside(g.offsets, g.groups, g.M, g.N, static_cast<TC *>(g.C), g.ldc, blockIdx.x,
+                             gridDim.x);
         if ((int64_t)blockIdx.x >= (int64_t)total * tiles_n) return;
         tile_of_block(blockIdx.x, total, tiles_n, 8, tm, tn);
         int64_t before = 0;
@@ -675,15 +701,19 @@ tile_kernel(TileArgs g)
     // columns 0-3, 8-11 and 4-7, 12-15; exchanged, each lane stores eight in a row, half as
     // many and twice as wide stores.
     constexpr bool PAIRED = BL == 32 && sizeof(TC) == 2;
-    auto store_pair = [&](TC *crow, int u, auto first, auto second) {
+    auto paired = [&](auto first, auto second) {
         typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
         if constexpr (sizeof(first) == sizeof(u32x2)) {
             const u32x2 x = __builtin_bit_cast(u32x2, first), y = __builtin_bit_cast(u32x2, second);
             const auto p = __builtin_amdgcn_permlane32_swap(x[0], y[0], false, false);
             const auto q = __builtin_amdgcn_permlane32_swap(x[1], y[1], false, false);
-            const int n = column(u) + 4 * lg;
-            *reinterpret_cast<u32x4 *>(crow + n) = u32x4{p[0], q[0], p[1], q[1]};
+            return u32x4{p[0], q[0], p[1], q[1]};
+        } else {
+            return u32x4{};
         }
+    };
+    auto store_pair = [&](TC *crow, int u, auto first, auto second) {
+        *reinterpret_cast<u32x4 *>(crow + column(u) + 4 * lg) = paired(first, second);
     };
     // A tile inside C with vector stores takes copies without per-column tests.
     const bool whole = n0 + BN <= g.N && g.vec_c >= (PAIRED ? 2 : 1);
@@ -749,10 +779,18 @@ tile_kernel(TileArgs g)
             store(std::false_type{}, std::false_type{});
     } else if constexpr (EP == SCALE) {
         // Sums below 2^31 become fp32 (half a step of 2^-24 relative), then two products and
-        // one rounding to TC.
+        // one rounding to TC.  Vector stores need no more than an element's alignment.
+        typedef Vec Loose __attribute__((aligned(sizeof(TC))));
+        typedef u32x4 LoosePair __attribute__((aligned(2)));
         TC *C = static_cast<TC *>(g.C);
         const float *sb = g.scale_b + (int64_t)group * g.N;
         auto store = [&](auto inside) {
+            f32x4 s[FN * GR];
+#pragma unroll
+            for (int u = 0; u < FN * GR; ++u)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    s[u][q] = decltype(inside)::value || column(u) + q < g.N ? sb[column(u) + q] : 0.f;
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
                 __builtin_amdgcn_sched_barrier(0);
@@ -764,20 +802,16 @@ tile_kernel(TileArgs g)
 #pragma unroll
                 for (int u = 0; u < FN * GR; ++u) {
                     const int n = column(u);
-                    float s[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        s[q] = decltype(inside)::value || n + q < g.N ? sb[n + q] : 0.f;
                     Vec out;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) out[q] = (TC)((float)value(i, u, q) * sa * s[q]);
+                    for (int q = 0; q < 4; ++q) out[q] = (TC)((float)value(i, u, q) * sa * s[u][q]);
                     if constexpr (PAIRED && decltype(inside)::value) {
                         if (u % 2 == 0)
                             before = out;
                         else
-                            store_pair(crow, u - 1, before, out);
-                    } else if (decltype(inside)::value || (g.vec_c && n + 4 <= g.N)) {
-                        *reinterpret_cast<Vec *>(crow + n) = out;
+                            *reinterpret_cast<LoosePair *>(crow + column(u - 1) + 4 * lg) = paired(before, out);
+                    } else if (decltype(inside)::value || n + 4 <= g.N) {
+                        *reinterpret_cast<Loose *>(crow + n) = out;
                     } else {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
@@ -786,7 +820,7 @@ tile_kernel(TileArgs g)
                 }
             }
         };
-        if (whole)
+        if (n0 + BN <= g.N)
             store(std::true_type{});
         else
             store(std::false_type{});

@@ -304,7 +304,7 @@ int sgemm_expert_combine_backward(int type, int tokens, int k, int H, int rows, 
  * scale for each output channel).
  *
  *   type      enum sgemm_type of X
- *   rows, K   >= 0;  X, ldx: rows x K
+ *   rows      >= 0;  K 0 .. 131071;  X, ldx: rows x K
  *   k, place  NULL place (k = 0): row r of X goes to row r of Q, out_rows = rows.  Otherwise
  *             row t goes to the k rows place[t*k + j], as sgemm_expert_gather sends them
  *             (rows without a token: left as they were, but those of dropped slots set
@@ -332,17 +332,19 @@ int sgemm_q8_quantize(int type, int rows, int K, const void *X, int ldx, int k, 
  *   W, ldw, stride_w   N x K bytes a group, ldw >= max(1, K), stride_w >= 0 bytes from one
  *             group to the next;  w_scales: groups x N floats, packed
  *   Y, ldy    rows x N, written
- *   offsets   groups + 1 ints on the device, as in sgemm_grouped (rows outside every group
- *             are left as they were), or NULL: all rows, one group
+ *   offsets   groups + 1 ints on the device, as in sgemm_grouped, or NULL: all rows, one group
+ *   fill      with offsets: 0: rows before offsets[0] and from offsets[groups] on are left as they
+ *             were; 1: they are set to zero
  * X and W at 4-byte addresses with leading dimensions (and stride_w) of multiples of 4 are
  * loaded straight to LDS; others go through registers, more slowly.
  * Returns -1 type, -2 groups, -3 rows, -4 N (or more than 2^31 - 1 tiles), -5 K, -6 X, -7
  * ldx, -8 x_scales, -9 W, -10 ldw, -11 stride_w, -12 w_scales, -13 Y, -14 ldy, -15 offsets
- * not 4-byte aligned.
+ * not 4-byte aligned, -16 fill.
  */
 int sgemm_q8_gemm(int type, int groups, int rows, int N, int K, const int8_t *X, int ldx,
                   const float *x_scales, const int8_t *W, int ldw, int64_t stride_w,
-                  const float *w_scales, void *Y, int ldy, const int *offsets, hipStream_t stream);
+                  const float *w_scales, void *Y, int ldy, const int *offsets, int fill,
+                  hipStream_t stream);
 
 /*
  * sgemm_q8_matvec -- sgemm_q8_quantize and sgemm_q8_gemm in one launch, for a few rows of X:
@@ -352,13 +354,14 @@ int sgemm_q8_gemm(int type, int groups, int rows, int N, int K, const int8_t *X,
  * are those of the two calls bit for bit.
  *
  *   type      enum sgemm_type of X and Y
- *   groups    as in sgemm_q8_gemm, at most 65535;  K at most 106496
+ *   groups, fill   as in sgemm_q8_gemm, groups at most 65535;  K at most 106496
  * Returns -1 type, -2 groups, -3 rows, -4 N, -5 K, -6 X, -7 ldx, -8 W, -9 ldw, -10
- * stride_w, -11 w_scales, -12 Y, -13 ldy, -14 offsets not 4-byte aligned.
+ * stride_w, -11 w_scales, -12 Y, -13 ldy, -14 offsets not 4-byte aligned, -15
+ * fill.
  */
 int sgemm_q8_matvec(int type, int groups, int rows, int N, int K, const void *X, int ldx,
                     const int8_t *W, int ldw, int64_t stride_w, const float *w_scales, void *Y,
-                    int ldy, const int *offsets, hipStream_t stream);
+                    int ldy, const int *offsets, int fill, hipStream_t stream);
 
 #ifdef __cplusplus
 }

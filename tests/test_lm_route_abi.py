@@ -21,9 +21,9 @@ BACK = dict(type=0, tokens=8, k=2, H=32, rows=16, dout=4096, lddo=32, R=8192, ld
             weights=16384, dR=20480, lddr=32, fill=0, dweights=24576)
 QUANT = dict(type=1, rows=8, K=32, X=4096, ldx=32, k=0, place=0, out_rows=8, Q=8192, ldq=32, scales=12288)
 GEMM = dict(type=1, groups=1, rows=8, N=16, K=32, X=4096, ldx=32, x_scales=8192, W=12288, ldw=32,
-            stride_w=512, w_scales=16384, Y=20480, ldy=16, offsets=0)
+            stride_w=512, w_scales=16384, Y=20480, ldy=16, offsets=0, fill=0)
 VEC = dict(type=1, groups=1, rows=8, N=16, K=32, X=4096, ldx=32, W=12288, ldw=32, stride_w=512,
-           w_scales=16384, Y=20480, ldy=16, offsets=0)
+           w_scales=16384, Y=20480, ldy=16, offsets=0, fill=0)
 CALLS = {"sgemm_expert_sort": SORT, "sgemm_expert_gather": GATHER, "sgemm_expert_combine": COMBINE,
          "sgemm_expert_combine_backward": BACK, "sgemm_q8_quantize": QUANT, "sgemm_q8_gemm": GEMM,
          "sgemm_q8_matvec": VEC}
@@ -66,7 +66,8 @@ def call(fn, kw):
     ("sgemm_expert_combine_backward", dict(fill=-1), -14),
     ("sgemm_expert_combine_backward", dict(dweights=2), -15),
     ("sgemm_q8_quantize", dict(type=2), -1), ("sgemm_q8_quantize", dict(rows=-1), -2),
-    ("sgemm_q8_quantize", dict(K=-1), -3), ("sgemm_q8_quantize", dict(X=0), -4),
+    ("sgemm_q8_quantize", dict(K=-1), -3), ("sgemm_q8_quantize", dict(K=131072, ldx=131072, ldq=131072), -3),
+    ("sgemm_q8_quantize", dict(X=0), -4),
     ("sgemm_q8_quantize", dict(ldx=31), -5), ("sgemm_q8_quantize", dict(k=1), -6),
     ("sgemm_q8_quantize", dict(k=-1, place=4096), -6), ("sgemm_q8_quantize", dict(k=MOST, place=4096), -6),
     ("sgemm_q8_quantize", dict(k=1, place=2), -7), ("sgemm_q8_quantize", dict(out_rows=9), -8),
@@ -81,14 +82,14 @@ def call(fn, kw):
     ("sgemm_q8_gemm", dict(x_scales=0), -8), ("sgemm_q8_gemm", dict(W=0), -9),
     ("sgemm_q8_gemm", dict(ldw=31), -10), ("sgemm_q8_gemm", dict(stride_w=-1), -11),
     ("sgemm_q8_gemm", dict(w_scales=2), -12), ("sgemm_q8_gemm", dict(Y=20481), -13),
-    ("sgemm_q8_gemm", dict(ldy=15), -14), ("sgemm_q8_gemm", dict(offsets=2), -15),
+    ("sgemm_q8_gemm", dict(ldy=15), -14), ("sgemm_q8_gemm", dict(offsets=2), -15), ("sgemm_q8_gemm", dict(fill=2), -16),
     ("sgemm_q8_matvec", dict(type=2), -1), ("sgemm_q8_matvec", dict(groups=65536, offsets=4096), -2),
     ("sgemm_q8_matvec", dict(rows=-1), -3), ("sgemm_q8_matvec", dict(N=MOST + 1), -4),
     ("sgemm_q8_matvec", dict(K=106497, ldx=2 ** 20, ldw=2 ** 20), -5), ("sgemm_q8_matvec", dict(X=4097), -6),
     ("sgemm_q8_matvec", dict(ldx=31), -7), ("sgemm_q8_matvec", dict(W=0), -8),
     ("sgemm_q8_matvec", dict(ldw=31), -9), ("sgemm_q8_matvec", dict(stride_w=-1), -10),
     ("sgemm_q8_matvec", dict(w_scales=0), -11), ("sgemm_q8_matvec", dict(Y=0), -12),
-    ("sgemm_q8_matvec", dict(ldy=15), -13), ("sgemm_q8_matvec", dict(offsets=2), -14),
+    ("sgemm_q8_matvec", dict(ldy=15), -13), ("sgemm_q8_matvec", dict(offsets=2), -14), ("sgemm_q8_matvec", dict(fill=-1), -15),
 ])
 def test_invalid_arguments(fn, kw, code):
     assert call(fn, kw) == code

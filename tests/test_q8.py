@@ -124,7 +124,7 @@ def product(X, sx, W, sw):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("rows,N,K", [(1, 1, 1), (1, 70, 130), (16, 64, 128), (17, 65, 127), (40, 200, 500),
                                       (100, 131, 1000), (130, 260, 96), (257, 300, 144), (1030, 1100, 272),
-                                      (5, 33, 0), (0, 8, 8), (8, 0, 8), (3, 50, 4099)])
+                                      (5, 33, 0), (0, 8, 8), (8, 0, 8), (3, 50, 4099), (30, 7, 0)])
 @pytest.mark.parametrize("pad", [0, 4, 3])
 def test_gemm(dtype, rows, N, K, pad):
     say("q8 gemm", dtype, rows, N, K, pad)
@@ -204,12 +204,55 @@ def test_matvec(dtype, rows, N, K, pad, shift):
     assert torch.equal(into._base.view(bits), base.view(bits))
 
 
-@pytest.mark.parametrize("rows,K", [(1, 106496), (3, 50000), (16, 7000), (9, 9000), (2, 106496)])
-def test_matvec_of_long_rows_takes_passes(rows, K):
-    say("q8 matvec long", rows, K)
-    X, W, sw = rand((rows, K), BF16, 1), bytes_of((37, K), 2), positive((37,), 3)
+def one_launch(X, W, sw, offsets=None):
+    """sgemm_q8_matvec whatever the number of values (q8_matvec quantises many beforehand)."""
+    groups, N, (rows, K) = W.shape[0] if W.dim() == 3 else 1, W.shape[-2], X.shape
+    Y = torch.full((rows, N), float("nan"), dtype=X.dtype, device="cuda")
+    status = sg.sgemm_q8_matvec(
+        int(X.dtype == BF16), groups, rows, N, K, X.data_ptr(), X.stride(0), W.data_ptr(), W.stride(-2),
+        W.stride(0) if W.dim() == 3 else 0, sw.data_ptr(), Y.data_ptr(), N,
+        offsets.data_ptr() if offsets is not None else 0, 1, torch.cuda.current_stream().cuda_stream)
+    assert status == 0
+    return Y
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,K", [(1, 106496), (3, 50000), (16, 7000), (9, 9000), (2, 106496), (16, 4096),
+                                    (40, 1200), (1, 40000)])
+@pytest.mark.parametrize("pad", [0, 2])
+def test_matvec_of_long_rows_takes_passes(dtype, rows, K, pad):
+    say("q8 matvec long", dtype, rows, K, pad)
+    X, W, sw = rand((rows, K), dtype, 1), bytes_of((37, K + pad), 2)[:, :K], positive((37,), 3)
     Q, s = sg.q8_quantize(X)
-    assert torch.equal(sg.q8_matvec(X, W, sw), sg.q8_gemm(Q, s, W, sw))
+    ref = sg.q8_gemm(Q, s, W, sw, dtype=dtype)
+    assert torch.equal(one_launch(X, W, sw), ref) and torch.equal(sg.q8_matvec(X, W, sw), ref)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("sizes", [[0, 0, 0], [3, 0, 40], [16, 17, 1, 0]])
+def test_matvec_of_groups_fills_rows_outside(dtype, sizes):
+    """In one launch and in two; rows outside every group become zero where the result is allocated."""
+    say("q8 matvec groups", dtype, sizes)
+    ends, off = offsets_of(sizes, first=3)
+    for K in (200, 3000):
+        X, W, sw = rand((ends[-1] + 4, K), dtype, 1), bytes_of((len(sizes), 70, K), 2), positive((len(sizes), 70), 3)
+        Q, s = sg.q8_quantize(X)
+        ref = torch.zeros((X.shape[0], 70), dtype=torch.float64, device="cuda")
+        for e in range(len(sizes)):
+            a, b = ends[e], ends[e + 1]
+            ref[a:b] = product(Q[a:b], s[a:b], W[e], sw[e])
+        for Y in (one_launch(X, W, sw, off), sg.q8_matvec(X, W, sw, offsets=off),
+                  sg.q8_gemm(Q, s, W, sw, off, dtype=dtype)):
+            check(Y, ref, ref.abs(), 3, "groups")
+
+
+def test_no_groups_at_all():
+    say("q8 no groups")
+    X, off = rand((5, 32), BF16, 1), torch.tensor([2], dtype=torch.int32, device="cuda")
+    W, sw = torch.empty((0, 9, 32), dtype=torch.int8, device="cuda"), torch.empty((0, 9), device="cuda")
+    Q, s = sg.q8_quantize(X)
+    for Y in (sg.q8_matvec(X, W, sw, offsets=off), sg.q8_gemm(Q, s, W, sw, off)):
+        assert Y.shape == (5, 9) and (Y == 0).all()
 
 
 def test_matvec_over_many_tiles():

@@ -762,12 +762,17 @@ def expert_sort(experts, groups: int, stream=None):
 
 def _slots(place, weights, device, tokens, name):
     """(k, place's pointer, weights' pointer): one row and one weight for each choice."""
-    if place.dim() != 2 or place.shape[0] != tokens:
+    shape = place.shape
+    if len(shape) != 2 or shape[0] != tokens:
         raise ValueError("place must be (%d, k) for the rows of %s" % (tokens, name))
-    _extent(place.numel(), "place")
-    pp = _packed(place, "place", torch.int32, device, place.shape)
-    pw = _packed(weights, "weights", torch.float32, device, place.shape) if weights is not None else 0
-    return place.shape[1], pp, pw
+    k = shape[1]
+    if tokens * k > _MOST_INT:
+        _extent(tokens * k, "place")
+    if place.dtype is not torch.int32 or place.device != device or not place.is_contiguous():
+        raise ValueError("place must be a packed int32 tensor on %s" % device)
+    if weights is None:
+        return k, place.data_ptr(), 0
+    return k, place.data_ptr(), _packed(weights, "weights", torch.float32, device, shape)
 
 
 def expert_gather(X, place, weights=None, out=None, stream=None):
@@ -888,7 +893,9 @@ def q8_quantize(X, place=None, stream=None):
 
     def body(s):
         nonlocal Q, scales
-        Q = X.new_empty(lead + (out if place is not None else rows, ldq), dtype=torch.int8)[..., :K]
+        Q = X.new_empty(lead + (out if place is not None else rows, ldq), dtype=torch.int8)
+        if ldq != K:
+            Q = Q[..., :K]
         scales = X.new_empty(lead + (out if place is not None else rows,), dtype=torch.float32)
         return _lib.sgemm_q8_quantize(t, n, K, X.data_ptr(), ldx, k, pp, out, Q.data_ptr(), ldq,
                                       scales.data_ptr(), s)
@@ -898,13 +905,14 @@ def q8_quantize(X, place=None, stream=None):
 
 def _q8_weights(Q, scales, offsets, device, K):
     """(groups, N, leading dimension, offsets' pointer, scales' pointer) of 8-bit weights."""
-    if Q.dim() != (2 if offsets is None else 3):
+    shape = Q.shape
+    if len(shape) != (2 if offsets is None else 3):
         raise ValueError("Q must be (N, K), or (groups, N, K) with offsets")
-    groups, N = Q.shape[0] if Q.dim() == 3 else 1, Q.shape[-2]
-    ldw = _operand(Q, "Q", torch.int8, device, Q.dim(), N, K)
-    ps = _packed(scales, "scales", torch.float32, device, Q.shape[:-1])
-    off = _vector(offsets, "offsets", torch.int32, device, groups + 1) if offsets is not None else 0
-    return groups, N, ldw, off, ps
+    ldw = _operand(Q, "Q", torch.int8, device, len(shape), None, K)
+    ps = _packed(scales, "scales", torch.float32, device, shape[:-1])
+    if offsets is None:
+        return 1, shape[0], ldw, 0, ps
+    return shape[0], shape[1], ldw, _vector(offsets, "offsets", torch.int32, device, shape[0] + 1), ps
 
 
 def q8_gemm(X, x_scales, Q, scales, offsets=None, Y=None, dtype=torch.bfloat16, stream=None):

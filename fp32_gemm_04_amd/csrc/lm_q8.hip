@@ -56,7 +56,7 @@ int vec_product(VecArgs &a, bool bytes, bool bf16_out, int cus, hipStream_t stre
     const int64_t tiles = ceil_div(a.N, 16), used = a.groups < 1 ? 1 : a.groups < a.rows ? a.groups : a.rows;
     const int64_t room = (int64_t)cus * (160 * 1024 / lds < 2 ? 1 : 2) / used;
     const int64_t blocks = room < 1 ? 1 : room < tiles ? room : tiles;
-    kernel<<<dim3((unsigned)blocks, (unsigned)(a.groups < 1 ? 1 : a.groups)), dim3(kVecWaves * 64), lds, stream>>>(a);
+    kernel<<<dim3((unsigned)blocks, (unsigned)used), dim3(kVecWaves * 64), lds, stream>>>(a);
     return (int)hipGetLastError();
 }
 

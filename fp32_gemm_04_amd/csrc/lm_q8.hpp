@@ -279,11 +279,27 @@ __global__ void __launch_bounds__(kVecWaves * 64) q8_vec_kernel(VecArgs a)
     float *scales = reinterpret_cast<float *>(maxima + 16 * kVecWaves);
     char *rows_lds = reinterpret_cast<char *>(scales + 16);
 
-    const int group = blockIdx.y;
-    if (a.fill && group == 0)
+    if (a.fill && blockIdx.y == 0)
         zero_outside(a.offsets, a.groups, a.rows, a.N, static_cast<TY *>(a.Y), a.ldy, blockIdx.x, gridDim.x);
-    if (group >= a.groups) return;
-    int begin = 0, end = a.rows;
+    int group = blockIdx.y, begin = 0, end = a.rows;
+    if ((int)gridDim.y < a.groups) {
+        // More groups than rows: the blockIdx.y-th of those that have rows.
+        int before = blockIdx.y, at = -1;
+        for (int g0 = 0; g0 < a.groups && at < 0; g0 += 64) {
+            int b = 0, e = 0;
+            if (g0 + lane < a.groups) group_rows(a.offsets, g0 + lane, a.rows, b, e);
+            uint64_t some = __ballot(e > b);
+            const int n = __popcll(some);
+            if (before >= n) {
+                before -= n;
+                continue;
+            }
+            for (; before > 0; --before) some &= some - 1;
+            at = g0 + __builtin_ctzll(some);
+        }
+        group = at;
+    }
+    if (group < 0 || group >= a.groups) return;
     if (a.offsets) group_rows(a.offsets, group, a.rows, begin, end);
     begin = __builtin_amdgcn_readfirstlane(begin);
     end = __builtin_amdgcn_readfirstlane(end);

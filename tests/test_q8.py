@@ -229,7 +229,8 @@ def test_matvec_of_long_rows_takes_passes(dtype, rows, K, pad):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("sizes", [[0, 0, 0], [3, 0, 40], [16, 17, 1, 0]])
+@pytest.mark.parametrize("sizes", [[0, 0, 0], [3, 0, 40], [16, 17, 1, 0], [0] * 70 + [2, 0, 1] + [0] * 60 + [5],
+                                   [0] * 63 + [1, 1] + [0] * 200, [1] + [0] * 9])
 def test_matvec_of_groups_fills_rows_outside(dtype, sizes):
     """In one launch and in two; rows outside every group become zero where the result is allocated."""
     say("q8 matvec groups", dtype, sizes)

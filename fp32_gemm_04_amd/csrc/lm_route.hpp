@@ -103,11 +103,20 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(SortArgs a)
             atomicAdd(&base[e], earlier);
         }
     } else if (!alone) {
-#pragma unroll 4
-        for (int s = threadIdx.x; s < a.slots; s += blockDim.x) {
-            const int e = sort_key(a.experts, s, a.groups);
-            atomicAdd(&total[e], 1);
-            if (s < s0) atomicAdd(&base[e], 1);
+        // Eight loads in flight; past the last slot the last is read again and not counted.
+        for (int s = threadIdx.x; s < a.slots; s += 8 * blockDim.x) {
+            int e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int at = s + i * (int)blockDim.x;
+                e[i] = sort_key(a.experts, at < a.slots ? at : a.slots - 1, a.groups);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int at = s + i * (int)blockDim.x;
+                if (at < a.slots) atomicAdd(&total[e[i]], 1);
+                if (at < s0) atomicAdd(&base[e[i]], 1);
+            }
         }
     }
     const int bits = 32 - __builtin_clz(n);  // n itself marks lanes without a slot

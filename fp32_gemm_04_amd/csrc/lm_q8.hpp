@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kVecWaves * 64) q8_vec_kernel(VecArgs a)
     char *rows_lds = reinterpret_cast<char *>(scales + 16);
 
     if (a.fill && blockIdx.y == 0)
-        zero_outside(a.offsets, a.groups, a.rows, a.N, static_cast<TY *>(a.Y), a.ldy, blockIdx.x, gridDim.x);
+        zero_outside(a.offsets, a.groups, a.rows, a.N, static_cast<TY *>(a.Y), a.ldy);
     int group = blockIdx.y, begin = 0, end = a.rows;
     if ((int)gridDim.y < a.groups) {
         // More groups than rows: the blockIdx.y-th of those that have rows.

@@ -307,13 +307,13 @@ __device__ __forceinline__ void group_rows(const int *offsets, int e, int rows, 
     end = clamp_row(offsets[e + 1], begin, rows);
 }
 
-// Rows of C outside increasing groups are set to zero, each by one of all workgroups.
+// Rows of C outside increasing groups are set to zero, each by one of all workgroups along x.
 template <typename TC>
 __device__ __forceinline__ void zero_outside(const int *offsets, int groups, int rows, int N, TC *C,
-                                             int64_t ldc, int block, int blocks)
+                                             int64_t ldc)
 {
     const int low = clamp_row(offsets[0], 0, rows), high = clamp_row(offsets[groups], low, rows);
-    for (int64_t i = block; i < (int64_t)low + rows - high; i += blocks) {
+    for (int64_t i = blockIdx.x; i < (int64_t)low + rows - high; i += gridDim.x) {
         TC *c = C + (i < low ? i : high + i - low) * ldc;
         for (int n = threadIdx.x; n < N; n += blockDim.x) c[n] = (TC)0.f;
     }
@@ -376,21 +376,25 @@ tile_kernel(TileArgs g)
     // ---- which tile, of which group
     int tm, tn, group = 0, begin = 0, end = 0, m0;
     if constexpr (RG == ROWS) {
+        // (Up to 64 groups are counted once: a tile's first loads wait for this.)
         int b, e, n;
-        int64_t all = 0;
-        for (int g0 = 0; g0 < g.groups; g0 += 64)
-            all += __shfl((long long)scan_tiles(g.offsets, g.groups, g.M, BM, g0, b, e, n), 63);
+        int64_t sum = scan_tiles(g.offsets, g.groups, g.M, BM, 0, b, e, n);
+        int64_t all = __shfl((long long)sum, 63);
+        for (int g0 = 64; g0 < g.groups; g0 += 64) {
+            int b1, e1, n1;
+            all += __shfl((long long)scan_tiles(g.offsets, g.groups, g.M, BM, g0, b1, e1, n1), 63);
+        }
         const int total = (int)(all < g.most_tiles ? all : g.most_tiles);
         const int tiles_n = (g.N + BN - 1) / BN;
-        if constexpr (EP == SCALE)
-            if (g.fill)
-                zero_outside(g.offsets, g.groups, g.M, g.N, static_cast<TC *>(g.C), g.ldc, blockIdx.x,
-                             gridDim.x);
-        if ((int64_t)blockIdx.x >= (int64_t)total * tiles_n) return;
+        if ((int64_t)blockIdx.x >= (int64_t)total * tiles_n) {
+            if constexpr (EP == SCALE)
+                if (g.fill) zero_outside(g.offsets, g.groups, g.M, g.N, static_cast<TC *>(g.C), g.ldc);
+            return;
+        }
         tile_of_block(blockIdx.x, total, tiles_n, 8, tm, tn);
         int64_t before = 0;
         for (int g0 = 0; g0 < g.groups; g0 += 64) {
-            const int64_t sum = scan_tiles(g.offsets, g.groups, g.M, BM, g0, b, e, n);
+            if (g0 > 0) sum = scan_tiles(g.offsets, g.groups, g.M, BM, g0, b, e, n);
             const uint64_t past = __ballot(before + sum > tm);
             if (past) {
                 const int at = __builtin_ctzll(past);
@@ -824,6 +828,8 @@ tile_kernel(TileArgs g)
             store(std::true_type{});
         else
             store(std::false_type{});
+        if constexpr (RG == ROWS)
+            if (g.fill) zero_outside(g.offsets, g.groups, g.M, g.N, C, g.ldc);
     } else if constexpr (EP == PART) {
         float *C = static_cast<float *>(g.C) + blockIdx.z * g.slice_stride;
 #pragma unroll

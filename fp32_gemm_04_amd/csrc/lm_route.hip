@@ -18,16 +18,22 @@ constexpr int kMostSegments = 256;
 // How a sort is cut into segments of whole chunks, one a workgroup.  Few slots are counted by
 // every workgroup for itself, in one launch; for more, a launch before counts each segment's.
 struct SortPlan {
-    int waves, segment, segments, pitch;
+    int waves, items, segment, segments, pitch;
     int64_t bytes;  // of counts; 0: one launch
 };
 
+// us in a graph.  One launch and two: 12297 slots, 33 experts 8.2 and 8.3, 16384, 32 experts 8.8
+// and 8.5 (a call of Python's: 10.0 and 14.6).  Chunks of one and two slots a lane: 128 slots, 64
+// experts 4.0 and 4.6, 16384, 32 experts 7.9 and 8.7, 65536, 64 experts 8.2 and 9.0, 262144, 64 experts
+// 10.6 both, 256 experts 19.9 and 15.0 (every workgroup reads all counts).
 SortPlan sort_plan(int slots, int groups)
 {
     SortPlan p;
     p.waves = groups <= 2048 ? 16 : 8;  // whose counters fit LDS
-    const int chunk = sort_chunk(p.waves);
-    const int64_t chunks = slots > 0 ? ceil_div(slots, chunk) : 1;
+    const int most = slots > 0 ? slots : 1;
+    p.items = slots <= 16384 || ceil_div(slots, p.waves * 64) * (groups + 1) <= 16384 ? 1 : 2;
+    const int chunk = p.waves * 64 * p.items;
+    const int64_t chunks = ceil_div(most, chunk);
     p.segments = (int)(chunks < kMostSegments ? chunks : kMostSegments);
     // The last segments may be empty.
     p.segment = (int)(ceil_div(chunks, p.segments) * chunk);
@@ -104,7 +110,7 @@ extern "C" int sgemm_expert_sort(int slots, int groups, const int64_t *experts, 
         if (int rc = (int)hipGetLastError()) return rc;
     }
     const int lds = 2 * n * 4 + p.waves * n * 2;
-    sort_place_kernel<<<dim3(p.segments), dim3(p.waves * 64), lds, stream>>>(a);
+    (p.items == 1 ? sort_place_kernel<1> : sort_place_kernel<2>)<<<dim3(p.segments), dim3(p.waves * 64), lds, stream>>>(a);
     return (int)hipGetLastError();
 }
 

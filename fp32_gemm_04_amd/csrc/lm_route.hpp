@@ -25,9 +25,6 @@ struct SortArgs {
     int pitch;      // counts of one expert: segments, rounded up to 4
 };
 
-constexpr int kSortItems = 2;  // slots of a lane, in registers, per chunk
-inline __host__ __device__ int sort_chunk(int waves) { return waves * 64 * kSortItems; }
-
 // The place of an expert's number among the counters: those outside come last.
 __device__ __forceinline__ int sort_key(const int64_t *experts, int64_t slot, int groups)
 {
@@ -57,11 +54,13 @@ __global__ void __launch_bounds__(1024) sort_count_kernel(SortArgs a)
 // found 64 slots at a time: the lanes with one expert are the and, over the bits of its
 // number, of the ballots of that bit (or their complements); the first of them advances
 // the wave's counter of the expert.  Integer counts: any order of the atomics gives the same.
+// A chunk is ITEMS slots of each lane, in registers.
+template <int ITEMS>
 __global__ void __launch_bounds__(1024) sort_place_kernel(SortArgs a)
 {
     extern __shared__ int shared[];
     __shared__ int wave_sum[16];
-    const int n = a.groups + 1, waves = blockDim.x >> 6, chunk = sort_chunk(waves);
+    const int n = a.groups + 1, waves = blockDim.x >> 6, chunk = blockDim.x * ITEMS;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int *base = shared;                                            // n: next row of each expert
     int *total = shared + n;                                       // n
@@ -69,11 +68,11 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(SortArgs a)
     uint16_t *own = cnt + wave * n;
     const int64_t s0 = (int64_t)blockIdx.x * a.segment;
     const int64_t s1 = s0 + a.segment < a.slots ? s0 + a.segment : a.slots;
-    int key[kSortItems], rank[kSortItems];
+    int key[ITEMS], rank[ITEMS];
     const auto load = [&](int64_t c0) {
-        const int64_t w0 = c0 + wave * (64 * kSortItems) + lane;
+        const int64_t w0 = c0 + wave * (64 * ITEMS) + lane;
 #pragma unroll
-        for (int i = 0; i < kSortItems; ++i)
+        for (int i = 0; i < ITEMS; ++i)
             key[i] = w0 + i * 64 < s1 ? sort_key(a.experts, w0 + i * 64, a.groups) : n;
     };
     load(s0);
@@ -124,7 +123,7 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(SortArgs a)
         for (int e = lane; e < n; e += 64) own[e] = 0;
         if (c0 > s0) load(c0);
 #pragma unroll
-        for (int i = 0; i < kSortItems; ++i) {
+        for (int i = 0; i < ITEMS; ++i) {
             uint64_t same = ~0ull;
             for (int b = 0; b < bits; ++b) {
                 const uint64_t set = __ballot(key[i] >> b & 1);
@@ -173,9 +172,9 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(SortArgs a)
             __syncthreads();
         }
 #pragma unroll
-        for (int i = 0; i < kSortItems; ++i) {
+        for (int i = 0; i < ITEMS; ++i) {
             if (key[i] >= n) continue;
-            const int slot = (int)(c0 + wave * (64 * kSortItems) + i * 64 + lane);
+            const int slot = (int)(c0 + wave * (64 * ITEMS) + i * 64 + lane);
             const int row = base[key[i]] + own[key[i]] + rank[i];
             a.place[slot] = key[i] < a.groups ? row : -2 - row;
             if (a.order) a.order[row] = slot;
@@ -184,7 +183,7 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(SortArgs a)
         __syncthreads();
         // The next chunk's rows follow.
 #pragma unroll
-        for (int i = 0; i < kSortItems; ++i)
+        for (int i = 0; i < ITEMS; ++i)
             if (key[i] < n) atomicAdd(&base[key[i]], 1);
         __syncthreads();
     }

@@ -45,9 +45,10 @@ def assert_sorted(ids, E, got):
     assert place.shape == ids.shape and place.flatten().tolist() == ref[2]
 
 
-# One workgroup's chunk is 2048 slots (1024 above 2048 experts); up to 16384 go in one launch.
+# One workgroup's chunk is 1024 slots or 2048 (half of that above 2048 experts); up to 16384 go in
+# one launch.
 @pytest.mark.parametrize("T,k", [(0, 2), (1, 0), (1, 1), (1, 7), (63, 1), (64, 1), (65, 3), (1024, 2),
-                                 (2049, 1), (2731, 6), (5462, 3)])
+                                 (2049, 1), (2731, 6), (5462, 3), (21000, 1)])
 @pytest.mark.parametrize("E", [0, 1, 2, 7, 64, 257, 1024, 2048, 2049, 4096])
 def test_sort(T, k, E):
     say("sort", T, k, E)
@@ -67,7 +68,7 @@ def test_sort_of_uneven_choices(ids):
 
 def test_sort_of_many_slots_takes_long_segments():
     """Past 256 chunks a segment is several of them."""
-    for n, E in [(256 * 2048 + 5, 40), (3 * 256 * 1024 + 77, 3000)]:
+    for n, E in [(300001, 40), (256 * 2048 + 5, 40), (3 * 256 * 1024 + 77, 3000)]:
         say("sort", n, E)
         ids = torch.randint(-3, E + 3, (n, 1), generator=torch.Generator().manual_seed(n)).cuda()
         offsets, order, place = sg.expert_sort(ids, E)

@@ -126,7 +126,8 @@ def test_sort_workspace():
     size = sg.sgemm_expert_sort_workspace
     assert size(-1, 1) == -1 and size(MOST + 1, 1) == -1 and size(1, -1) == -2 and size(1, 4097) == -2
     assert size(0, 0) == 0 and size(16384, 64) == 0  # one launch needs none
-    assert size(16385, 64) == 12 * 65 * 4  # nine chunks of 2048, rounded up to four
+    assert size(16385, 64) == 20 * 65 * 4  # seventeen chunks of 1024, rounded up to four
+    assert size(65537, 2000) == 36 * 2001 * 4  # many experts: 33 chunks of 2048
     assert size(MOST, 4096) == 256 * 4097 * 4  # never more than 256 segments
 
 

@@ -56,11 +56,41 @@ dim3 copy_grid(int tokens, int pieces, int log2)
     return dim3((unsigned)(work < kMostBlocks ? work : kMostBlocks));
 }
 
-template <typename T, int KT> auto backward_of(int waves)
+typedef void (*RouteFn)(RouteArgs);
+
+// Two, four or eight choices at a time; from 64 threads a row on a wave has one token.  us with
+// as many as k needs and with eight: gather of 4096 x 1 fp32 rows of 2048 12.4 and 17.4, weighted
+// gather of 8192 x 2 bf16 rows of 4096 37.7 and 43.2, combine 38.2 and 41.7, its gradients 69.9 and 73.7.
+template <typename T, int KT> RouteFn gather_of_choices(bool weighted, bool uniform)
+{
+    if (weighted) return uniform ? gather_kernel<T, KT, true, true> : gather_kernel<T, KT, true, false>;
+    return uniform ? gather_kernel<T, KT, false, true> : gather_kernel<T, KT, false, false>;
+}
+template <typename T> RouteFn gather_of(int k, bool weighted, int cols_log2)
+{
+    const bool uniform = cols_log2 >= 6;
+    return k <= 2   ? gather_of_choices<T, 2>(weighted, uniform)
+           : k <= 4 ? gather_of_choices<T, 4>(weighted, uniform)
+                    : gather_of_choices<T, 8>(weighted, uniform);
+}
+template <typename T> RouteFn combine_of(int k, int cols_log2)
+{
+    const bool uniform = cols_log2 >= 6;
+    if (k <= 2) return uniform ? combine_kernel<T, 2, true> : combine_kernel<T, 2, false>;
+    if (k <= 4) return uniform ? combine_kernel<T, 4, true> : combine_kernel<T, 4, false>;
+    return uniform ? combine_kernel<T, 8, true> : combine_kernel<T, 8, false>;
+}
+template <typename T, int KT> RouteFn backward_of_choices(int waves)
 {
     return waves == 1   ? combine_backward_kernel<T, 1, KT>
            : waves == 2 ? combine_backward_kernel<T, 2, KT>
                         : combine_backward_kernel<T, 4, KT>;
+}
+template <typename T> RouteFn backward_of(int k, int waves)
+{
+    return k <= 2   ? backward_of_choices<T, 2>(waves)
+           : k <= 4 ? backward_of_choices<T, 4>(waves)
+                    : backward_of_choices<T, 8>(waves);
 }
 
 // The checks that the copies share, of sizes; `type` is parameter 1, tokens 2, k 3, H 4.
@@ -134,17 +164,10 @@ extern "C" int sgemm_expert_gather(int type, int tokens, int k, int H, const voi
     a.X = X, a.out = R, a.place = place, a.weights = weights;
     a.ldx = ldx, a.ldo = ldr;
     a.tokens = tokens, a.k = k, a.H = H, a.rows = rows, a.fill = fill;
-    const int pieces = (int)ceil_div(H, 16 / size);
+    const int pieces = H / (16 / size) > 1 ? H / (16 / size) : 1;  // whole ones; the rest is theirs
     a.cols_log2 = cols_log2(pieces);
-    const bool uniform = a.cols_log2 >= 6;  // a wave has one token
-    const auto of = [&](auto plain, auto plain_uniform, auto weighted, auto weighted_uniform) {
-        return weights ? (uniform ? weighted_uniform : weighted) : uniform ? plain_uniform : plain;
-    };
-    auto fn = type == SGEMM_TYPE_BF16
-                  ? of(gather_kernel<bf16, false, false>, gather_kernel<bf16, false, true>,
-                       gather_kernel<bf16, true, false>, gather_kernel<bf16, true, true>)
-                  : of(gather_kernel<float, false, false>, gather_kernel<float, false, true>,
-                       gather_kernel<float, true, false>, gather_kernel<float, true, true>);
+    const auto fn = type == SGEMM_TYPE_BF16 ? gather_of<bf16>(k, weights != nullptr, a.cols_log2)
+                                            : gather_of<float>(k, weights != nullptr, a.cols_log2);
     fn<<<copy_grid(tokens, pieces, a.cols_log2), dim3(256), 0, stream>>>(a);
     return (int)hipGetLastError();
 }
@@ -168,12 +191,10 @@ extern "C" int sgemm_expert_combine(int type, int tokens, int k, int H, int rows
     a.R = R, a.out = out, a.place = place, a.weights = weights;
     a.ldr = ldr, a.ldo = ldo, a.beta = beta;
     a.tokens = tokens, a.k = reads ? k : 0, a.H = H, a.rows = rows;
-    const int pieces = (int)ceil_div(H, 16 / size);
+    const int pieces = H / (16 / size) > 1 ? H / (16 / size) : 1;  // whole ones; the rest is theirs
     a.cols_log2 = cols_log2(pieces);
-    const bool uniform = a.cols_log2 >= 6;  // a wave has one token
-    auto fn = type == SGEMM_TYPE_BF16
-                  ? (uniform ? combine_kernel<bf16, true> : combine_kernel<bf16, false>)
-                  : (uniform ? combine_kernel<float, true> : combine_kernel<float, false>);
+    const auto fn = type == SGEMM_TYPE_BF16 ? combine_of<bf16>(a.k, a.cols_log2)
+                                            : combine_of<float>(a.k, a.cols_log2);
     fn<<<copy_grid(tokens, pieces, a.cols_log2), dim3(256), 0, stream>>>(a);
     return (int)hipGetLastError();
 }
@@ -205,15 +226,12 @@ extern "C" int sgemm_expert_combine_backward(int type, int tokens, int k, int H,
     a.dweights = dweights;
     a.ldx = lddo, a.ldr = ldr, a.ldo = lddr;
     a.tokens = tokens, a.k = k, a.H = H, a.rows = work ? rows : 0, a.fill = fill;
-    // As many waves a token as its row has 16-byte pieces for, and four or eight choices at a time.
-    // us with 1, 2 and 4 waves: 32768 x 8 choices, 64 pieces 122, 132, 180; 128 pieces 232, 232, 242; 16384
-    // x 4, 256 pieces 139, 135, 122; 8192 x 2, 512 pieces 81, 73, 72.  With 4 and 8 choices: 16384 x 4
-    // 122 and 125, 8192 x 6 rows of 896 pieces 313 and 312, 4099 x 3 of 251 fp32 pieces 29.6 and 33.0.
+    // As many waves a token as its row has 16-byte pieces for.  us with 1, 2 and 4 waves: 32768 x 8
+    // choices, 64 pieces 122, 132, 180; 128 pieces 232, 232, 242; 16384 x 4, 256 pieces 139, 135, 122;
+    // 8192 x 2, 512 pieces 81, 73, 72.
     const int64_t pieces = ceil_div(H, 16 / size);
     const int waves = pieces <= 64 ? 1 : pieces <= 128 ? 2 : 4;
-    auto fn = type == SGEMM_TYPE_BF16
-                  ? (k <= 4 ? backward_of<bf16, 4>(waves) : backward_of<bf16, 8>(waves))
-                  : (k <= 4 ? backward_of<float, 4>(waves) : backward_of<float, 8>(waves));
+    const auto fn = type == SGEMM_TYPE_BF16 ? backward_of<bf16>(k, waves) : backward_of<float>(k, waves);
     const int64_t blocks = ceil_div(tokens, 4 / waves);
     fn<<<dim3((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks)), dim3(256), 0, stream>>>(a);
     return (int)hipGetLastError();

@@ -6,6 +6,7 @@
 // token once, so neither direction needs atomics, and sums have one order.
 #pragma once
 
+#include <climits>
 #include <type_traits>
 
 #include "lm_tile.hpp"
@@ -224,10 +225,8 @@ template <typename T> struct Single {
     __device__ __forceinline__ void zero() { v[0] = (T)0.f; }
 };
 
-// Choices of a token that are handled together: their rows are all in flight at once.
-constexpr int kChoices = 8;
-
-// Up to N choices of a token from j0 on: their places and weights.
+// Up to N choices of a token from j0 on: their places and weights.  The kernels handle KT at a
+// time, whose rows are all in flight at once.
 template <bool UNIFORM, int N> struct Choices {
     int p[N];
     float w[N];
@@ -249,49 +248,71 @@ template <bool UNIFORM, int N> struct Choices {
     __device__ __forceinline__ bool dropped(int j) const { return (uint32_t)(-2 - p[j]) < rows; }
 };
 
-// Which token and column a workgroup's turn b is for.  UNIFORM: a wave has one token, and the
-// compiler is told so: its places and weights then are scalar loads, and its rows' addresses a
-// scalar base each, where vector loads of them would be two more for each of a row.
-template <bool UNIFORM, int E>
-__device__ __forceinline__ bool turn_of(const RouteArgs &a, int64_t b, int parts, int &t, int &h0)
+// Turns of workgroups over the tokens' rows: `parts` of a row's whole pieces, each a thread.
+template <int E> struct Turns {
+    int cols, per, parts;
+    int64_t count;
+    __device__ __forceinline__ explicit Turns(const RouteArgs &a)
+        : cols(1 << a.cols_log2), per(256 >> a.cols_log2)
+    {
+        parts = (a.H / E + cols - 1) >> a.cols_log2;
+        if (parts == 0) parts = 1;
+        count = ((int64_t)a.tokens + per - 1) / per * parts;
+    }
+    // Turn b: which `per` tokens, and which part of their rows.
+    __device__ __forceinline__ int64_t tokens(int64_t b, int &part) const
+    {
+        part = 0;
+        if (parts == 1) return b;
+        if (b <= INT_MAX) {  // 32 bits: a division of 64 is a hundred instructions
+            const uint32_t q = (uint32_t)b / (uint32_t)parts;
+            part = (int)((uint32_t)b - q * parts);
+            return q;
+        }
+        part = (int)(b % parts);
+        return b / parts;
+    }
+};
+
+// f(piece, column) for what this thread has of a row in a part of it: a whole piece, and, in the
+// first part, the values after the last whole piece, one each for as many threads.
+template <typename T, typename F>
+__device__ __forceinline__ void row_pieces(const RouteArgs &a, int cols, int col, int part, F f)
 {
-    const int cols = 1 << a.cols_log2, per = 256 >> a.cols_log2;
-    const int col = threadIdx.x & (cols - 1);
-    int sub = threadIdx.x >> a.cols_log2;
-    if constexpr (UNIFORM) sub = __builtin_amdgcn_readfirstlane(sub);
-    const int64_t at = b / parts * per + sub;
-    const uint32_t h = ((uint32_t)(b % parts) * cols + col) * E;  // may pass 2^31
-    t = (int)at;
-    h0 = (int)h;
-    return at < a.tokens && h < (uint32_t)a.H;
+    constexpr int E = Piece<T>::E;
+    const uint32_t h = ((uint32_t)part * cols + col) * E, whole = (uint32_t)a.H / E * E;
+    if (h < whole) f(Piece<T>(), (int)h);
+    if (part == 0)
+        for (uint32_t at = whole + col; at < (uint32_t)a.H; at += cols) f(Single<T>(), (int)at);
 }
 
-__device__ __forceinline__ int parts_of_row(const RouteArgs &a, int e)
+// The token of a workgroup's turn.  UNIFORM: a wave has one, and the compiler is told so: its
+// places and weights then are scalar loads, and its rows' addresses a scalar base each, where
+// vector loads of them would be two more for each of a row.
+template <bool UNIFORM>
+__device__ __forceinline__ int64_t token_of(const RouteArgs &a, int64_t turn, int per)
 {
-    return ((a.H + e - 1) / e + (1 << a.cols_log2) - 1) >> a.cols_log2;
-}
-__device__ __forceinline__ int64_t turns(const RouteArgs &a, int parts)
-{
-    const int per = 256 >> a.cols_log2;
-    return ((int64_t)a.tokens + per - 1) / per * parts;
+    int sub = threadIdx.x >> a.cols_log2;
+    if constexpr (UNIFORM) sub = __builtin_amdgcn_readfirstlane(sub);
+    return turn * per + sub;
 }
 
 // R[place] <- w X[t], a thread per 16 bytes of a token.
-template <typename T, bool WEIGHTED, bool UNIFORM>
+template <typename T, int KT, bool WEIGHTED, bool UNIFORM>
 __global__ void __launch_bounds__(256) gather_kernel(RouteArgs a)
 {
-    constexpr int E = Piece<T>::E;
-    const int parts = parts_of_row(a, E);
-    const int64_t work = turns(a, parts);
-    for (int64_t b = blockIdx.x; b < work; b += gridDim.x) {
-        int t, h;
-        if (!turn_of<UNIFORM, E>(a, b, parts, t, h)) continue;
+    const Turns<Piece<T>::E> turns(a);
+    for (int64_t b = blockIdx.x; b < turns.count; b += gridDim.x) {
+        int part;
+        const int64_t at_token = token_of<UNIFORM>(a, turns.tokens(b, part), turns.per);
+        if (at_token >= a.tokens) continue;
+        const int t = (int)at_token;
         const auto copy = [&](auto x, int at) {
             x.load(static_cast<const T *>(a.X) + t * a.ldx + at);
-            for (int j0 = 0; j0 < a.k; j0 += kChoices) {
-                const Choices<UNIFORM, kChoices> c(a, t, j0, WEIGHTED);
+            for (int j0 = 0; j0 < a.k; j0 += KT) {
+                const Choices<UNIFORM, KT> c(a, t, j0, WEIGHTED);
 #pragma unroll
-                for (int j = 0; j < kChoices; ++j) {
+                for (int j = 0; j < KT; ++j) {
                     auto y = x;
                     if (c.held(j)) {
                         if constexpr (WEIGHTED) {
@@ -306,35 +327,32 @@ __global__ void __launch_bounds__(256) gather_kernel(RouteArgs a)
                 }
             }
         };
-        if (h + E <= a.H)
-            copy(Piece<T>(), h);
-        else
-            for (; h < a.H; ++h) copy(Single<T>(), h);
+        row_pieces<T>(a, turns.cols, threadIdx.x & (turns.cols - 1), part, copy);
     }
 }
 
 // out[t] <- beta out[t] + sum_j w R[place], a thread per 16 bytes of a token.
-template <typename T, bool UNIFORM>
+template <typename T, int KT, bool UNIFORM>
 __global__ void __launch_bounds__(256) combine_kernel(RouteArgs a)
 {
-    constexpr int E = Piece<T>::E;
-    const int parts = parts_of_row(a, E);
-    const int64_t work = turns(a, parts);
-    for (int64_t b = blockIdx.x; b < work; b += gridDim.x) {
-        int t, h;
-        if (!turn_of<UNIFORM, E>(a, b, parts, t, h)) continue;
+    const Turns<Piece<T>::E> turns(a);
+    for (int64_t b = blockIdx.x; b < turns.count; b += gridDim.x) {
+        int part;
+        const int64_t at_token = token_of<UNIFORM>(a, turns.tokens(b, part), turns.per);
+        if (at_token >= a.tokens) continue;
+        const int t = (int)at_token;
         const auto sum_up = [&](auto y, int at) {
             float sum[y.E];
 #pragma unroll
             for (int i = 0; i < y.E; ++i) sum[i] = 0.f;
-            for (int j0 = 0; j0 < a.k; j0 += kChoices) {
-                const Choices<UNIFORM, kChoices> c(a, t, j0, a.weights != nullptr);
-                decltype(y) x[kChoices];
+            for (int j0 = 0; j0 < a.k; j0 += KT) {
+                const Choices<UNIFORM, KT> c(a, t, j0, a.weights != nullptr);
+                decltype(y) x[KT];
 #pragma unroll
-                for (int j = 0; j < kChoices; ++j)
+                for (int j = 0; j < KT; ++j)
                     if (c.held(j)) x[j].load(static_cast<const T *>(a.R) + c.p[j] * a.ldr + at);
 #pragma unroll
-                for (int j = 0; j < kChoices; ++j)
+                for (int j = 0; j < KT; ++j)
                     if (c.held(j))
 #pragma unroll
                         for (int i = 0; i < y.E; ++i) sum[i] = fmaf(c.w[j], (float)x[j].v[i], sum[i]);
@@ -349,10 +367,7 @@ __global__ void __launch_bounds__(256) combine_kernel(RouteArgs a)
             for (int i = 0; i < y.E; ++i) y.v[i] = (T)sum[i];
             y.store(out);
         };
-        if (h + E <= a.H)
-            sum_up(Piece<T>(), h);
-        else
-            for (; h < a.H; ++h) sum_up(Single<T>(), h);
+        row_pieces<T>(a, turns.cols, threadIdx.x & (turns.cols - 1), part, sum_up);
     }
 }
 
@@ -413,13 +428,10 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(RouteArgs a)
                                     dot[j] = fmaf((float)d.v[i], (float)x[j].v[i], dot[j]);
                     }
                 };
-                for (uint32_t h = ((wave % WAVES) * 64 + lane) * E; h < (uint32_t)a.H;
-                     h += WAVES * 64 * E) {
-                    if (h + E <= (uint32_t)a.H)
-                        both(Piece<T>(), (int)h);
-                    else
-                        for (int at = (int)h; at < a.H; ++at) both(Single<T>(), at);
-                }
+                constexpr int THREADS = WAVES * 64;
+                const uint32_t thread = (wave % WAVES) * 64 + lane, whole = (uint32_t)a.H / E * E;
+                for (uint32_t h = thread * E; h < whole; h += THREADS * E) both(Piece<T>(), (int)h);
+                if (whole + thread < (uint32_t)a.H) both(Single<T>(), (int)(whole + thread));
             }
             if (!a.dweights) continue;
             // While several sums are left a lane exchanges half of them for its neighbour's other

@@ -172,7 +172,8 @@ def test_places_outside_the_rows_are_left_out():
 
 # One, two and four waves a token (by H), four and eight choices at a time (by k).
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("T,k,H", SHAPES + [(4097, 3, 40), (5000, 9, 700), (40, 5, 900)])
+@pytest.mark.parametrize("T,k,H", SHAPES + [(4097, 3, 40), (5000, 9, 700), (40, 5, 900), (20, 2, 1000), (20, 3, 1000), (20, 2, 400),
+                                            (20, 3, 400)])
 @pytest.mark.parametrize("pad,shift", [(0, 0), (3, 1)])
 def test_combine_backward(dtype, T, k, H, pad, shift):
     say("combine backward", dtype, T, k, H, pad, shift)

@@ -84,20 +84,20 @@ inline int rows_tile(int size, bool fast, int64_t used, int64_t rows, int64_t N,
     return choose_tile(size, F_ROWS_N, fast, row_tiles, N, K, cus);
 }
 
-// 8-bit products.  As above, with the contraction in pairs of bytes (a slab is 64), and `alone`:
-// what a tile costs, in those of a unit that is never idle, where it is the unit's only one.
-// Rates are those of 8192 x 4096 x 14336 (439 us with the 256 tile; 479, 557, 657, 915 and 2110
-// us with the smaller ones); alone and lead were fitted to the times of all tiles on 86 sizes
-// of 17 to 32768 rows: the rule's choice is 2.0% slower than the best of them on average, 3.0%
-// with the bf16 tiles' costs.
+// 8-bit products.  As above, with the contraction in pairs of bytes (a slab is 64); a unit takes two
+// tiles at a time (of the 256 tile one), and where a last one has the unit to itself it costs
+// `alone`, in tiles of a unit that is never idle.  Rates are those of 8192 x 4096 x 14336 (439 us
+// with the 256 tile; 479, 557, 657, 915 and 2110 us with the smaller ones); alone and lead were
+// fitted to the times of all tiles on 86 sizes of 17 to 32768 rows: the rule's choice is 1.1%
+// slower than the best of them on average, 3.0% with the bf16 tiles' rule and costs.
 struct ByteTileCost {
     int bm, bn;
     double rate, alone;
     int lead;
 };
 constexpr ByteTileCost kI8Tiles[NUM_TILES] = {
-    {16, 64, 0.21, 2.8, 64}, {32, 128, 0.48, 0.85, 256}, {0, 0, 0, 0, 0}, {64, 128, 0.67, 1.25, 96},
-    {128, 128, 0.79, 1.4, 64}, {128, 192, 0.92, 0.95, 96}, {256, 256, 1.0, 1.05, 64}};
+    {16, 64, 0.21, 0.7, 384}, {32, 128, 0.48, 0.9, 384}, {0, 0, 0, 0, 0}, {64, 128, 0.67, 1.55, 128},
+    {128, 128, 0.79, 1.4, 96}, {128, 192, 0.92, 1.65, 64}, {256, 256, 1.0, 0.9, 128}};
 
 template <typename RowTiles>
 int byte_tile(bool fast, RowTiles row_tiles, int64_t N, int64_t K, int cus)
@@ -108,8 +108,9 @@ int byte_tile(bool fast, RowTiles row_tiles, int64_t N, int64_t K, int cus)
         const ByteTileCost &t = kI8Tiles[i];
         if (t.bm == 0) continue;
         const int64_t tiles = row_tiles(t.bm) * ceil_div(N, t.bn);
-        double rounds = i == T256 ? (double)ceil_div(tiles, cus) : 0.5 * ceil_div(2 * tiles, cus);
-        if (tiles <= cus || rounds < t.alone) rounds = t.alone;
+        const int64_t left = tiles % (2 * cus);
+        double rounds = (double)(tiles / (2 * cus)) * 2 + (left == 0 ? 0 : left <= cus ? t.alone : 2);
+        if (i == T256) rounds = tiles <= cus ? t.alone : (double)ceil_div(tiles, cus);
         const double cost = rounds * t.bm * t.bn * (0.5 * K + t.lead) / t.rate;
         if (i == 0 || cost < least) best = i, least = cost;
     }

@@ -28,12 +28,12 @@ extern "C" int rule(int fast, int64_t used, int64_t rows, int64_t N, int64_t K)
 }
 """
 # (rows, N, K) of one group and (groups, rows, N, K), by whether the operands take direct loads.
-ONE = {True: [(18, 33, 35), (35, 1001, 310), (8270, 66, 34), (12309, 145, 34), (16707, 131, 175), (910, 12438, 33),
+ONE = {True: [(18, 33, 35), (2071, 67, 102), (2094, 66, 33), (16789, 34, 34), (17794, 129, 38), (16512, 650, 68),
               (300, 2060, 4100)],
-       False: [(18, 33, 35), (35, 1001, 311), (8270, 66, 33), (12309, 145, 33), (300, 2060, 4099)]}
-GROUPS = {True: [(1, 18, 33, 35), (3, 40, 34, 310), (3, 8270, 66, 34), (33, 11633, 147, 34), (36, 4254, 923, 43),
-                 (16, 2219, 3932, 33), (32, 2048, 1530, 2000)],
-          False: [(1, 18, 33, 35), (3, 40, 34, 311), (3, 8270, 66, 33), (33, 11633, 147, 35), (8, 2000, 700, 1517)]}
+       False: [(18, 33, 35), (2071, 67, 102), (2094, 66, 33), (16789, 34, 34), (300, 2060, 4099)]}
+GROUPS = {True: [(1, 18, 33, 35), (1, 4314, 34, 94), (2, 2094, 66, 33), (19, 15982, 34, 35), (5, 22, 13207, 34),
+                 (28, 4680, 2004, 70), (32, 2048, 1530, 2000)],
+          False: [(1, 18, 33, 35), (1, 4314, 34, 94), (2, 2094, 66, 33), (19, 15982, 34, 35), (8, 2000, 700, 1517)]}
 
 
 def _load():
@@ -75,7 +75,7 @@ def test_every_tile_is_reached():
 def test_one_group(dtype, fast, case):
     rows, N, K = case
     say("q8 tiles", dtype, case)
-    ld = -(-K // 4) * 4 if fast else K
+    ld = -(-K // 4) * 4 + (0 if fast else 1)
     X, W = bytes_of((rows, ld), 1)[:, :K], bytes_of((N, ld), 2)[:, :K]
     sx, sw = positive((rows,), 3), positive((N,), 4)
     ref = product(X, sx, W, sw)
@@ -99,7 +99,7 @@ def test_groups(dtype, fast, case):
     cuts = sorted(rng.randrange(rows + 1) for _ in range(groups - 1))
     sizes = [b - a for a, b in zip([0] + cuts, cuts + [rows])]
     ends, off = offsets_of(sizes, first=1)
-    ld = -(-K // 4) * 4 if fast else K
+    ld = -(-K // 4) * 4 + (0 if fast else 1)
     X, W = bytes_of((rows + 4, ld), 1)[:, :K], bytes_of((groups, N, ld), 2)[..., :K]
     sx, sw = positive((rows + 4,), 3), positive((groups, N), 4)
     Y = sg.q8_gemm(X, sx, W, sw, off, dtype=dtype)

@@ -109,8 +109,28 @@ __device__ __forceinline__ void load_values(const T *row, int k, int K, float (&
         for (int i = 0; i < N; ++i) v[i] = (float)x[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = k + i < K ? (float)row[k + i] : 0.f;
+        for (int i = 0; i < N; ++i) {
+            const float x = K > 0 ? (float)row[k + i < K ? k + i : K - 1] : 0.f;
+            v[i] = k + i < K ? x : 0.f;
+        }
     }
+}
+
+// The first `left` of 16 bytes, zeros after them.  (Each byte of a part is a load of its own, all in
+// flight at once: past the last the last is read again.)
+template <typename B> __device__ __forceinline__ u32x4 load_bytes(const B *p, int left)
+{
+    u32x4 q = {0, 0, 0, 0};
+    if (left >= 16) {
+        __builtin_memcpy(&q, p, 16);
+    } else if (left > 0) {
+        uint32_t b[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) b[i] = (uint8_t)p[i < left ? i : left - 1];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) q[i / 4] |= (i < left ? b[i] : 0u) << (8 * (i % 4));
+    }
+    return q;
 }
 
 template <int N> __device__ __forceinline__ uint32_t max_of(const float (&v)[N], uint32_t m)
@@ -339,14 +359,7 @@ __global__ void __launch_bounds__(kVecWaves * 64) q8_vec_kernel(VecArgs a)
                     const int row = h ? frow2 : frow, c = (h ? fchunk2 : fchunk) * 16;
                     const char *q = p + row * a.ldw + c;
                     const int room = more && n0 + row < a.N ? a.K - k - c : 0;
-                    hold[h] = u32x4{0, 0, 0, 0};
-                    if (room >= 16) {
-                        __builtin_memcpy(&hold[h], q, 16);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (i < room) hold[h][i / 4] |= (uint32_t)(uint8_t)q[i] << (8 * (i % 4));
-                    }
+                    hold[h] = load_bytes(q, room);
                 }
             }
             if (++f_slab >= ns) f_slab = 0, f_tile += gridDim.x;
@@ -369,16 +382,7 @@ __global__ void __launch_bounds__(kVecWaves * 64) q8_vec_kernel(VecArgs a)
             if (threadIdx.x < R) scales[threadIdx.x] = a.x_scales[first + threadIdx.x];
             for (int i = threadIdx.x; i < R * a.slabs * 8; i += kVecWaves * 64) {
                 const int r = i / (a.slabs * 8), c = i - r * (a.slabs * 8), left = a.K - c * 16;
-                const int8_t *x = X + r * a.ldx + c * 16;
-                u32x4 q = {0, 0, 0, 0};
-                if (left >= 16) {
-                    __builtin_memcpy(&q, x, 16);
-                } else {
-#pragma unroll
-                    for (int b = 0; b < 16; ++b)
-                        if (b < left) q[b / 4] |= (uint32_t)(uint8_t)x[b] << (8 * (b % 4));
-                }
-                *chunk_of(r, c) = q;
+                *chunk_of(r, c) = load_bytes(X + r * a.ldx + c * 16, left);
             }
         } else {
             int per = 1;  // waves of a row

@@ -635,6 +635,77 @@ tile_kernel(TileArgs g)
             advance();
         }
         wait_slab_barrier<0>();  // nothing may land in LDS any more
+    } else if constexpr (std::is_same<T, int8_t>::value) {
+        // Rows at any byte: 16-byte loads into registers, two slabs ahead.  They are kept free of
+        // branches but at the operand's end: rows past the last repeat it (and are not
+        // stored), and values past K meet A's, which are cleared in the last slab.
+        static_assert(LA == KC && LB == KC, "bytes are contiguous along the contraction");
+        u32x4 hold0[LPW], hold1[LPW];
+        const uint8_t *ends[2] = {reinterpret_cast<const uint8_t *>(pa) + left_a,
+                                  reinterpret_cast<const uint8_t *>(pb) + left_b};
+        const uint8_t *src[LPW];
+        int at[LPW];
+#pragma unroll
+        for (int i = 0; i < LPW; ++i) {
+            int row, chunk;
+            slot(i, row, chunk);
+            const int rows = ua[i] ? a_rows : b_rows;
+            at[i] = chunk * EPC;
+            src[i] = reinterpret_cast<const uint8_t *>(ua[i] ? pa : pb) +
+                     (int64_t)(row < rows ? row : rows - 1) * (ua[i] ? g.lda : g.ldb) + at[i];
+        }
+        auto fetch = [&](int t, u32x4(&hold)[LPW]) {
+            if (t >= slabs) return;
+#pragma unroll
+            for (int i = 0; i < LPW; ++i) {
+                const uint8_t *p = src[i] + (int64_t)t * BK, *end = ends[ua[i] ? 0 : 1];
+                if (p + 16 <= end) {
+                    __builtin_memcpy(&hold[i], p, 16);
+                } else {
+                    hold[i] = u32x4{0, 0, 0, 0};
+                    for (int j = 0; j < 16; ++j)
+                        if (p + j < end) hold[i][j / 4] |= (uint32_t)p[j] << (8 * (j % 4));
+                }
+            }
+        };
+        auto put = [&](int t, u32x4(&hold)[LPW]) {
+            if (t >= slabs) return;
+            const bool last = t + 1 == slabs;
+#pragma unroll
+            for (int i = 0; i < LPW; ++i) {
+                u32x4 v = hold[i];
+                if (last && ua[i]) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int keep = K - t * BK - at[i] - 4 * w;  // bytes of this word
+                        v[w] = keep >= 4 ? v[w] : keep <= 0 ? 0u : v[w] & ((1u << (8 * keep)) - 1u);
+                    }
+                }
+                *reinterpret_cast<u32x4 *>(lds + (t & 1) * STAGE + uat[i] + lane * 16) = v;
+            }
+        };
+        // Slab t runs; t + 1 is in flight in `next`; t + 2 goes where t was held.
+        auto step = [&](int t, u32x4(&free)[LPW], u32x4(&next)[LPW]) {
+            if (t >= slabs) return;
+            fetch(t + 2, free);
+            Frag a[KS][FM], b[KS][FN];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) read_op(r, lds + (t & 1) * STAGE, h, a, b);
+                products(a, b, [](int) {});
+            }
+            put(t + 1, next);
+            __syncthreads();
+        };
+        fetch(0, hold0);
+        fetch(1, hold1);
+        put(0, hold0);
+        __syncthreads();
+        for (int t = 0; t < slabs; t += 2) {
+            step(t, hold0, hold1);
+            step(t + 1, hold1, hold0);
+        }
     } else {
         u32x4 hold[LPW];
         auto fetch = [&](int t) {

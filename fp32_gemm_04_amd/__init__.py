@@ -838,7 +838,8 @@ def expert_combine_backward(dout, R, place, weights=None, dR=None, need_dR: bool
 
     dout: (tokens, H); R: (rows, H) as the forward pass had it.  dR: (rows, H), whose rows
     without a choice are left as they were; when None it is allocated, and rows of dropped
-    choices are zero (for a place that ``expert_sort`` did not give, give ``dR``).
+    choices are zero (for a place that ``expert_sort`` did not give, give ``dR``).  A row that several
+    choices share would need the sum of their gradients, which this does not compute.
     dweights: (tokens, k) float32, 0 for a dropped choice.  One that is not needed is not
     computed and comes back as None.
     """
@@ -875,7 +876,8 @@ def q8_quantize(X, place=None, stream=None):
     bfloat16.  Q: int8 of the same shape, rows padded to a multiple of 16 bytes; scales: float32,
     one for each row.  With ``place`` ((rows, k) int32, as ``expert_sort`` gives it; X 2-D) row
     t goes to the k rows place[t] of (rows * k, K), sorted by expert; those of dropped choices are
-    zero.  A row with an infinity or a NaN gets the scale NaN.
+    zero (for a place of another origin, rows that it does not name hold anything).  A row with an infinity or a
+    NaN gets the scale NaN.
     """
     t = _type_of(X, "X")
     dev, lead = X.device, tuple(X.shape[:-2])
@@ -949,15 +951,16 @@ def q8_gemm(X, x_scales, Q, scales, offsets=None, Y=None, dtype=torch.bfloat16, 
     return Y
 
 
-# Values of X up to which every workgroup quantises them for itself.  us, that and two launches:
-# 4 rows, 4096 x 4096 8.8 and 10.1, 8 rows 10.8 and 10.9, 16 rows 14.8 and 12.3, 12 rows, 8192 x
-# 28001 60.5 and 53.0.
-_MOST_MATVEC = 32768
+# Values of X up to which every workgroup quantises them for itself, where it takes them in one pass.  us
+# a call (in a graph), that and two launches: 1 row, 4096 x 4096 8.4 and 12.7 (8.5 and 9.5), 4 rows 10.1
+# and 13.3 (10.5 and 9.8), 8 rows 13.7 and 13.2 (14.4 and 9.9), 16 rows, 1024 x 1024 8.8 and 13.5 (9.0 and 6.8),
+# 2048 x 4096 12.1 and 13.5 (12.4 and 7.4).
+_MOST_MATVEC = 16384
 
 
 def q8_matvec(X, Q, scales, Y=None, offsets=None, stream=None):
     """Y <- ``q8_gemm(*q8_quantize(X), Q, scales)``, bit for bit, for a few rows of X: with at most
-    32768 values of X in one launch (``sgemm_q8_matvec``), with more in those two.
+    16 rows (4 a group) and 16384 values of X in one launch (``sgemm_q8_matvec``), with more in those two.
 
     X: (rows, K), float32 or bfloat16, K at most 131071; Q and scales as in ``q8_gemm``; Y:
     (rows, N) of X's type, allocated when None (its rows outside every group zero).  Returns Y.
@@ -977,7 +980,7 @@ def q8_matvec(X, Q, scales, Y=None, offsets=None, stream=None):
         if Y is None:
             Y = X.new_empty(rows, N)
         stride = _groups_of(Q) if offsets is not None else 0
-        if rows * K > _MOST_MATVEC:
+        if rows * K > _MOST_MATVEC or rows > (4 * groups if off else 16) or groups > 65535:
             ldq = -(-K // 16) * 16
             ws = X.new_empty(rows * (ldq + 4), dtype=torch.uint8)
             q = ws.data_ptr()

@@ -26,8 +26,6 @@ TileKernel of_type(bool grouped, int tile, bool fast)
         return entry<TC, 128, 128, 2, 2, 2, 16, 2, false>(grouped);
     }
     switch (tile) {
-    case S16: return entry<TC, 16, 64, 1, 4, 4, 16, 4, true>(grouped);
-    case M32: return entry<TC, 32, 128, 1, 4, 4, 16, 2, true>(grouped);
     case M64: return entry<TC, 64, 128, 2, 2, 3, 16, 2, true>(grouped);
     case T128: return entry<TC, 128, 128, 2, 2, 2, 16, 2, true>(grouped);
     case T192: return entry<TC, 128, 192, 2, 2, 2, 16, 2, true>(grouped);

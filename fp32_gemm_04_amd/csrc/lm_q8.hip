@@ -33,6 +33,26 @@ template <typename T, bool PLACED> auto quantize_of(int waves)
                         : q8_quantize_kernel<T, 4, PLACED>;
 }
 
+template <typename TY, int BM, int BN, int DEPTH> TileKernel split_entry(bool grouped)
+{
+    return TileKernel{grouped ? (TileFn)q8_split_kernel<TY, BM, BN, DEPTH, true>
+                              : (TileFn)q8_split_kernel<TY, BM, BN, DEPTH, false>,
+                      BM, BN, kSplitWaves * 64};
+}
+template <typename TY> TileKernel split_of(bool grouped, int split)
+{
+    switch (split) {
+    case 0: return split_entry<TY, 16, 32, 2>(grouped);
+    case 1: return split_entry<TY, 32, 32, 2>(grouped);
+    case 2: return split_entry<TY, 32, 64, 1>(grouped);
+    default: return split_entry<TY, 64, 64, 1>(grouped);
+    }
+}
+TileKernel split_kernel(bool bf16_out, bool grouped, int split)
+{
+    return bf16_out ? split_of<bf16>(grouped, split) : split_of<float>(grouped, split);
+}
+
 // A product of few rows: X is int8 with scales, or of the results' type.
 int vec_product(VecArgs &a, bool bytes, bool bf16_out, int cus, hipStream_t stream)
 {
@@ -133,20 +153,17 @@ extern "C" int sgemm_q8_gemm(int type, int groups, int rows, int N, int K, const
     const int cus = compute_units(&rc);
     if (cus == 0) return rc;
     const bool bf16_out = type == SGEMM_TYPE_BF16;
-    // Few rows: every workgroup streams weights.  us, this and the smallest tile: 16 rows, 4096 x
-    // 4096 9.1 and 13.0, 12 rows, 8192 x 28001 48.5 and 51.2, 16 rows, 4096 x 14336 17.9 and 16.1, 24 rows
-    // 4096 x 4096 13.2 and 13.2; 3 rows a group, 64 groups of 2048 x 1408 33.8 and 37.9, 8 rows, 32
-    // groups of 2048 x 1536 34.5 and 26.2.
-    if (K <= kVecRows && groups <= 65535 && rows <= (offsets ? 4 * (int64_t)used : 16)) {
+    const bool fast = K == 0 || (q8_fast(X, ldx, 0) && q8_fast(W, ldw, stride_w));
+    if (K <= kVecRows && byte_few_rows(fast, offsets ? groups : 0, used, rows)) {
         VecArgs v = {};
         v.X = X, v.x_scales = x_scales, v.W = W, v.w_scales = w_scales, v.Y = Y, v.offsets = offsets;
         v.ldx = ldx, v.ldw = ldw, v.stride_w = stride_w, v.ldy = ldy;
         v.rows = rows, v.N = N, v.K = K, v.groups = groups, v.fill = offsets && fill;
         return vec_product(v, true, bf16_out, cus, stream);
     }
-    const bool fast = K == 0 || (q8_fast(X, ldx, 0) && q8_fast(W, ldw, stride_w));
     const int tile = byte_rows_tile(fast, offsets ? used : 0, rows, N, K, cus);
-    const TileKernel k = i8_kernel(bf16_out, offsets != nullptr, tile, fast);
+    const TileKernel k = tile >= NUM_TILES ? split_kernel(bf16_out, offsets != nullptr, tile - NUM_TILES)
+                                           : i8_kernel(bf16_out, offsets != nullptr, tile, fast);
     TileArgs a = {};
     a.A = X, a.B = W, a.C = Y;
     a.lda = ldx, a.ldb = ldw, a.ldc = ldy;

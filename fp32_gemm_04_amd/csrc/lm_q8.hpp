@@ -252,8 +252,8 @@ __global__ void __launch_bounds__(256) q8_quantize_kernel(QuantArgs a)
 
 // ------------------------------------------------------------- a few rows
 
-// Y[r][n] for a few rows: every weight is used once a row, so the time is that of reading the
-// weights.  A workgroup of eight waves puts its rows into LDS once, quantising them where TX is
+// Y[r][n] for a few rows that are quantised on the way, have weights at odd bytes or more than 64
+// groups: every weight is used once a row, so the time is that of reading the weights.  A workgroup of eight waves puts its rows into LDS once, quantising them where TX is
 // not int8, then takes tiles of 16
 // columns; the waves split the contraction, slab by slab of 128 bytes, and their integer sums
 // meet in LDS.  Weights travel through a ring of LDS of each wave's own by direct loads,
@@ -477,6 +477,179 @@ __global__ void __launch_bounds__(kVecWaves * 64) q8_vec_kernel(VecArgs a)
         if constexpr (FAST) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();  // the rows and the rings may be written again
     }
+}
+
+// ------------------------------------------------------ tens of rows
+
+// A tile of BM x BN whose contraction the workgroup's waves split, slab by slab of 128 bytes.  With tens
+// to hundreds of rows the operands come from L2, and the tiles have to be small for every unit to have
+// some; waves that split such a tile among them wait for each other at every slab and read LDS several times
+// over.  Here each wave has a ring of its own, no barrier before the end of the contraction, and
+// reads each byte of LDS once; the sums, exact in any order, meet in LDS.  Rings are short, so that a unit
+// has two or three workgroups.  us in a graph, K = N = 4096, with this and with the best of the tile
+// kernels: 16 rows 5.7 and 13.0, 64 rows 7.1 and 13.4, 128 rows 9.1 and 13.7, 256 rows 12.4 and 13.9, 512 rows
+// 18.7 and 17.5; 64 rows with K 14336 14.4 and 35.0; 64 rows of tiles of 32 x 32 with eight waves
+// 7.5, with rings of three slabs 6.9 against 6.6, tiles of 64 x 16 7.5, 64 x 32 8.6.
+constexpr int kSplitWaves = 4;
+
+// Workgroups a unit's LDS has room for.
+constexpr int split_room(int ring)
+{
+    return 160 * 1024 / ring;
+}
+
+template <typename TY, int BM, int BN, int DEPTH, bool GROUPED>
+__global__ void __launch_bounds__(kSplitWaves * 64)
+    __attribute__((amdgpu_waves_per_eu(split_room(kSplitWaves * DEPTH * (BM + BN) * 128))))
+q8_split_kernel(TileArgs g)
+{
+    constexpr int WAVES = kSplitWaves;
+    constexpr int STAGE = (BM + BN) * 128, LPW = STAGE / 1024, FM = BM / 16, FN = BN / 16;
+    constexpr int RING = WAVES * DEPTH * STAGE;
+    // Columns whose sums of all waves fit the rings at once.
+    constexpr int BLOCK = WAVES * BM * 16 * 4, FIT = RING / BLOCK, COLS = FIT >= FN ? FN : FN % FIT == 0 ? FIT : 1;
+    static_assert(FIT >= 1 && FN % COLS == 0, "whole blocks of columns");
+    static_assert(LPW * (DEPTH - 1) <= 63, "loads in flight must fit the vmcnt field");
+    __shared__ __attribute__((aligned(1024))) char lds[RING];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    TY *C = static_cast<TY *>(g.C);
+
+    int tm, tn, group = 0, begin = 0, end = g.M;
+    if constexpr (GROUPED) {
+        if (!rows_tile_of_block(g, BM, BN, tm, tn, group, begin, end)) {
+            if (g.fill) zero_outside(g.offsets, g.groups, g.M, g.N, C, g.ldc);
+            return;
+        }
+    } else {
+        tile_of_block(blockIdx.x, (g.M + BM - 1) / BM, (g.N + BN - 1) / BN, 8, tm, tn);
+    }
+    const int first = begin + tm * BM, n0 = tn * BN;
+    const int rows = end - first < BM ? end - first : BM;
+    const char *pa = static_cast<const char *>(g.A) + first * g.lda;
+    const char *pb = static_cast<const char *>(g.B) + group * g.group_stride + n0 * g.ldb;
+    const int64_t left_a = (int64_t)(rows - 1) * g.lda + g.K;
+    const int64_t left_b = (int64_t)(g.N - 1 - n0) * g.ldb + g.K;
+    const int slabs = (g.K + 127) / 128;
+
+    // The results' columns and rows of this thread, and their scales, long before they are used.
+    constexpr int QUADS = COLS * 4, THREADS = WAVES * 64, ITEMS = (BM * QUADS + THREADS - 1) / THREADS;
+    static_assert(THREADS % QUADS == 0, "a thread's items are in one column");
+    const int out_col = threadIdx.x % QUADS * 4, out_row = threadIdx.x / QUADS;
+    const float *sb = g.scale_b + (int64_t)group * g.N;
+    float row_scale[ITEMS];
+    f32x4 col_scale[FN / COLS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        const int r = out_row + i * (THREADS / QUADS);
+        row_scale[i] = g.scale_a[first + (r < rows ? r : rows - 1)];
+    }
+#pragma unroll
+    for (int c = 0; c < FN / COLS; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int n = n0 + c * (COLS * 16) + out_col + q;
+            col_scale[c][q] = sb[n < g.N ? n : g.N - 1];
+        }
+
+    uint32_t voff[LPW];
+#pragma unroll
+    for (int i = 0; i < LPW; ++i) {
+        const int row = (i < BM / 8 ? i : i - BM / 8) * 8 + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
+        voff[i] = (uint32_t)row * (uint32_t)(i < BM / 8 ? g.lda : g.ldb) + chunk * 16u;
+    }
+    char *ring = lds + wave * (DEPTH * STAGE);
+    const auto fetch = [&](int t, int buf) {
+        // (Past the last slab: nothing is in range, and zeros are written.)
+        u32x4 ra = descriptor(pa + t * (int64_t)128, t < slabs ? left_a - t * (int64_t)128 : 0);
+        u32x4 rb = descriptor(pb + t * (int64_t)128, t < slabs ? left_b - t * (int64_t)128 : 0);
+        uint32_t at = (uint32_t)(uintptr_t)(lds_char *)ring + buf * STAGE;
+        // Wait states between a vector unit's write of these and their use.
+        asm volatile("s_nop 4" : "+s"(ra), "+s"(rb), "+s"(at));
+#pragma unroll
+        for (int i = 0; i < LPW; ++i) load_slab16(i < BM / 8 ? ra : rb, voff[i], at + i * 1024);
+    };
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) fetch(wave + d * WAVES, d);
+    i32x4 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    const int l16 = lane & 15, lg = lane >> 4;
+    int buf = 0;
+    for (int t = wave; t < slabs; t += WAVES) {
+        asm volatile("s_waitcnt vmcnt(%0)" : : "n"(LPW * (DEPTH - 1)) : "memory");
+        const char *slab = ring + buf * STAGE + l16 * 128;
+        i32x4 a[2][FM], b[2][FN];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int c = ((4 * k + lg) ^ ((l16 >> 1) & 7)) << 4;
+#pragma unroll
+            for (int i = 0; i < FM; ++i) a[k][i] = *reinterpret_cast<const i32x4 *>(slab + i * 2048 + c);
+#pragma unroll
+            for (int j = 0; j < FN; ++j) b[k][j] = *reinterpret_cast<const i32x4 *>(slab + BM * 128 + j * 2048 + c);
+        }
+        // Read before the buffer is filled again.
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        fetch(t + DEPTH * WAVES, buf);
+        buf = buf + 1 == DEPTH ? 0 : buf + 1;
+        if (t == slabs - 1 && g.K % 128) {
+            // What lies past K is anything: it meets zeros.
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int keep = g.K - t * 128 - (4 * k + lg) * 16 - 4 * w;  // bytes of this word
+                    const uint32_t mask = keep >= 4 ? ~0u : keep <= 0 ? 0u : (1u << (8 * keep)) - 1u;
+#pragma unroll
+                    for (int i = 0; i < FM; ++i) a[k][i][w] &= (int)mask;
+                }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[k][j], a[k][i], acc[i][j], 0, 0, 0);
+    }
+    // ---- the waves' sums meet in LDS: blocks of 16 x 16, a lane's four columns in one piece
+#pragma unroll
+    for (int c = 0; c < FN / COLS; ++c) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+        for (int j = 0; j < COLS; ++j)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+                *reinterpret_cast<i32x4 *>(lds + ((wave * COLS + j) * FM + i) * 1024 + (l16 * 4 + lg) * 16) =
+                    acc[i][c * COLS + j];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int r = out_row + i * (THREADS / QUADS), n = n0 + c * (COLS * 16) + out_col;
+            if (r >= rows || n >= g.N) continue;
+            const char *p = lds + ((out_col >> 4) * FM + (r >> 4)) * 1024 + ((r & 15) * 4 + (out_col >> 2 & 3)) * 16;
+            i32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) sum += *reinterpret_cast<const i32x4 *>(p + w * (COLS * FM * 1024));
+            typedef TY Vec __attribute__((ext_vector_type(4)));
+            typedef Vec Loose __attribute__((aligned(sizeof(TY))));
+            Vec y;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) y[q] = (TY)((float)sum[q] * row_scale[i] * col_scale[c][q]);
+            TY *out = C + (int64_t)(first + r) * g.ldc + n;
+            if (n + 4 <= g.N) {
+                *reinterpret_cast<Loose *>(out) = y;
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (n + q < g.N) out[q] = y[q];
+            }
+        }
+    }
+    if constexpr (GROUPED)
+        if (g.fill) zero_outside(g.offsets, g.groups, g.M, g.N, C, g.ldc);
 }
 
 }  // namespace lm

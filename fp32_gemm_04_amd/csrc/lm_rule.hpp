@@ -87,9 +87,12 @@ inline int rows_tile(int size, bool fast, int64_t used, int64_t rows, int64_t N,
 // 8-bit products.  As above, with the contraction in pairs of bytes (a slab is 64); a unit takes two
 // tiles at a time (of the 256 tile one), and where a last one has the unit to itself it costs
 // `alone`, in tiles of a unit that is never idle.  Rates are those of 8192 x 4096 x 14336 (439 us
-// with the 256 tile; 479, 557, 657, 915 and 2110 us with the smaller ones); alone and lead were
-// fitted to the times of all tiles on 86 sizes of 17 to 32768 rows: the rule's choice is 1.1%
-// slower than the best of them on average, 3.0% with the bf16 tiles' rule and costs.
+// with the 256 tile; 479, 557, 657, 915 and 2110 us with the smaller ones).  Operands of direct loads
+// have the contraction split over waves instead of the two smallest: there time goes with the bytes of
+// both operands.  alone and lead were fitted to the times of all on 86 sizes of 17 to 32768 rows, and
+// the split ones' to 390 sizes of 1 to 8192: the rule's choice is 2.3% slower than the best on
+// average; without the split ones the best is 20.6% slower, with one, two and three of them 3.6, 1.6
+// and 0.9%.
 struct ByteTileCost {
     int bm, bn;
     double rate, alone;
@@ -98,21 +101,33 @@ struct ByteTileCost {
 constexpr ByteTileCost kI8Tiles[NUM_TILES] = {
     {16, 64, 0.21, 0.7, 384}, {32, 128, 0.48, 0.9, 384}, {0, 0, 0, 0, 0}, {64, 128, 0.67, 1.55, 128},
     {128, 128, 0.79, 1.4, 96}, {128, 192, 0.92, 1.65, 64}, {256, 256, 1.0, 0.9, 128}};
+constexpr int kSplits = 4;
+constexpr ByteTileCost kI8Splits[kSplits] = {
+    {16, 32, 0.0321, 0.71, 1152}, {32, 32, 0.0295, 0.82, 1152}, {32, 64, 0.0264, 0.71, 832},
+    {64, 64, 0.026, 0.71, 1408}};
 
+// A tile, or NUM_TILES and which of the split ones.
 template <typename RowTiles>
 int byte_tile(bool fast, RowTiles row_tiles, int64_t N, int64_t K, int cus)
 {
-    int best = S16;
+    int best = -1;
     double least = 0;
-    for (int i = 0; i < (fast ? (int)NUM_TILES : T128 + 1); ++i) {
+    const auto offer = [&](int i, double cost) {
+        if (best < 0 || cost < least) best = i, least = cost;
+    };
+    for (int i = fast ? M64 : S16; i <= (fast ? T256 : T128); ++i) {
         const ByteTileCost &t = kI8Tiles[i];
         if (t.bm == 0) continue;
         const int64_t tiles = row_tiles(t.bm) * ceil_div(N, t.bn);
         const int64_t left = tiles % (2 * cus);
         double rounds = (double)(tiles / (2 * cus)) * 2 + (left == 0 ? 0 : left <= cus ? t.alone : 2);
         if (i == T256) rounds = tiles <= cus ? t.alone : (double)ceil_div(tiles, cus);
-        const double cost = rounds * t.bm * t.bn * (0.5 * K + t.lead) / t.rate;
-        if (i == 0 || cost < least) best = i, least = cost;
+        offer(i, rounds * t.bm * t.bn * (0.5 * K + t.lead) / t.rate);
+    }
+    for (int i = 0; fast && i < kSplits; ++i) {
+        const ByteTileCost &t = kI8Splits[i];
+        const double share = (double)(row_tiles(t.bm) * ceil_div(N, t.bn)) / cus;
+        offer(NUM_TILES + i, (share > t.alone ? share : t.alone) * (t.bm + t.bn) * (K + t.lead) / t.rate);
     }
     return best;
 }
@@ -126,6 +141,17 @@ inline int byte_rows_tile(bool fast, int64_t used, int64_t rows, int64_t N, int6
         return t > used ? t : used;
     };
     return byte_tile(fast, row_tiles, N, K, cus);
+}
+
+// Whether rows of one group (groups 0), or of `used` of the groups, are few enough for a workgroup to hold
+// them while it streams weights.  us, that and the best of the others: direct loads of one group, 1 row,
+// 4096 x 4096 5.4 and 5.7, 16 rows 8.3 and 5.7, 12 rows, 8192 x 28001 48.4 and 42.1; by group, 16 rows, 4 groups
+// of 2048 x 1536 5.8 and 5.3, 29 rows, 12 groups of 1136 x 1561 8.9 and 8.5, but 64 rows, 256 groups
+// of 2048 x 1408, each tile of which is found by counting all of them, 29.2 and 33.8.
+inline bool byte_few_rows(bool fast, int64_t groups, int64_t used, int64_t rows)
+{
+    if (fast && groups <= 64) return false;
+    return groups <= 65535 && rows <= (groups ? 4 * used : 16);
 }
 
 // For M x N outputs of each group, the contraction over its rows.

@@ -337,6 +337,43 @@ __device__ __forceinline__ int64_t scan_tiles(const int *offsets, int groups, in
     return sum;  // inclusive
 }
 
+// The workgroup's tile of its group, and the group's rows; false where there is none for it.
+__device__ __forceinline__ bool rows_tile_of_block(const TileArgs &g, int bm, int bn, int &tm, int &tn,
+                                                   int &group, int &begin, int &end)
+{
+    // (Up to 64 groups are counted once: a tile's first loads wait for this.)
+    int b, e, n;
+    int64_t sum = scan_tiles(g.offsets, g.groups, g.M, bm, 0, b, e, n);
+    int64_t all = __shfl((long long)sum, 63);
+    for (int g0 = 64; g0 < g.groups; g0 += 64) {
+        int b1, e1, n1;
+        all += __shfl((long long)scan_tiles(g.offsets, g.groups, g.M, bm, g0, b1, e1, n1), 63);
+    }
+    const int total = (int)(all < g.most_tiles ? all : g.most_tiles);
+    const int tiles_n = (g.N + bn - 1) / bn;
+    if ((int64_t)blockIdx.x >= (int64_t)total * tiles_n) return false;
+    tile_of_block(blockIdx.x, total, tiles_n, 8, tm, tn);
+    int64_t before = 0;
+    for (int g0 = 0; g0 < g.groups; g0 += 64) {
+        if (g0 > 0) sum = scan_tiles(g.offsets, g.groups, g.M, bm, g0, b, e, n);
+        const uint64_t past = __ballot(before + sum > tm);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            group = g0 + at;
+            begin = __shfl(b, at);
+            end = __shfl(e, at);
+            tm -= (int)(before + __shfl((long long)sum, at) - __shfl(n, at));
+            break;
+        }
+        before += __shfl((long long)sum, 63);
+    }
+    group = __builtin_amdgcn_readfirstlane(group);
+    begin = __builtin_amdgcn_readfirstlane(begin);
+    end = __builtin_amdgcn_readfirstlane(end);
+    tm = __builtin_amdgcn_readfirstlane(tm);
+    return true;
+}
+
 // WM x WN waves share the tile, NBUF slabs the ring; WPE waves per SIMD bound the registers.
 // What bounds it: the matrix cores where tiles have many rows (256 x 256, T 8192, H 2048, V
 // 131072: logits to row statistics 3.70-3.85 ms, 1140-1190 TF/s, the cores 56% busy at 2.0
@@ -376,40 +413,11 @@ tile_kernel(TileArgs g)
     // ---- which tile, of which group
     int tm, tn, group = 0, begin = 0, end = 0, m0;
     if constexpr (RG == ROWS) {
-        // (Up to 64 groups are counted once: a tile's first loads wait for this.)
-        int b, e, n;
-        int64_t sum = scan_tiles(g.offsets, g.groups, g.M, BM, 0, b, e, n);
-        int64_t all = __shfl((long long)sum, 63);
-        for (int g0 = 64; g0 < g.groups; g0 += 64) {
-            int b1, e1, n1;
-            all += __shfl((long long)scan_tiles(g.offsets, g.groups, g.M, BM, g0, b1, e1, n1), 63);
-        }
-        const int total = (int)(all < g.most_tiles ? all : g.most_tiles);
-        const int tiles_n = (g.N + BN - 1) / BN;
-        if ((int64_t)blockIdx.x >= (int64_t)total * tiles_n) {
+        if (!rows_tile_of_block(g, BM, BN, tm, tn, group, begin, end)) {
             if constexpr (EP == SCALE)
                 if (g.fill) zero_outside(g.offsets, g.groups, g.M, g.N, static_cast<TC *>(g.C), g.ldc);
             return;
         }
-        tile_of_block(blockIdx.x, total, tiles_n, 8, tm, tn);
-        int64_t before = 0;
-        for (int g0 = 0; g0 < g.groups; g0 += 64) {
-            if (g0 > 0) sum = scan_tiles(g.offsets, g.groups, g.M, BM, g0, b, e, n);
-            const uint64_t past = __ballot(before + sum > tm);
-            if (past) {
-                const int at = __builtin_ctzll(past);
-                group = g0 + at;
-                begin = __shfl(b, at);
-                end = __shfl(e, at);
-                tm -= (int)(before + __shfl((long long)sum, at) - __shfl(n, at));
-                break;
-            }
-            before += __shfl((long long)sum, 63);
-        }
-        group = __builtin_amdgcn_readfirstlane(group);
-        begin = __builtin_amdgcn_readfirstlane(begin);
-        end = __builtin_amdgcn_readfirstlane(end);
-        tm = __builtin_amdgcn_readfirstlane(tm);
     } else {
         const int tiles_m = ((EP == GRAD ? g.store_rows : g.M) + BM - 1) / BM;
         const int tiles_n = (g.N + BN - 1) / BN;

@@ -282,7 +282,9 @@ int sgemm_expert_combine(int type, int tokens, int k, int H, int rows, const voi
  *   dout, lddo   tokens x H of `type`
  *   R, ldr    as the forward pass had it; not read where dweights is NULL
  *   weights   tokens * k floats, or NULL: 1
- *   dR, lddr  rows x H of `type`, or NULL: not computed;  fill as in sgemm_expert_gather
+ *   dR, lddr  rows x H of `type`, or NULL: not computed.  No two places are the same then: a row
+ *             that serves several slots gets one of their gradients, not the sum.  fill as in
+ *             sgemm_expert_gather
  *   dweights  tokens * k floats, or NULL: not computed
  * Returns -1 type, -2 tokens, -3 k, -4 H, -5 rows, -6 dout, -7 lddo, -8 R, -9 ldr, -10
  * place, -11 weights, -12 dR, -13 lddr, -14 fill, -15 dweights.

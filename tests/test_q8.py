@@ -247,6 +247,21 @@ def test_matvec_of_groups_fills_rows_outside(dtype, sizes):
             check(Y, ref, ref.abs(), 3, "groups")
 
 
+def test_matvec_of_more_groups_than_a_grid_has():
+    groups, K, N = 65540, 20, 3
+    say("q8 matvec groups", groups)
+    sizes = [0] * groups
+    sizes[0], sizes[40], sizes[-1] = 2, 1, 3
+    ends, off = offsets_of(sizes)
+    X, W, sw = rand((6, K), BF16, 1), bytes_of((groups, N, K), 2), positive((groups, N), 3)
+    Q, s = sg.q8_quantize(X)
+    group = torch.tensor([0, 0, 40] + [groups - 1] * 3, device="cuda")
+    ref = torch.stack([product(Q[r:r + 1], s[r:r + 1], W[g], sw[g])[0] for r, g in enumerate(group.tolist())])
+    Y = sg.q8_matvec(X, W, sw, offsets=off)
+    check(Y, ref, ref.abs(), 3, "groups")
+    assert torch.equal(Y, sg.q8_gemm(Q, s, W, sw, off))
+
+
 def test_no_groups_at_all():
     say("q8 no groups")
     X, off = rand((5, 32), BF16, 1), torch.tensor([2], dtype=torch.int32, device="cuda")

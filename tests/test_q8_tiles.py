@@ -26,14 +26,20 @@ extern "C" int rule(int fast, int64_t used, int64_t rows, int64_t N, int64_t K)
 {
     return sgemm::lm::byte_rows_tile(fast, used, rows, N, K, 256);
 }
+extern "C" int few(int fast, int64_t groups, int64_t used, int64_t rows)
+{
+    return sgemm::lm::byte_few_rows(fast, groups, used, rows);
+}
 """
 # (rows, N, K) of one group and (groups, rows, N, K), by whether the operands take direct loads.
 ONE = {True: [(18, 33, 35), (2071, 67, 102), (2094, 66, 33), (16789, 34, 34), (17794, 129, 38), (16512, 650, 68),
-              (300, 2060, 4100)],
-       False: [(18, 33, 35), (2071, 67, 102), (2094, 66, 33), (16789, 34, 34), (300, 2060, 4099)]}
+              (300, 2060, 4100), (8170, 34, 35), (15, 10400, 34), (41, 900, 2050), (640, 1250, 547)],
+       False: [(18, 33, 35), (2071, 67, 102), (2094, 66, 33), (16789, 34, 34), (300, 2060, 4099), (5, 70, 33)]}
 GROUPS = {True: [(1, 18, 33, 35), (1, 4314, 34, 94), (2, 2094, 66, 33), (19, 15982, 34, 35), (5, 22, 13207, 34),
-                 (28, 4680, 2004, 70), (32, 2048, 1530, 2000)],
-          False: [(1, 18, 33, 35), (1, 4314, 34, 94), (2, 2094, 66, 33), (19, 15982, 34, 35), (8, 2000, 700, 1517)]}
+                 (28, 4680, 2004, 70), (32, 2048, 1530, 2000), (75, 9, 70, 130), (1, 380, 2300, 650),
+                 (220, 4600, 34, 35), (3, 5, 3500, 134), (6, 150, 700, 1030)],
+          False: [(1, 18, 33, 35), (1, 4314, 34, 94), (2, 2094, 66, 33), (19, 15982, 34, 35), (8, 2000, 700, 1517),
+                  (3, 7, 70, 130)]}
 
 
 def _load():
@@ -45,12 +51,13 @@ def _load():
         lib = ctypes.CDLL(lib)
     i, l = ctypes.c_int, ctypes.c_int64
     lib.rule.argtypes = [i, l, l, l, l]
+    lib.few.argtypes = [i, l, l, l]
     return lib
 
 
 def kernel(lib, fast, groups, rows, N, K):
     used = min(groups, rows) or 1
-    if rows <= (4 * used if groups else 16):
+    if lib.few(fast, groups, used, rows):
         return "few rows", fast, groups > 0
     return lib.rule(fast, used if groups else 0, rows, N, K), fast, groups > 0
 
@@ -63,7 +70,7 @@ def test_every_tile_is_reached():
     for fast in (True, False):
         listed = {kernel(lib, fast, 0, *c) for c in ONE[fast]} | {kernel(lib, fast, *c) for c in GROUPS[fast]}
         for _ in range(20000):
-            rows, N, K = size(17, 40000), size(1, 40000), size(1, 20000)
+            rows, N, K = size(1, 40000), size(1, 40000), size(1, 20000)
             for groups in (0, size(1, 300)):
                 k = kernel(lib, fast, groups, rows, N, K)
                 assert k in listed or k[0] == "few rows", (k, groups, rows, N, K)

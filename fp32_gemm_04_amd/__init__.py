@@ -952,8 +952,8 @@ def q8_gemm(X, x_scales, Q, scales, offsets=None, Y=None, dtype=torch.bfloat16, 
 
 
 # Values of X up to which every workgroup quantises them for itself, where it takes them in one pass.  us
-# a call (in a graph), that and two launches: 1 row, 4096 x 4096 8.4 and 12.7 (8.5 and 9.5), 4 rows 10.1
-# and 13.3 (10.5 and 9.8), 8 rows 13.7 and 13.2 (14.4 and 9.9), 16 rows, 1024 x 1024 8.8 and 13.5 (9.0 and 6.8),
+# a call (in a graph), that and two launches: 1 row, 4096 x 4096 8.3 and 12.7 (7.9 and 9.5), 4 rows 10.1
+# and 13.3 (10.7 and 9.7), 8 rows 13.7 and 13.2 (14.4 and 9.9), 16 rows, 1024 x 1024 8.8 and 13.5 (9.1 and 6.8),
 # 2048 x 4096 12.1 and 13.5 (12.4 and 7.4).
 _MOST_MATVEC = 16384
 

@@ -501,9 +501,11 @@ __global__ void __launch_bounds__(kVecWaves * 64) q8_vec_kernel(VecArgs a)
 // over.  Here each wave has a ring of its own, no barrier before the end of the contraction, and
 // reads each byte of LDS once; the sums, exact in any order, meet in LDS.  Rings are short, so that a unit
 // has two or three workgroups.  us in a graph, K = N = 4096, with this and with the best of the tile
-// kernels: 16 rows 5.7 and 13.0, 64 rows 7.1 and 13.4, 128 rows 9.1 and 13.7, 256 rows 12.4 and 13.9, 512 rows
-// 18.7 and 17.5; 64 rows with K 14336 14.4 and 35.0; 64 rows of tiles of 32 x 32 with eight waves
-// 7.5, with rings of three slabs 6.9 against 6.6, tiles of 64 x 16 7.5, 64 x 32 8.6.
+// kernels: 16 rows 5.6 and 13.0, 64 rows 7.0 and 13.4, 128 rows 9.4 and 13.7, 256 rows 12.0 and 13.9, 512 rows
+// 17.2 and 17.5; 64 rows with K 14336 13.8 and 35.0.  64 rows in tiles of 32 x 32 with eight waves took 7.5
+// where this took 6.6, with rings of three slabs 6.9, in tiles of 64 x 16 7.5, of 64 x 32 8.6.  A tile of
+// 128 x 128 for each wave, which reads the least LDS of all, was slower or (1024 rows) within 3% of the
+// tile kernels: its waves read their slabs and multiply in step.
 constexpr int kSplitWaves = 4;
 
 // Workgroups a unit's LDS has room for.
@@ -573,18 +575,23 @@ q8_split_kernel(TileArgs g)
         voff[i] = (uint32_t)row * (uint32_t)(i < BM / 8 ? g.lda : g.ldb) + chunk * 16u;
     }
     char *ring = lds + wave * (DEPTH * STAGE);
-    const auto fetch = [&](int t, int buf) {
+    u32x4 ra, rb;
+    uint32_t at;
+    const auto aim = [&](int t, int buf) {  // at slab t's bytes and where they go
         // (Past the last slab: nothing is in range, and zeros are written.)
-        u32x4 ra = descriptor(pa + t * (int64_t)128, t < slabs ? left_a - t * (int64_t)128 : 0);
-        u32x4 rb = descriptor(pb + t * (int64_t)128, t < slabs ? left_b - t * (int64_t)128 : 0);
-        uint32_t at = (uint32_t)(uintptr_t)(lds_char *)ring + buf * STAGE;
+        ra = descriptor(pa + t * (int64_t)128, t < slabs ? left_a - t * (int64_t)128 : 0);
+        rb = descriptor(pb + t * (int64_t)128, t < slabs ? left_b - t * (int64_t)128 : 0);
+        at = (uint32_t)(uintptr_t)(lds_char *)ring + buf * STAGE;
         // Wait states between a vector unit's write of these and their use.
         asm volatile("s_nop 4" : "+s"(ra), "+s"(rb), "+s"(at));
-#pragma unroll
-        for (int i = 0; i < LPW; ++i) load_slab16(i < BM / 8 ? ra : rb, voff[i], at + i * 1024);
     };
+    const auto load = [&](int i) { load_slab16(i < BM / 8 ? ra : rb, voff[i], at + i * 1024); };
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) fetch(wave + d * WAVES, d);
+    for (int d = 0; d < DEPTH; ++d) {
+        aim(wave + d * WAVES, d);
+#pragma unroll
+        for (int i = 0; i < LPW; ++i) load(i);
+    }
     i32x4 acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -606,7 +613,7 @@ q8_split_kernel(TileArgs g)
         }
         // Read before the buffer is filled again.
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        fetch(t + DEPTH * WAVES, buf);
+        aim(t + DEPTH * WAVES, buf);
         buf = buf + 1 == DEPTH ? 0 : buf + 1;
         if (t == slabs - 1 && g.K % 128) {
             // What lies past K is anything: it meets zeros.
@@ -620,13 +627,29 @@ q8_split_kernel(TileArgs g)
                     for (int i = 0; i < FM; ++i) a[k][i][w] &= (int)mask;
                 }
         }
+        // The next slab's loads: between the products where these are many, since all at once they would
+        // keep them waiting.
+        constexpr int M = 2 * FM * FN;
+        if constexpr (M < 32) {
+#pragma unroll
+            for (int i = 0; i < LPW; ++i) load(i);
+        }
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
-                for (int j = 0; j < FN; ++j)
+                for (int j = 0; j < FN; ++j) {
+                    if constexpr (M >= 32) {
+                        static_assert(M < 32 || LPW <= M, "a load at a product at most");
+                        const int n = (k * FM + i) * FN + j;
+                        if (n * LPW % M < LPW) {
+                            load(n * LPW / M);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
                     acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[k][j], a[k][i], acc[i][j], 0, 0, 0);
+                }
     }
     // ---- the waves' sums meet in LDS: blocks of 16 x 16, a lane's four columns in one piece
 #pragma unroll

@@ -90,9 +90,9 @@ inline int rows_tile(int size, bool fast, int64_t used, int64_t rows, int64_t N,
 // with the 256 tile; 479, 557, 657, 915 and 2110 us with the smaller ones).  Operands of direct loads
 // have the contraction split over waves instead of the two smallest: there time goes with the bytes of
 // both operands.  alone and lead were fitted to the times of all on 86 sizes of 17 to 32768 rows, and
-// the split ones' to 390 sizes of 1 to 8192: the rule's choice is 2.3% slower than the best on
-// average; without the split ones the best is 20.6% slower, with one, two and three of them 3.6, 1.6
-// and 0.9%.
+// the split ones' to 390 sizes of 1 to 8192: the rule's choice is 1.5% slower than the best of these on
+// average, 1.8% on 130 sizes from 300 rows on.  Of 13 kernels the six tiles without the split ones are 20.6%
+// slower, with one, two and three of them 3.6, 1.6 and 0.9%, each choice the best there is.
 struct ByteTileCost {
     int bm, bn;
     double rate, alone;

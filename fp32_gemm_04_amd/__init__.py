@@ -751,7 +751,7 @@ def expert_sort(experts, groups: int, stream=None):
             return n
         offsets = experts.new_empty(groups + 1, dtype=torch.int32)
         order = experts.new_empty(slots, dtype=torch.int32)
-        place = experts.new_empty(experts.shape, dtype=torch.int32)
+        place = torch.empty_like(experts, dtype=torch.int32)
         ws = experts.new_empty(n, dtype=torch.uint8) if n else None
         return _lib.sgemm_expert_sort(slots, groups, experts.data_ptr(), offsets.data_ptr(),
                                       order.data_ptr(), place.data_ptr(),
@@ -860,7 +860,7 @@ def expert_combine_backward(dout, R, place, weights=None, dR=None, need_dR: bool
         if need_dR and dR is None:
             dR = (R.new_empty if rows <= tokens * k else R.new_zeros)(rows, H)
         if need_dweights:
-            dw = dout.new_empty(place.shape, dtype=torch.float32)
+            dw = torch.empty_like(place, dtype=torch.float32)
         return _lib.sgemm_expert_combine_backward(
             t, tokens, k, H, rows, dout.data_ptr(), lddo, R.data_ptr(), ldr, pp, pw,
             dR.data_ptr() if need_dR else 0, lddr, fill, dw.data_ptr() if need_dweights else 0, s)

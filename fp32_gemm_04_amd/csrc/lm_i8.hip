@@ -20,7 +20,6 @@ template <typename TC>
 TileKernel of_type(bool grouped, int tile, bool fast)
 {
     if (!fast) {
-        if (tile == S16) return entry<TC, 16, 64, 1, 4, 2, 16, 2, false>(grouped);
         if (tile == M32) return entry<TC, 32, 128, 1, 4, 2, 16, 2, false>(grouped);
         if (tile == M64) return entry<TC, 64, 128, 2, 2, 2, 16, 2, false>(grouped);
         return entry<TC, 128, 128, 2, 2, 2, 16, 2, false>(grouped);

@@ -33,24 +33,25 @@ template <typename T, bool PLACED> auto quantize_of(int waves)
                         : q8_quantize_kernel<T, 4, PLACED>;
 }
 
-template <typename TY, int BM, int BN, int DEPTH> TileKernel split_entry(bool grouped)
+template <typename TY, int BM, int BN, int DEPTH, bool FAST> TileKernel split_entry(bool grouped)
 {
-    return TileKernel{grouped ? (TileFn)q8_split_kernel<TY, BM, BN, DEPTH, true>
-                              : (TileFn)q8_split_kernel<TY, BM, BN, DEPTH, false>,
+    return TileKernel{grouped ? (TileFn)q8_split_kernel<TY, BM, BN, DEPTH, true, FAST>
+                              : (TileFn)q8_split_kernel<TY, BM, BN, DEPTH, false, FAST>,
                       BM, BN, kSplitWaves * 64};
 }
-template <typename TY> TileKernel split_of(bool grouped, int split)
+template <typename TY> TileKernel split_of(bool grouped, int split, bool fast)
 {
+    if (!fast) return split == 0 ? split_entry<TY, 16, 32, 1, false>(grouped) : split_entry<TY, 32, 32, 1, false>(grouped);
     switch (split) {
-    case 0: return split_entry<TY, 16, 32, 2>(grouped);
-    case 1: return split_entry<TY, 32, 32, 2>(grouped);
-    case 2: return split_entry<TY, 32, 64, 1>(grouped);
-    default: return split_entry<TY, 64, 64, 1>(grouped);
+    case 0: return split_entry<TY, 16, 32, 2, true>(grouped);
+    case 1: return split_entry<TY, 32, 32, 2, true>(grouped);
+    case 2: return split_entry<TY, 32, 64, 1, true>(grouped);
+    default: return split_entry<TY, 64, 64, 1, true>(grouped);
     }
 }
-TileKernel split_kernel(bool bf16_out, bool grouped, int split)
+TileKernel split_kernel(bool bf16_out, bool grouped, int split, bool fast)
 {
-    return bf16_out ? split_of<bf16>(grouped, split) : split_of<float>(grouped, split);
+    return bf16_out ? split_of<bf16>(grouped, split, fast) : split_of<float>(grouped, split, fast);
 }
 
 // A product of few rows: X is int8 with scales, or of the results' type.
@@ -162,7 +163,7 @@ extern "C" int sgemm_q8_gemm(int type, int groups, int rows, int N, int K, const
         return vec_product(v, true, bf16_out, cus, stream);
     }
     const int tile = byte_rows_tile(fast, offsets ? used : 0, rows, N, K, cus);
-    const TileKernel k = tile >= NUM_TILES ? split_kernel(bf16_out, offsets != nullptr, tile - NUM_TILES)
+    const TileKernel k = tile >= NUM_TILES ? split_kernel(bf16_out, offsets != nullptr, tile - NUM_TILES, fast)
                                            : i8_kernel(bf16_out, offsets != nullptr, tile, fast);
     TileArgs a = {};
     a.A = X, a.B = W, a.C = Y;

@@ -508,13 +508,13 @@ __global__ void __launch_bounds__(kVecWaves * 64) q8_vec_kernel(VecArgs a)
 // tile kernels: its waves read their slabs and multiply in step.
 constexpr int kSplitWaves = 4;
 
-// Workgroups a unit's LDS has room for.
+// Workgroups a unit's LDS has room for, of which three are enough.
 constexpr int split_room(int ring)
 {
-    return 160 * 1024 / ring;
+    return 160 * 1024 / ring < 3 ? 160 * 1024 / ring : 3;
 }
 
-template <typename TY, int BM, int BN, int DEPTH, bool GROUPED>
+template <typename TY, int BM, int BN, int DEPTH, bool GROUPED, bool FAST>
 __global__ void __launch_bounds__(kSplitWaves * 64)
     __attribute__((amdgpu_waves_per_eu(split_room(kSplitWaves * DEPTH * (BM + BN) * 128))))
 q8_split_kernel(TileArgs g)
@@ -526,6 +526,7 @@ q8_split_kernel(TileArgs g)
     constexpr int BLOCK = WAVES * BM * 16 * 4, FIT = RING / BLOCK, COLS = FIT >= FN ? FN : FN % FIT == 0 ? FIT : 1;
     static_assert(FIT >= 1 && FN % COLS == 0, "whole blocks of columns");
     static_assert(LPW * (DEPTH - 1) <= 63, "loads in flight must fit the vmcnt field");
+    static_assert(FAST || DEPTH == 1, "the register path has one buffer");
     __shared__ __attribute__((aligned(1024))) char lds[RING];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -568,11 +569,23 @@ q8_split_kernel(TileArgs g)
             col_scale[c][q] = sb[n < g.N ? n : g.N - 1];
         }
 
-    uint32_t voff[LPW];
+    // Load i: eight rows of A or B, 16 bytes a lane.
+    uint32_t voff[FAST ? LPW : 1];
+    const uint8_t *src[FAST ? 1 : LPW];
+    u32x4 hold[FAST ? 1 : LPW];
+    const uint8_t *ends[2] = {reinterpret_cast<const uint8_t *>(pa) + left_a,
+                              reinterpret_cast<const uint8_t *>(pb) + left_b};
 #pragma unroll
     for (int i = 0; i < LPW; ++i) {
-        const int row = (i < BM / 8 ? i : i - BM / 8) * 8 + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
-        voff[i] = (uint32_t)row * (uint32_t)(i < BM / 8 ? g.lda : g.ldb) + chunk * 16u;
+        const bool of_a = i < BM / 8;
+        const int row = (of_a ? i : i - BM / 8) * 8 + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
+        if constexpr (FAST) {
+            voff[i] = (uint32_t)row * (uint32_t)(of_a ? g.lda : g.ldb) + chunk * 16u;
+        } else {  // (Rows past the last repeat it, and are not stored.)
+            const int last = of_a ? rows - 1 : g.N - 1 - n0;
+            src[i] = reinterpret_cast<const uint8_t *>(of_a ? pa : pb) +
+                     (row < last ? row : last) * (of_a ? g.lda : g.ldb) + chunk * 16;
+        }
     }
     char *ring = lds + wave * (DEPTH * STAGE);
     u32x4 ra, rb;
@@ -586,11 +599,30 @@ q8_split_kernel(TileArgs g)
         asm volatile("s_nop 4" : "+s"(ra), "+s"(rb), "+s"(at));
     };
     const auto load = [&](int i) { load_slab16(i < BM / 8 ? ra : rb, voff[i], at + i * 1024); };
+    // Rows at any byte: slab t into registers, while the one before it is multiplied.
+    const auto take = [&](int t) {
+        if (t >= slabs) return;
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) {
-        aim(wave + d * WAVES, d);
+        for (int i = 0; i < LPW; ++i) {
+            const uint8_t *p = src[i] + t * (int64_t)128, *end = ends[i < BM / 8 ? 0 : 1];
+            if (p + 16 <= end) {
+                __builtin_memcpy(&hold[i], p, 16);
+            } else {
+                hold[i] = u32x4{0, 0, 0, 0};
+                for (int j = 0; j < 16; ++j)
+                    if (p + j < end) hold[i][j / 4] |= (uint32_t)p[j] << (8 * (j % 4));
+            }
+        }
+    };
+    if constexpr (FAST) {
 #pragma unroll
-        for (int i = 0; i < LPW; ++i) load(i);
+        for (int d = 0; d < DEPTH; ++d) {
+            aim(wave + d * WAVES, d);
+#pragma unroll
+            for (int i = 0; i < LPW; ++i) load(i);
+        }
+    } else {
+        take(wave);
     }
     i32x4 acc[FM][FN];
 #pragma unroll
@@ -600,7 +632,14 @@ q8_split_kernel(TileArgs g)
     const int l16 = lane & 15, lg = lane >> 4;
     int buf = 0;
     for (int t = wave; t < slabs; t += WAVES) {
-        asm volatile("s_waitcnt vmcnt(%0)" : : "n"(LPW * (DEPTH - 1)) : "memory");
+        if constexpr (FAST) {
+            asm volatile("s_waitcnt vmcnt(%0)" : : "n"(LPW * (DEPTH - 1)) : "memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < LPW; ++i) *reinterpret_cast<u32x4 *>(ring + i * 1024 + lane * 16) = hold[i];
+            __builtin_amdgcn_wave_barrier();  // a wave's writes and reads of LDS stay in order
+            take(t + WAVES);
+        }
         const char *slab = ring + buf * STAGE + l16 * 128;
         i32x4 a[2][FM], b[2][FN];
 #pragma unroll
@@ -611,10 +650,14 @@ q8_split_kernel(TileArgs g)
 #pragma unroll
             for (int j = 0; j < FN; ++j) b[k][j] = *reinterpret_cast<const i32x4 *>(slab + BM * 128 + j * 2048 + c);
         }
-        // Read before the buffer is filled again.
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        aim(t + DEPTH * WAVES, buf);
-        buf = buf + 1 == DEPTH ? 0 : buf + 1;
+        if constexpr (FAST) {
+            // Read before the buffer is filled again.
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            aim(t + DEPTH * WAVES, buf);
+            buf = buf + 1 == DEPTH ? 0 : buf + 1;
+        } else {
+            __builtin_amdgcn_wave_barrier();
+        }
         if (t == slabs - 1 && g.K % 128) {
             // What lies past K is anything: it meets zeros.
 #pragma unroll
@@ -630,7 +673,7 @@ q8_split_kernel(TileArgs g)
         // The next slab's loads: between the products where these are many, since all at once they would
         // keep them waiting.
         constexpr int M = 2 * FM * FN;
-        if constexpr (M < 32) {
+        if constexpr (FAST && M < 32) {
 #pragma unroll
             for (int i = 0; i < LPW; ++i) load(i);
         }
@@ -640,7 +683,7 @@ q8_split_kernel(TileArgs g)
             for (int i = 0; i < FM; ++i)
 #pragma unroll
                 for (int j = 0; j < FN; ++j) {
-                    if constexpr (M >= 32) {
+                    if constexpr (FAST && M >= 32) {
                         static_assert(M < 32 || LPW <= M, "a load at a product at most");
                         const int n = (k * FM + i) * FN + j;
                         if (n * LPW % M < LPW) {

@@ -87,24 +87,27 @@ inline int rows_tile(int size, bool fast, int64_t used, int64_t rows, int64_t N,
 // 8-bit products.  As above, with the contraction in pairs of bytes (a slab is 64); a unit takes two
 // tiles at a time (of the 256 tile one), and where a last one has the unit to itself it costs
 // `alone`, in tiles of a unit that is never idle.  Rates are those of 8192 x 4096 x 14336 (439 us
-// with the 256 tile; 479, 557, 657, 915 and 2110 us with the smaller ones).  Operands of direct loads
-// have the contraction split over waves instead of the two smallest: there time goes with the bytes of
-// both operands.  alone and lead were fitted to the times of all on 86 sizes of 17 to 32768 rows, and
-// the split ones' to 390 sizes of 1 to 8192: the rule's choice is 1.5% slower than the best of these on
-// average, 1.8% on 130 sizes from 300 rows on.  Of 13 kernels the six tiles without the split ones are 20.6%
-// slower, with one, two and three of them 3.6, 1.6 and 0.9%, each choice the best there is.
+// with the 256 tile; 479, 557 and 657 us with the smaller ones).  Small tiles have the contraction split over
+// waves: there time goes with the bytes of both operands.  alone and lead were fitted to the times of all on
+// 86 sizes of 17 to 32768 rows, and the split ones' to 390 sizes of 1 to 8192: the rule's choice is 1.5%
+// slower than the best of these on average, 1.8% on 130 sizes from 300 rows on.  Of 13 kernels the six
+// tiles without the split ones are 20.6% slower, with one, two and three of them 3.6, 1.6 and 0.9%, each
+// choice the best there is.  Operands without direct loads have costs of their own, fitted to 180 sizes (2.7%;
+// 18.2% without the split ones, which take more registers from 32 x 64 on than there are).
 struct ByteTileCost {
     int bm, bn;
     double rate, alone;
     int lead;
 };
-constexpr ByteTileCost kI8Tiles[NUM_TILES] = {
-    {16, 64, 0.21, 0.7, 384}, {32, 128, 0.48, 0.9, 384}, {0, 0, 0, 0, 0}, {64, 128, 0.67, 1.55, 128},
-    {128, 128, 0.79, 1.4, 96}, {128, 192, 0.92, 1.65, 64}, {256, 256, 1.0, 0.9, 128}};
 constexpr int kSplits = 4;
-constexpr ByteTileCost kI8Splits[kSplits] = {
-    {16, 32, 0.0321, 0.71, 1152}, {32, 32, 0.0295, 0.82, 1152}, {32, 64, 0.0264, 0.71, 832},
-    {64, 64, 0.026, 0.71, 1408}};
+constexpr ByteTileCost kI8Tiles[2][NUM_TILES] = {
+    {{}, {32, 128, 0.576, 1.18, 400}, {}, {64, 128, 0.667, 1.51, 150}, {128, 128, 0.829, 1.55, 207}, {}, {}},
+    {{}, {}, {}, {64, 128, 0.67, 1.55, 128}, {128, 128, 0.79, 1.4, 96}, {128, 192, 0.92, 1.65, 64},
+     {256, 256, 1.0, 0.9, 128}}};
+constexpr ByteTileCost kI8Splits[2][kSplits] = {
+    {{16, 32, 0.0429, 0.92, 700}, {32, 32, 0.0637, 1.41, 1340}, {}, {}},
+    {{16, 32, 0.0321, 0.71, 1152}, {32, 32, 0.0295, 0.82, 1152}, {32, 64, 0.0264, 0.71, 832},
+     {64, 64, 0.026, 0.71, 1408}}};
 
 // A tile, or NUM_TILES and which of the split ones.
 template <typename RowTiles>
@@ -115,8 +118,8 @@ int byte_tile(bool fast, RowTiles row_tiles, int64_t N, int64_t K, int cus)
     const auto offer = [&](int i, double cost) {
         if (best < 0 || cost < least) best = i, least = cost;
     };
-    for (int i = fast ? M64 : S16; i <= (fast ? T256 : T128); ++i) {
-        const ByteTileCost &t = kI8Tiles[i];
+    for (int i = 0; i < NUM_TILES; ++i) {
+        const ByteTileCost &t = kI8Tiles[fast][i];
         if (t.bm == 0) continue;
         const int64_t tiles = row_tiles(t.bm) * ceil_div(N, t.bn);
         const int64_t left = tiles % (2 * cus);
@@ -124,8 +127,9 @@ int byte_tile(bool fast, RowTiles row_tiles, int64_t N, int64_t K, int cus)
         if (i == T256) rounds = tiles <= cus ? t.alone : (double)ceil_div(tiles, cus);
         offer(i, rounds * t.bm * t.bn * (0.5 * K + t.lead) / t.rate);
     }
-    for (int i = 0; fast && i < kSplits; ++i) {
-        const ByteTileCost &t = kI8Splits[i];
+    for (int i = 0; i < kSplits; ++i) {
+        const ByteTileCost &t = kI8Splits[fast][i];
+        if (t.bm == 0) continue;
         const double share = (double)(row_tiles(t.bm) * ceil_div(N, t.bn)) / cus;
         offer(NUM_TILES + i, (share > t.alone ? share : t.alone) * (t.bm + t.bn) * (K + t.lead) / t.rate);
     }

@@ -34,12 +34,13 @@ extern "C" int few(int fast, int64_t groups, int64_t used, int64_t rows)
 # (rows, N, K) of one group and (groups, rows, N, K), by whether the operands take direct loads.
 ONE = {True: [(18, 33, 35), (2071, 67, 102), (2094, 66, 33), (16789, 34, 34), (17794, 129, 38), (16512, 650, 68),
               (300, 2060, 4100), (8170, 34, 35), (15, 10400, 34), (41, 900, 2050), (640, 1250, 547)],
-       False: [(18, 33, 35), (2071, 67, 102), (2094, 66, 33), (16789, 34, 34), (300, 2060, 4099), (5, 70, 33)]}
+       False: [(18, 33, 35), (2071, 67, 102), (2094, 66, 33), (16789, 34, 34), (300, 2060, 4099), (5, 70, 33),
+               (520, 1300, 143), (3040, 2070, 199), (70, 530, 2049)]}
 GROUPS = {True: [(1, 18, 33, 35), (1, 4314, 34, 94), (2, 2094, 66, 33), (19, 15982, 34, 35), (5, 22, 13207, 34),
                  (28, 4680, 2004, 70), (32, 2048, 1530, 2000), (75, 9, 70, 130), (1, 380, 2300, 650),
                  (220, 4600, 34, 35), (3, 5, 3500, 134), (6, 150, 700, 1030)],
           False: [(1, 18, 33, 35), (1, 4314, 34, 94), (2, 2094, 66, 33), (19, 15982, 34, 35), (8, 2000, 700, 1517),
-                  (3, 7, 70, 130)]}
+                  (3, 7, 70, 130), (6, 2662, 250, 119), (1, 2790, 1420, 9), (5, 90, 530, 2049)]}
 
 
 def _load():

@@ -534,12 +534,12 @@ q8_split_kernel(TileArgs g)
 
     int tm, tn, group = 0, begin = 0, end = g.M;
     if constexpr (GROUPED) {
-        if (!rows_tile_of_block(g, BM, BN, tm, tn, group, begin, end)) {
+        if (!rows_tile_of_block(g, BM, BN, byte_band(true), tm, tn, group, begin, end)) {
             if (g.fill) zero_outside(g.offsets, g.groups, g.M, g.N, C, g.ldc);
             return;
         }
     } else {
-        tile_of_block(blockIdx.x, (g.M + BM - 1) / BM, (g.N + BN - 1) / BN, 8, tm, tn);
+        tile_of_block(blockIdx.x, (g.M + BM - 1) / BM, (g.N + BN - 1) / BN, byte_band(false), tm, tn);
     }
     const int first = begin + tm * BM, n0 = tn * BN;
     const int rows = end - first < BM ? end - first : BM;

@@ -338,8 +338,8 @@ __device__ __forceinline__ int64_t scan_tiles(const int *offsets, int groups, in
 }
 
 // The workgroup's tile of its group, and the group's rows; false where there is none for it.
-__device__ __forceinline__ bool rows_tile_of_block(const TileArgs &g, int bm, int bn, int &tm, int &tn,
-                                                   int &group, int &begin, int &end)
+__device__ __forceinline__ bool rows_tile_of_block(const TileArgs &g, int bm, int bn, int band, int &tm,
+                                                   int &tn, int &group, int &begin, int &end)
 {
     // (Up to 64 groups are counted once: a tile's first loads wait for this.)
     int b, e, n;
@@ -352,7 +352,7 @@ __device__ __forceinline__ bool rows_tile_of_block(const TileArgs &g, int bm, in
     const int total = (int)(all < g.most_tiles ? all : g.most_tiles);
     const int tiles_n = (g.N + bn - 1) / bn;
     if ((int64_t)blockIdx.x >= (int64_t)total * tiles_n) return false;
-    tile_of_block(blockIdx.x, total, tiles_n, 8, tm, tn);
+    tile_of_block(blockIdx.x, total, tiles_n, band, tm, tn);
     int64_t before = 0;
     for (int g0 = 0; g0 < g.groups; g0 += 64) {
         if (g0 > 0) sum = scan_tiles(g.offsets, g.groups, g.M, bm, g0, b, e, n);
@@ -372,6 +372,15 @@ __device__ __forceinline__ bool rows_tile_of_block(const TileArgs &g, int bm, in
     end = __builtin_amdgcn_readfirstlane(end);
     tm = __builtin_amdgcn_readfirstlane(tm);
     return true;
+}
+
+// Row tiles that an XCD's neighbouring workgroups walk a column of before the next column.  8-bit
+// operands: us with 8, 4 and 2, 8192 x 4096 x 14336 451, 447 and 455, 4096 x 4096 x 4096 70.3, 65.8 and
+// 66.2; by group with 8, 3 and 1, 16384 rows on 64 experts' 2048 x 1536 101, 99 and 98, 32768 rows 163, 158
+// and 161, 8192 rows on eight experts' 4096 x 2048 99, 95 and 95.
+constexpr int byte_band(bool grouped)
+{
+    return grouped ? 3 : 4;
 }
 
 // WM x WN waves share the tile, NBUF slabs the ring; WPE waves per SIMD bound the registers.
@@ -411,9 +420,10 @@ tile_kernel(TileArgs g)
     const int lrow = lane & (BL - 1), lg = lane / BL;
 
     // ---- which tile, of which group
+    constexpr int BAND = std::is_same<T, int8_t>::value ? byte_band(RG == ROWS) : 8;
     int tm, tn, group = 0, begin = 0, end = 0, m0;
     if constexpr (RG == ROWS) {
-        if (!rows_tile_of_block(g, BM, BN, tm, tn, group, begin, end)) {
+        if (!rows_tile_of_block(g, BM, BN, BAND, tm, tn, group, begin, end)) {
             if constexpr (EP == SCALE)
                 if (g.fill) zero_outside(g.offsets, g.groups, g.M, g.N, static_cast<TC *>(g.C), g.ldc);
             return;
@@ -430,7 +440,7 @@ tile_kernel(TileArgs g)
             begin = __builtin_amdgcn_readfirstlane(begin);
             end = __builtin_amdgcn_readfirstlane(end);
         }
-        tile_of_block(bid, tiles_m, tiles_n, 8, tm, tn);
+        tile_of_block(bid, tiles_m, tiles_n, BAND, tm, tn);
     }
     m0 = tm * BM;
     const int n0 = tn * BN;

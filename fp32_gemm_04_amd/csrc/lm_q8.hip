@@ -30,7 +30,8 @@ template <typename T, bool PLACED> auto quantize_of(int waves)
 {
     return waves == 1   ? q8_quantize_kernel<T, 1, PLACED>
            : waves == 2 ? q8_quantize_kernel<T, 2, PLACED>
-                        : q8_quantize_kernel<T, 4, PLACED>;
+           : waves == 4 ? q8_quantize_kernel<T, 4, PLACED>
+                        : q8_quantize_kernel<T, 8, PLACED>;
 }
 
 template <typename TY, int BM, int BN, int DEPTH, bool FAST> TileKernel split_entry(bool grouped)
@@ -111,15 +112,18 @@ extern "C" int sgemm_q8_quantize(int type, int rows, int K, const void *X, int l
     a.rows = rows, a.K = K, a.k = k, a.out_rows = out_rows;
     const int64_t pieces = ceil_div(K, 16 / size);
     // As few waves a row as hold it in registers, but more where they would not fill the units.
-    int waves = pieces <= 64 * kHeld ? 1 : pieces <= 128 * kHeld ? 2 : 4;
-    // us: 8192 rows of 2048 bf16 11.5 with one, 11.7 with two; 64 rows of 4096 3.6 with four, 7 with two.
-    while (waves < 4 && (int64_t)rows * waves < 4096 && pieces > 64 * waves) waves *= 2;
-    const int64_t blocks = ceil_div(rows, 4 / waves);
+    int waves = pieces <= 64 * kHeld ? 1 : pieces <= 128 * kHeld ? 2 : pieces <= 256 * kHeld ? 4 : 8;
+
+    // us: 8192 rows of 2048 bf16 11.5 with one, 11.7 with two; 64 rows of 4096 7 with two, 4.3 with four, 3.8
+    // with eight; 12 rows of 14336 8.0 with four, 5.3 with eight, 8192 fp32 rows of 8192 70.7 and 61.5 (6.8 TB/s,
+    // part of it from the last-level cache), of 5000 36.4 and 36.8.
+    while (waves < 8 && (int64_t)rows * waves < 4096 && pieces > 64 * waves) waves *= 2;
+    const int64_t blocks = ceil_div(rows, quantize_waves(waves) / waves);
     const dim3 grid((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks));
     const auto fn = type == SGEMM_TYPE_BF16
                         ? (place ? quantize_of<bf16, true>(waves) : quantize_of<bf16, false>(waves))
                         : (place ? quantize_of<float, true>(waves) : quantize_of<float, false>(waves));
-    fn<<<grid, dim3(256), 0, stream>>>(a);
+    fn<<<grid, dim3(quantize_waves(waves) * 64), 0, stream>>>(a);
     return (int)hipGetLastError();
 }
 

@@ -155,16 +155,21 @@ struct QuantArgs {
 // values meet another piece's, and so do the bytes that both write).
 constexpr int kHeld = 4;
 
-template <typename T, int WAVES, bool PLACED>
-__global__ void __launch_bounds__(256) q8_quantize_kernel(QuantArgs a)
+constexpr int quantize_waves(int waves)  // of a workgroup
 {
-    constexpr int ROWS = 4 / WAVES, E = 16 / sizeof(T), step = WAVES * 64 * E;
+    return waves < 4 ? 4 : waves;
+}
+
+template <typename T, int WAVES, bool PLACED>
+__global__ void __launch_bounds__(quantize_waves(WAVES) * 64) q8_quantize_kernel(QuantArgs a)
+{
+    constexpr int ROWS = quantize_waves(WAVES) / WAVES, E = 16 / sizeof(T), step = WAVES * 64 * E;
     typedef T Vec __attribute__((ext_vector_type(E)));
     typedef Vec Loose __attribute__((aligned(sizeof(T))));
     // Magnitudes order like their bits, as integers of the value's size.
     typedef typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type U;
     typedef U Bits __attribute__((ext_vector_type(E)));
-    __shared__ uint32_t part[4];
+    __shared__ uint32_t part[quantize_waves(WAVES)];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int k0 = ((wave % WAVES) * 64 + lane) * E;

@@ -85,7 +85,7 @@ def test_quantize_of_tiny_huge_and_missing_values():
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("T,k,K", [(1, 1, 1), (40, 2, 100), (9, 8, 2048), (5, 3, 5003)])
+@pytest.mark.parametrize("T,k,K", [(1, 1, 1), (40, 2, 100), (9, 8, 2048), (5, 3, 5003), (4, 2, 17001)])
 def test_quantize_to_sorted_rows(dtype, T, k, K):
     say("quantize to rows", dtype, T, k, K)
     _, order, place, _ = routed(T, k, 6, T + K, 0.2)

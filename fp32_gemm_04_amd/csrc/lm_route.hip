@@ -22,10 +22,10 @@ struct SortPlan {
     int64_t bytes;  // of counts; 0: one launch
 };
 
-// us in a graph.  One launch and two: 4096 slots, 64 experts 6.0 and 7.5, 16384, 32 experts 7.3 and
+// us in a graph.  One launch and two: 4096 slots, 64 experts 5.8 and 7.5, 16384, 32 experts 7.1 and
 // 7.4 (a call of Python's: 9.9 and 14.5), 32768, 128 experts 9.9 and 8.5.  Chunks of one and two slots a
-// lane: 128 slots, 64 experts 4.1 and 4.7, 16384, 32 experts 7.3 and 8.3, 65536, 64 experts 8.3 and 9.1,
-// 262144, 64 experts 10.7 both, 256 experts 19.8 and 15.0 (every workgroup reads all counts).
+// lane: 128 slots, 64 experts 4.0 and 4.7, 16384, 32 experts 7.1 and 8.3, 65536, 64 experts 8.2 and 9.1,
+// 262144, 64 experts 10.6 both, 256 experts 19.8 and 15.0 (every workgroup reads all counts).
 SortPlan sort_plan(int slots, int groups)
 {
     SortPlan p;

@@ -981,7 +981,7 @@ def q8_matvec(X, Q, scales, Y=None, offsets=None, stream=None):
             Y = X.new_empty(rows, N)
         stride = _groups_of(Q) if offsets is not None else 0
         if rows * K > _MOST_MATVEC or rows > (4 * groups if off else 16) or groups > 65535:
-            ldq = -(-K // 16) * 16
+            ldq = max(16, -(-K // 16) * 16)
             ws = X.new_empty(rows * (ldq + 4), dtype=torch.uint8)
             q = ws.data_ptr()
             return (_lib.sgemm_q8_quantize(t, rows, K, X.data_ptr(), ldx, 0, 0, rows, q, ldq,

@@ -247,6 +247,19 @@ def test_matvec_of_groups_fills_rows_outside(dtype, sizes):
             check(Y, ref, ref.abs(), 3, "groups")
 
 
+@pytest.mark.parametrize("rows", [0, 3, 40])
+@pytest.mark.parametrize("groups", [0, 5])
+def test_products_without_a_contraction(rows, groups):
+    say("q8 K 0", rows, groups)
+    X = torch.empty((rows, 0), dtype=BF16, device="cuda")
+    W = torch.empty(((groups,) if groups else ()) + (70, 0), dtype=torch.int8, device="cuda")
+    sw, off = positive(W.shape[:-1], 1), offsets_of([0, rows] + [0] * 3)[1] if groups else None
+    Q, s = sg.q8_quantize(X)
+    assert Q.shape == (rows, 0) and not s.any()
+    for Y in (sg.q8_matvec(X, W, sw, offsets=off), sg.q8_gemm(Q, s, W, sw, off)):
+        assert Y.shape == (rows, 70) and not Y.any()
+
+
 def test_matvec_of_more_groups_than_a_grid_has():
     groups, K, N = 65540, 20, 3
     say("q8 matvec groups", groups)

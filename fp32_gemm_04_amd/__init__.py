@@ -870,7 +870,7 @@ def expert_combine_backward(dout, R, place, weights=None, dR=None, need_dR: bool
 
 def q8_quantize(X, place=None, stream=None):
     """(Q, scales): each row of X in 8 bits with a scale of its own, the largest magnitude
-    over 127 (``sgemm_q8_quantize``).  A row is Q[r] * scales[r].
+    times 1 / 127 (``sgemm_q8_quantize``).  A row is Q[r] * scales[r].
 
     X: (rows, K) or (groups, rows, K) (weights of all experts, packed groups), float32 or
     bfloat16.  Q: int8 of the same shape, rows padded to a multiple of 16 bytes; scales: float32,

@@ -1,6 +1,7 @@
 // Rows in 8-bit integers, and products of a few such rows with 8-bit weights (include/slm.h).
 //
-// Quantisation.  scale = m / 127 with m the row's largest magnitude; q is x / scale
+// Quantisation.  scale = m * fl(1/127) with m the row's largest magnitude, which is what a division of a
+// tensor by 127 gives on the device in torch (m / 127 or its neighbour); q is x / scale
 // rounded to the nearest integer, ties to even, of the exact quotient.  One fma with the
 // reciprocal of scale and 1.5 * 2^23 rounds x / scale to an integer, in the last bits of its
 // result, and a second gives how far from it the quotient was.  The reciprocal's rounding moves
@@ -29,7 +30,8 @@ struct Quantum {
     // m: the largest magnitude's bits, in which an infinity or a NaN lies above every number.
     __device__ __forceinline__ explicit Quantum(uint32_t m)
     {
-        scale = __builtin_bit_cast(float, m) / 127.f;
+        constexpr float kPart = 1.f / 127.f;
+        scale = __builtin_bit_cast(float, m) * kPart;
         by = scale < 0x1p-60f ? 0x1p80f : 1.f;
         step = scale * by;
         inverse = step > 0.f ? 1.f / step : 0.f;

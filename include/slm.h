@@ -299,7 +299,8 @@ int sgemm_expert_combine_backward(int type, int tokens, int k, int H, int rows, 
  * (channel): the value of q is q times its scale.
  *
  * sgemm_q8_quantize -- rows to 8 bits: with m the largest magnitude of row r of X,
- *     scales[r] = m / 127 (fp32)        Q[r][k] = X[r][k] / scales[r]
+ *     scales[r] = m * (1 / 127)        Q[r][k] = X[r][k] / scales[r]
+ * (the scale in fp32, 1 / 127 and the product rounded to it once each: m / 127 or its neighbour); Q
  * rounded to the nearest integer, ties to even, of the exact quotient of the stored values.
  * A row whose scale is zero gets zeros; a row that holds an infinity or a NaN gets
  * the scale NaN and zeros, so that its products are NaN.  Weights are quantised by the same call (N x K: a

@@ -283,4 +283,4 @@ def test_more_rows_than_workgroups(release):
     assert torch.equal(dR, R) and dw[0].item() == 4.25 and dw[-1].item() == 11.25 and not dw[1:-1].any()
     Q, s = sg.q8_quantize(X)
     assert Q[-1].tolist() == [127, -64] and Q[0].tolist() == [32, 127] and not Q[1:-1].any()
-    assert s[-1] == torch.tensor(3.0) / 127 and not s[1:-1].any()
+    assert s[-1] == torch.tensor(3.0) * torch.tensor(1 / 127) and not s[1:-1].any()

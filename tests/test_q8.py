@@ -18,13 +18,14 @@ from .test_lm_route import routed  # noqa: E402
 pytestmark = pytest.mark.gpu
 
 F32, BF16 = torch.float32, torch.bfloat16
+PART = torch.tensor(1 / 127, dtype=F32).item()  # products of two 24-bit numbers are exact in 64 bits
 
 
 def quantize_reference(X):
     X = X.double()
     finite = torch.isfinite(X).all(1)
     m = X.abs().amax(1) if X.shape[1] else X.new_zeros(X.shape[0])
-    scales = (m / 127.0).float()
+    scales = (m * PART).float()
     q = torch.round(X / scales.double()[:, None])
     q = torch.where((scales > 0)[:, None] & finite[:, None], q, 0.0).nan_to_num(0.0).clamp(-127, 127)
     return q.to(torch.int8), torch.where(finite, scales, float("nan"))
@@ -54,7 +55,7 @@ def test_quantize_rounds_the_exact_quotient():
     say("quantize ties")
     m = torch.cat([torch.arange(1, 4096, dtype=torch.float64) / 2048, torch.tensor([127.0, 254.0, 1 / 3])])
     m = m.float()
-    s = (m.double() / 127).float().double()
+    s = (m.double() * PART).float().double()
     steps = torch.arange(0, 127, dtype=torch.float64) + 0.5
     mid = (s[:, None] * steps).float()
     near = [mid, torch.nextafter(mid, torch.zeros(())), torch.nextafter(mid, torch.tensor(9e9))]

@@ -1,14 +1,13 @@
 // Rows in 8-bit integers, and products of a few such rows with 8-bit weights (include/slm.h).
 //
-// Quantisation.  scale = m * fl(1/127) with m the row's largest magnitude, which is what a division of a
-// tensor by 127 gives on the device in torch (m / 127 or its neighbour); q is x / scale
-// rounded to the nearest integer, ties to even, of the exact quotient.  One fma with the
-// reciprocal of scale and 1.5 * 2^23 rounds x / scale to an integer, in the last bits of its
-// result, and a second gives how far from it the quotient was.  The reciprocal's rounding moves
-// the quotient by less than 2^-17 (127 * 2^-24), so only where that distance is within 2^-16 of
-// a half may q be one off (values of a wave: some 3% of the time); there the
-// remainder x - q scale, exact in one fma (a multiple of the smaller operand's last bit, below
-// 2 scale), is compared with half of scale.
+// Quantisation.  scale = m * fl(1/127) with m the row's largest magnitude, which is what torch
+// makes of a division by 127 on the device (m / 127 or its neighbour); q is x / scale rounded to
+// the nearest integer, ties to even, of the exact quotient.  One fma with the reciprocal of scale
+// and 1.5 * 2^23 rounds x / scale to an integer, in the last bits of its result, and a second gives
+// how far from it the quotient was.  The reciprocal's rounding moves the quotient by less than
+// 2^-17 (127 * 2^-24), so only where that distance is within 2^-16 of a half may q be one off
+// (values of a wave: some 3% of the time); there the remainder x - q scale, exact in one fma (a
+// multiple of the smaller operand's last bit, below 2 scale), is compared with half of scale.
 #pragma once
 
 #include "lm_tile.hpp"
@@ -260,14 +259,14 @@ __global__ void __launch_bounds__(quantize_waves(WAVES) * 64) q8_quantize_kernel
 // ------------------------------------------------------------- a few rows
 
 // Y[r][n] for a few rows that are quantised on the way, have weights at odd bytes or more than 64
-// groups: every weight is used once a row, so the time is that of reading the weights.  A workgroup of eight waves puts its rows into LDS once, quantising them where TX is
-// not int8, then takes tiles of 16
-// columns; the waves split the contraction, slab by slab of 128 bytes, and their integer sums
-// meet in LDS.  Weights travel through a ring of LDS of each wave's own by direct loads,
-// which ask for whole 128-byte rows; fetched straight into the lanes that the matrix
-// instruction wants them in, neighbouring lanes would ask for different rows.  The ring runs on
-// from tile to tile, and is filled before the rows are quantised.  us in a graph: 1 row, 4096 x 4096 7.9
-// (of 8-bit rows 5.4), 4096 x 14336 13.8, 8192 x 28001 41.4 (5.5 TB/s).
+// groups: every weight is used once a row, so the time is that of reading the weights.  A workgroup
+// of eight waves puts its rows into LDS once, quantising them where TX is not int8, then takes tiles
+// of 16 columns; the waves split the contraction, slab by slab of 128 bytes, and their integer sums
+// meet in LDS.  Weights travel through a ring of LDS of each wave's own by direct loads, which ask
+// for whole 128-byte rows; fetched straight into the lanes that the matrix instruction wants them
+// in, neighbouring lanes would ask for different rows.  The ring runs on from tile to tile, and is
+// filled before the rows are quantised.  us in a graph: 1 row, 4096 x 4096 7.9 (of 8-bit rows 5.4),
+// 4096 x 14336 13.8, 8192 x 28001 41.4 (5.5 TB/s).
 struct VecArgs {
     const void *X;
     const float *x_scales;  // of 8-bit rows

@@ -262,6 +262,8 @@ int sgemm_expert_gather(int type, int tokens, int k, int H, const void *X, int l
  *     out[t] <- beta * out[t] + sum_j weights[t*k + j] * R[place[t*k + j]]
  * summed in fp32 in the order of j, rounded once.  A slot without a row adds nothing and
  * its weight is not used; a token with none gets beta * out[t].  One row may serve several slots.
+ * (bf16 rows were rounded before the sum: fp32 rows, as sgemm_q8_gemm gives them too, leave one
+ * rounding, of the fp32 result.)
  *
  *   R, ldr    rows x H of `type`;  place, weights as above
  *   beta      beta == 0: out is written, not read

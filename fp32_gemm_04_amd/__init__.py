@@ -891,6 +891,8 @@ def q8_quantize(X, place=None, stream=None):
     if lead and lead[0] > 1 and X.numel() and X.stride(0) != rows * ldx:
         raise ValueError("X's groups must follow one another")
     k, pp, _ = _slots(place, None, dev, rows, "X") if place is not None else (0, 0, 0)
+    if place is not None and not pp:
+        pp = 4  # an empty tensor's pointer, which the call would take for no place: nothing is read
     n = _extent(rows * (lead[0] if lead else 1), "X as one matrix")
     out = n * k if place is not None else n
     ldq = _extent(-(-K // 16) * 16 if K else 1, "Q")

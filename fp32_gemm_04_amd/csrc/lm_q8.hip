@@ -99,9 +99,10 @@ extern "C" int sgemm_q8_quantize(int type, int rows, int K, const void *X, int l
     const bool work = rows > 0 && out_rows > 0 && (!place || k > 0);
     if ((work && K > 0 && !X) || !aligned(X, size)) return -4;
     if (ldx < least) return -5;
-    if (k < 0 || (!place && k != 0) || (rows > 0 && k > kMostExtent / rows)) return -6;
+    // (Places of no rows may be NULL: then k says that there were some.)
+    if (k < 0 || (rows > 0 && (k > kMostExtent / rows || (!place && k > 0)))) return -6;
     if (!aligned(place, 4)) return -7;
-    if (out_rows < 0 || out_rows > kMostExtent || (!place && out_rows != rows)) return -8;
+    if (out_rows < 0 || out_rows > kMostExtent || (!place && k == 0 && out_rows != rows)) return -8;
     if (work && K > 0 && !Q) return -9;
     if (ldq < least) return -10;
     if ((work && !scales) || !aligned(scales, 4)) return -11;

@@ -310,16 +310,16 @@ int sgemm_expert_combine_backward(int type, int tokens, int k, int H, int rows, 
  *
  *   type      enum sgemm_type of X
  *   rows      >= 0;  K 0 .. 131071;  X, ldx: rows x K
- *   k, place  NULL place (k = 0): row r of X goes to row r of Q, out_rows = rows.  Otherwise
+ *   k, place  NULL place and k 0: row r of X goes to row r of Q, out_rows = rows.  Otherwise
  *             row t goes to the k rows place[t*k + j], as sgemm_expert_gather sends them
  *             (rows without a token: left as they were, but those of dropped slots set
- *             to zero, with the scale 0)
+ *             to zero, with the scale 0); NULL too where rows is 0
  *   out_rows  rows of Q and scales
  *   Q, ldq    out_rows x K bytes, ldq >= max(1, K).  The products read rows at 4-byte
  *             addresses (Q and ldq multiples of 4) fastest
  *   scales    out_rows floats
  * Returns -1 type, -2 rows, -3 K, -4 X, -5 ldx, -6 k (negative, rows * k too large, or not
- * 0 without place), -7 place, -8 out_rows, -9 Q, -10 ldq, -11 scales.
+ * 0 without place for rows), -7 place, -8 out_rows, -9 Q, -10 ldq, -11 scales.
  */
 int sgemm_q8_quantize(int type, int rows, int K, const void *X, int ldx, int k, const int *place,
                       int out_rows, int8_t *Q, int ldq, float *scales, hipStream_t stream);

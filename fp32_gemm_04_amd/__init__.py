@@ -987,7 +987,8 @@ def q8_matvec(X, Q, scales, Y=None, offsets=None, stream=None):
         if Y is None:
             Y = X.new_empty(rows, N)
         stride = _groups_of(Q) if offsets is not None else 0
-        if rows * K > _MOST_MATVEC or rows > (4 * groups if off else 16) or groups > 65535:
+        # (No rows count as one: the one launch takes K up to 106496 whatever the rows.)
+        if (rows or 1) * K > _MOST_MATVEC or rows > (4 * groups if off else 16) or groups > 65535:
             ldq = max(16, -(-K // 16) * 16)
             ws = X.new_empty(rows * (ldq + 4), dtype=torch.uint8)
             q = ws.data_ptr()

@@ -14,6 +14,13 @@ constexpr int kMostExtent = INT_MAX - 1024;
 // Most workgroups of 256 a launch takes along x: below 2^32 work items.
 constexpr int kMostBlocks = (1 << 24) - 1;
 
+// Workgroups for `work` turns, which those of a grid of fewer take several of.
+inline unsigned launch_blocks(int64_t work, int threads)
+{
+    const int64_t most = ((int64_t)1 << 32) / threads - 1;
+    return (unsigned)(work < most ? work : most);
+}
+
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 inline bool aligned(const void *p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }

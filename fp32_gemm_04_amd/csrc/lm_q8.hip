@@ -119,12 +119,12 @@ extern "C" int sgemm_q8_quantize(int type, int rows, int K, const void *X, int l
     // with eight; 12 rows of 14336 8.0 with four, 5.3 with eight, 8192 fp32 rows of 8192 70.7 and 61.5 (6.8 TB/s,
     // part of it from the last-level cache), of 5000 36.4 and 36.8.
     while (waves < 8 && (int64_t)rows * waves < 4096 && pieces > 64 * waves) waves *= 2;
-    const int64_t blocks = ceil_div(rows, quantize_waves(waves) / waves);
-    const dim3 grid((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks));
+    const int threads = quantize_waves(waves) * 64;
+    const dim3 grid(launch_blocks(ceil_div(rows, quantize_waves(waves) / waves), threads));
     const auto fn = type == SGEMM_TYPE_BF16
                         ? (place ? quantize_of<bf16, true>(waves) : quantize_of<bf16, false>(waves))
                         : (place ? quantize_of<float, true>(waves) : quantize_of<float, false>(waves));
-    fn<<<grid, dim3(quantize_waves(waves) * 64), 0, stream>>>(a);
+    fn<<<grid, dim3(threads), 0, stream>>>(a);
     return (int)hipGetLastError();
 }
 

@@ -153,14 +153,16 @@ extern "C" int sgemm_q8_gemm(int type, int groups, int rows, int N, int K, const
     if (fill != 0 && fill != 1) return -16;
     if (!work) return 0;
     const int used = groups < 1 ? 1 : groups < rows ? groups : rows;  // groups with rows, at most
-    if ((rows + (int64_t)used * 15) / 16 * ceil_div(N, 64) > INT_MAX) return -4;
+    const bool bf16_out = type == SGEMM_TYPE_BF16;
+    const bool fast = K == 0 || (q8_fast(X, ldx, 0) && q8_fast(W, ldw, stride_w));
+    const bool few = K <= kVecRows && byte_few_rows(fast, offsets ? groups : 0, used, rows);
+    const int side = byte_side(fast);
+    if (!few && byte_blocks(offsets ? used : 0, rows, N, side, side) > kMostBlocks) return -4;
 
     int rc = 0;
     const int cus = compute_units(&rc);
     if (cus == 0) return rc;
-    const bool bf16_out = type == SGEMM_TYPE_BF16;
-    const bool fast = K == 0 || (q8_fast(X, ldx, 0) && q8_fast(W, ldw, stride_w));
-    if (K <= kVecRows && byte_few_rows(fast, offsets ? groups : 0, used, rows)) {
+    if (few) {
         VecArgs v = {};
         v.X = X, v.x_scales = x_scales, v.W = W, v.w_scales = w_scales, v.Y = Y, v.offsets = offsets;
         v.ldx = ldx, v.ldw = ldw, v.stride_w = stride_w, v.ldy = ldy;
@@ -177,13 +179,9 @@ extern "C" int sgemm_q8_gemm(int type, int groups, int rows, int N, int K, const
     a.M = rows, a.N = N, a.K = K;
     a.a_cols = a.b_cols = K;
     a.scale_a = x_scales, a.scale_b = w_scales;
-    int64_t most = ceil_div(rows, k.bm);
-    if (offsets) {  // every group's last tile may be part full
-        most = (rows + (int64_t)used * (k.bm - 1)) / k.bm;
-        a.groups = groups, a.offsets = offsets, a.most_tiles = (int)most, a.fill = fill;
-    }
-    const int64_t blocks = most > 0 ? most * ceil_div(N, k.bn) : 1;
-    if (blocks > kMostBlocks) return (int)hipErrorInvalidConfiguration;
+    const int64_t blocks = byte_blocks(offsets ? used : 0, rows, N, k.bm, k.bn);
+    if (offsets)
+        a.groups = groups, a.offsets = offsets, a.most_tiles = (int)(blocks / ceil_div(N, k.bn)), a.fill = fill;
     k.fn<<<dim3((unsigned)blocks), dim3(k.threads), 0, stream>>>(a);
     return (int)hipGetLastError();
 }

@@ -109,14 +109,23 @@ constexpr ByteTileCost kI8Splits[2][kSplits] = {
     {{16, 32, 0.0321, 0.71, 1152}, {32, 32, 0.0295, 0.82, 1152}, {32, 64, 0.0264, 0.71, 832},
      {64, 64, 0.026, 0.71, 1408}}};
 
-// A tile, or NUM_TILES and which of the split ones.
-template <typename RowTiles>
-int byte_tile(bool fast, RowTiles row_tiles, int64_t N, int64_t K, int cus)
+// Workgroups of a product with bm x bn tiles: of rows of one group (used 0), or of `used` groups, whose
+// last tiles may be part full.
+inline int64_t byte_blocks(int64_t used, int64_t rows, int64_t N, int bm, int bn)
+{
+    return (rows + (used ? used : 1) * (bm - 1)) / bm * ceil_div(N, bn);
+}
+// Sides of the largest tile.
+constexpr int byte_side(bool fast) { return fast ? 256 : 128; }
+
+// A tile, or NUM_TILES and which of the split ones, whose workgroups one launch takes (fits); -1: there is none.
+template <typename RowTiles, typename Fits>
+int byte_tile(bool fast, RowTiles row_tiles, Fits fits, int64_t N, int64_t K, int cus)
 {
     int best = -1;
     double least = 0;
-    const auto offer = [&](int i, double cost) {
-        if (best < 0 || cost < least) best = i, least = cost;
+    const auto offer = [&](int i, const ByteTileCost &t, double cost) {
+        if ((best < 0 || cost < least) && fits(t.bm, t.bn)) best = i, least = cost;
     };
     for (int i = 0; i < NUM_TILES; ++i) {
         const ByteTileCost &t = kI8Tiles[fast][i];
@@ -125,13 +134,13 @@ int byte_tile(bool fast, RowTiles row_tiles, int64_t N, int64_t K, int cus)
         const int64_t left = tiles % (2 * cus);
         double rounds = (double)(tiles / (2 * cus)) * 2 + (left == 0 ? 0 : left <= cus ? t.alone : 2);
         if (i == T256) rounds = tiles <= cus ? t.alone : (double)ceil_div(tiles, cus);
-        offer(i, rounds * t.bm * t.bn * (0.5 * K + t.lead) / t.rate);
+        offer(i, t, rounds * t.bm * t.bn * (0.5 * K + t.lead) / t.rate);
     }
     for (int i = 0; i < kSplits; ++i) {
         const ByteTileCost &t = kI8Splits[fast][i];
         if (t.bm == 0) continue;
         const double share = (double)(row_tiles(t.bm) * ceil_div(N, t.bn)) / cus;
-        offer(NUM_TILES + i, (share > t.alone ? share : t.alone) * (t.bm + t.bn) * (K + t.lead) / t.rate);
+        offer(NUM_TILES + i, t, (share > t.alone ? share : t.alone) * (t.bm + t.bn) * (K + t.lead) / t.rate);
     }
     return best;
 }
@@ -144,7 +153,8 @@ inline int byte_rows_tile(bool fast, int64_t used, int64_t rows, int64_t N, int6
         const int64_t t = rows / bm + used / 2;
         return t > used ? t : used;
     };
-    return byte_tile(fast, row_tiles, N, K, cus);
+    const auto fits = [&](int bm, int bn) { return byte_blocks(used, rows, N, bm, bn) <= kMostBlocks; };
+    return byte_tile(fast, row_tiles, fits, N, K, cus);
 }
 
 // Whether rows of one group (groups 0), or of `used` of the groups, are few enough for a workgroup to hold

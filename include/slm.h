@@ -342,7 +342,8 @@ int sgemm_q8_quantize(int type, int rows, int K, const void *X, int ldx, int k, 
  *             were; 1: they are set to zero
  * X and W at 4-byte addresses with leading dimensions (and stride_w) of multiples of 4 are
  * loaded straight to LDS; others go through registers, 1.1 to 2.5 times as slowly.
- * Returns -1 type, -2 groups, -3 rows, -4 N (or more than 2^31 - 1 tiles), -5 K, -6 X, -7
+ * Returns -1 type, -2 groups, -3 rows, -4 N (or rows and N of more than 2^24 - 1 tiles of 256 x 256,
+ * of 128 x 128 where they go through registers; each group may add one to its rows' tiles), -5 K, -6 X, -7
  * ldx, -8 x_scales, -9 W, -10 ldw, -11 stride_w, -12 w_scales, -13 Y, -14 ldy, -15 offsets
  * not 4-byte aligned, -16 fill.
  */

@@ -14,7 +14,8 @@ constexpr int kMostExtent = INT_MAX - 1024;
 // Most workgroups of 256 a launch takes along x: below 2^32 work items.
 constexpr int kMostBlocks = (1 << 24) - 1;
 
-// Workgroups for `work` turns, which those of a grid of fewer take several of.
+// Workgroups of `threads` along x for `work` turns, below 2^32 work items: where there are fewer than
+// turns, the kernel's workgroups take several.
 inline unsigned launch_blocks(int64_t work, int threads)
 {
     const int64_t most = ((int64_t)1 << 32) / threads - 1;

@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kVecWaves * 64) q8_vec_kernel(VecArgs a)
 // reads each byte of LDS once; the sums, exact in any order, meet in LDS.  Rings are short, so that a unit
 // has two or three workgroups.  us in a graph, K = N = 4096, with this and with the best of the tile
 // kernels: 16 rows 5.6 and 13.0, 64 rows 7.0 and 13.4, 128 rows 9.4 and 13.7, 256 rows 12.0 and 13.9, 512 rows
-// 17.2 and 17.5; 64 rows with K 14336 13.8 and 35.0.  64 rows in tiles of 32 x 32 with eight waves took 7.5
+// 17.2 and 17.5 (17.1-19.0 over several runs); 64 rows with K 14336 13.8 and 35.0.  64 rows in tiles of 32 x 32 with eight waves took 7.5
 // where this took 6.6, with rings of three slabs 6.9, in tiles of 64 x 16 7.5, of 64 x 32 8.6.  A tile of
 // 128 x 128 for each wave, which reads the least LDS of all, was slower or (1024 rows) within 3% of the
 // tile kernels: its waves read their slabs and multiply in step.

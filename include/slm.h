@@ -249,7 +249,7 @@ int64_t sgemm_expert_sort_workspace(int slots, int groups);
  *             slots (place -2 - r) are set to zero, so that with rows = tokens * k all
  *             of R is written
  * The gradient by X is sgemm_expert_combine of the gradient by R; that by the weights is
- * sgemm_expert_combine_backward's with X as dout and the gradient by R as Y.
+ * sgemm_expert_combine_backward's with X as dout and the gradient by R as R.
  * Returns -1 type, -2 tokens, -3 k (or tokens * k too large), -4 H, -5 X, -6 ldx, -7
  * place, -8 weights, -9 rows, -10 R, -11 ldr, -12 fill.
  */
